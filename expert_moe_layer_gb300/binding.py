@@ -25,6 +25,7 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
                 3: "MOE_ERR_WORKSPACE", 4: "MOE_ERR_CUDA", 5: "MOE_ERR_DEVICE_STATUS",
                 6: "MOE_ERR_TIMEOUT"}
 DEV_BAD_EXPERT_ID, DEV_CAP_OVERFLOW, DEV_TIMEOUT, DEV_BAD_SEGMENT = 0x1, 0x2, 0x4, 0x8
+DEV_BAD_POSITION, DEV_BAD_SLOT, DEV_BAD_PAGE = 0x10, 0x20, 0x40
 
 
 class MoeError(RuntimeError):
@@ -47,6 +48,21 @@ class MoeConfig(ctypes.Structure):
                 ("act_dtype", ctypes.c_int), ("router_dtype", ctypes.c_int),
                 ("scoring_func", ctypes.c_int), ("bias_mode", ctypes.c_int),
                 ("max_replicas", ctypes.c_int), ("num_redundant_experts", ctypes.c_int)]
+
+
+class AttnConfig(ctypes.Structure):
+    _fields_ = [("num_heads", ctypes.c_int), ("num_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("act_dtype", ctypes.c_int), ("rotary_dim", ctypes.c_int),
+                ("rope_layout", ctypes.c_int), ("rope_positions", ctypes.c_int),
+                ("window", ctypes.c_int), ("softmax_scale", ctypes.c_float),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_double), ("kind", ctypes.c_int), ("factor", ctypes.c_double),
+                ("original_positions", ctypes.c_double), ("slow_turns", ctypes.c_double),
+                ("fast_turns", ctypes.c_double), ("attention_factor", ctypes.c_double)]
 
 
 class WorkspaceOffsets(ctypes.Structure):
@@ -91,11 +107,30 @@ def make_config(num_experts, top_k, hidden_size, intermediate_size, renormalize=
                      num_redundant_experts)
 
 
+def make_attn_config(num_heads, num_kv_heads, head_dim, page_size=16, act_dtype="bf16",
+                     rotary_dim=0, rope_layout="half", rope_positions=0, window=0,
+                     softmax_scale=0.0, k_scale=1.0, v_scale=1.0) -> AttnConfig:
+    dt = {"bf16": MOE_BF16, "f32": MOE_F32}
+    lay = {"half": 0, "interleaved": 1}
+    return AttnConfig(num_heads, num_kv_heads, head_dim, page_size, dt[act_dtype], rotary_dim,
+                      lay[rope_layout], rope_positions, window, softmax_scale, k_scale, v_scale)
+
+
+def make_rope_scaling(base=10000.0, kind="none", factor=1.0, original_positions=0, slow_turns=0.0,
+                      fast_turns=0.0, attention_factor=0.0) -> RopeScaling:
+    kinds = {"none": 0, "linear": 1, "ntk": 2, "parts": 3, "yarn": 4}
+    return RopeScaling(base, kinds[kind], factor, original_positions, slow_turns, fast_turns,
+                       attention_factor)
+
+
 _libs: dict[bool, ctypes.CDLL] = {}  # debug build? -> loaded library
 _use_debug = False
 _lock = threading.Lock()
 _VP, _SZ, _I = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+_I64 = ctypes.c_int64
 _CFG = ctypes.POINTER(MoeConfig)
+_ACFG = ctypes.POINTER(AttnConfig)
+_ROWS = [_VP, _I64, _I64]  # a strided [T, heads, D] tensor: pointer, token and head strides
 
 _SIGS = {
     "moe_strerror": (ctypes.c_char_p, [_I]),
@@ -124,6 +159,15 @@ _SIGS = {
     "moe_ep_expert_compute_workspace_size": (_SZ, [_CFG, _I]),
     "moe_ep_expert_compute": (_I, [_CFG, _I] + [_VP] * 7 + [_SZ, _VP]),
     "moe_ep_combine": (_I, [_CFG, _I] + [_VP] * 5 + [_SZ, _VP]),
+    "moe_validate_attn_config": (_I, [_ACFG]),
+    "moe_kv_page_bytes": (_SZ, [_ACFG]),
+    "moe_rope_table": (_I, [_ACFG, _I, _VP, ctypes.POINTER(RopeScaling), _VP, _VP, _SZ, _VP]),
+    "moe_rope": (_I, [_ACFG, _I, _I] + _ROWS + [_VP, _VP, _I, _VP, _VP, _SZ, _VP]),
+    "moe_kv_append": (_I, [_ACFG, _I] + 3 * _ROWS + [_VP] * 5 + [_I64, _VP, _SZ, _VP]),
+    "moe_kv_read": (_I, [_ACFG, _I, _VP, _VP, _I64, _VP, _VP, _VP, _SZ, _VP]),
+    "moe_kv_attention_workspace_size": (_SZ, [_ACFG, _I, _I, _I]),
+    "moe_kv_attention": (_I, [_ACFG, _I, _I, _I] + _ROWS + [_VP] * 3 + [_I, _VP, _I64] +
+                         [_VP, _VP, _VP, _SZ, _VP]),
     "moe_debug_build": (_I, []),
     "moe_debug_take": (_I, [ctypes.POINTER(DebugRecord)]),
     "moe_debug_selftest": (_I, [_VP]),
@@ -326,6 +370,107 @@ def moe_forward_timed(cfg, T, x, router_w, router_bias, w13, w2, shared_w13, sha
         _p(shared_w13), _p(shared_w2), _p(expert_map), _p(out), _p(ws), _nbytes(ws),
         _stream(stream), handles, ctypes.byref(n)))
     return n.value
+
+
+# ------------------------------------------------------------------ attention
+def _typed(name, t, dtype, shape):
+    """Device pointer of a contiguous tensor of that type and shape (None
+    passes through; a None in the shape is not checked)."""
+    if t is None:
+        return None
+    if str(t.dtype) != dtype:
+        raise ValueError(f"{name} must be {dtype}; got {t.dtype}")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {shape}; got {tuple(t.shape)}")
+    return _p(t)
+
+
+def _act(cfg):
+    return "torch.bfloat16" if cfg.act_dtype == MOE_BF16 else "torch.float32"
+
+
+def _rows(name, t, cfg, T, heads):
+    """(pointer, token stride, head stride) of a [T, heads, head_dim] tensor
+    whose channels are contiguous; tokens and heads may be strided."""
+    if t is None:
+        return None, 0, 0
+    if str(t.dtype) != _act(cfg):
+        raise ValueError(f"{name} must be {_act(cfg)}; got {t.dtype}")
+    if tuple(t.shape) != (T, heads, cfg.head_dim):
+        raise ValueError(f"{name} must have shape {(T, heads, cfg.head_dim)}; "
+                         f"got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError("libmoe takes device tensors; got one on " + str(t.device))
+    st, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"the channels of {name} must be contiguous")
+    return t.data_ptr(), st, sh
+
+
+def _cache(cache, cfg):
+    """(pointer, pages) of a cache tensor [pages, kv heads, block bytes]."""
+    block = cfg.page_size * cfg.head_dim * 9 // 8
+    return _typed("cache", cache, "torch.uint8", (None, cfg.num_kv_heads, block)), cache.shape[0]
+
+
+def validate_attn_config(cfg: AttnConfig) -> int:
+    return lib().moe_validate_attn_config(ctypes.byref(cfg))
+
+
+def kv_page_bytes(cfg: AttnConfig) -> int:
+    return lib().moe_kv_page_bytes(ctypes.byref(cfg))
+
+
+def kv_attention_workspace_size(cfg, num_seqs, T, max_q_len) -> int:
+    return lib().moe_kv_attention_workspace_size(ctypes.byref(cfg), num_seqs, T, max_q_len)
+
+
+def moe_rope_table(cfg, n, positions, scaling, table, ws=None, stream=None):
+    _check("moe_rope_table", lib().moe_rope_table(
+        ctypes.byref(cfg), n, _typed("positions", positions, "torch.int32", (n,)),
+        ctypes.byref(scaling), _typed("table", table, "torch.float32", (n, cfg.rotary_dim)),
+        _p(ws), _nbytes(ws), _stream(stream)))
+
+
+def moe_rope(cfg, T, x, positions, table, out, inverse=False, ws=None, stream=None):
+    heads = x.shape[1] if x.dim() == 3 else 0
+    _check("moe_rope", lib().moe_rope(
+        ctypes.byref(cfg), T, heads, *_rows("x", x, cfg, T, heads),
+        _typed("positions", positions, "torch.int32", (T,)),
+        _typed("table", table, "torch.float32", (cfg.rope_positions, cfg.rotary_dim)),
+        int(bool(inverse)), _typed("out", out, _act(cfg), (T, heads, cfg.head_dim)), _p(ws),
+        _nbytes(ws), _stream(stream)))
+
+
+def moe_kv_append(cfg, T, q, k, v, positions, slots, table, q_out, cache, ws=None, stream=None):
+    _check("moe_kv_append", lib().moe_kv_append(
+        ctypes.byref(cfg), T, *_rows("q", q, cfg, T, cfg.num_heads),
+        *_rows("k", k, cfg, T, cfg.num_kv_heads), *_rows("v", v, cfg, T, cfg.num_kv_heads),
+        _typed("positions", positions, "torch.int32", (T,)),
+        _typed("slots", slots, "torch.int64", (T,)),
+        _typed("table", table, "torch.float32", (cfg.rope_positions, cfg.rotary_dim)),
+        _typed("q_out", q_out, _act(cfg), (T, cfg.num_heads, cfg.head_dim)),
+        *_cache(cache, cfg), _p(ws), _nbytes(ws), _stream(stream)))
+
+
+def moe_kv_read(cfg, N, slots, cache, k_out, v_out, ws=None, stream=None):
+    shape = (N, cfg.num_kv_heads, cfg.head_dim)
+    _check("moe_kv_read", lib().moe_kv_read(
+        ctypes.byref(cfg), N, _typed("slots", slots, "torch.int64", (N,)), *_cache(cache, cfg),
+        _typed("k_out", k_out, _act(cfg), shape), _typed("v_out", v_out, _act(cfg), shape),
+        _p(ws), _nbytes(ws), _stream(stream)))
+
+
+def moe_kv_attention(cfg, num_seqs, T, max_q_len, q, q_offsets, seq_lens, page_table, cache, out,
+                     lse, ws, stream=None):
+    _check("moe_kv_attention", lib().moe_kv_attention(
+        ctypes.byref(cfg), num_seqs, T, max_q_len, *_rows("q", q, cfg, T, cfg.num_heads),
+        _typed("q_offsets", q_offsets, "torch.int32", (num_seqs + 1,)),
+        _typed("seq_lens", seq_lens, "torch.int32", (num_seqs,)),
+        _typed("page_table", page_table, "torch.int32", (num_seqs, None)), page_table.shape[1],
+        *_cache(cache, cfg), _typed("out", out, _act(cfg), (T, cfg.num_heads, cfg.head_dim)),
+        _typed("lse", lse, "torch.float32", (T, cfg.num_heads)), _p(ws), _nbytes(ws),
+        _stream(stream)))
 
 
 def moe_get_status(ws, stream=None) -> tuple[int, int]:

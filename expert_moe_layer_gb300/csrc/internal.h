@@ -12,6 +12,12 @@
 
 namespace moe {
 
+// Records the failure behind a MOE_ERR_CUDA (moe_last_cuda_error); returns it.
+int fail_cuda(int code);
+
+// SMs of the current context (0: the query failed, recorded).
+int sm_count();
+
 // One GEMM work tile: `count` token rows of one expert's segment.
 //   x = expert (weight slab index), y = first B row, z = first output row,
 //   w = rows (1..nmax).

@@ -1,0 +1,674 @@
+// Attention over the 4-bit paged cache: the split kernel.
+//
+// A work unit is a tile of 16 cached tokens of one (request, row tile, kv
+// head) segment; a row is one (query token, query head of the group) pair and
+// a row tile has 8 or 16 of them. All segments' tiles form one list, which is
+// cut into equal ranges, one per CTA, so that requests of any lengths fill the
+// GPU evenly. A plan kernel sums the segments' sizes; a CTA whose range covers
+// a segment writes its rows, others leave fp32 partial sums and statistics,
+// which the last CTA of the segment joins in CTA order (the result does not
+// depend on who is last).
+//
+// Few rows read many bytes, so the cache's bandwidth bounds this kernel and
+// the arithmetic has to hide behind it. Per tile a warp loads its codes
+// straight into the registers of the matrix instruction: the k index of
+// S^T = K Q^T and the m index of O^T = V^T P^T may be permuted freely as long
+// as both operands agree, so a lane takes D/4 neighbouring channels of two key
+// rows and D/8 neighbouring channels of four value rows, whole words of codes
+// under one or two scales. Codes times scales are exact in f16.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+
+#include "attn.h"
+#include "kv4.cuh"
+#include "launch.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kTile = 16;   // cached tokens per tile
+constexpr int kWarps = 4;   // per CTA; each takes every fourth tile of a segment
+constexpr int kThreads = kWarps * 32;
+constexpr int kMinTiles = 2 * kWarps;  // smallest range of a CTA
+constexpr int kMaxCtasPerSm = 4;
+constexpr int kPlanThreads = 1024;
+
+// P is kept as f16 times 2^kLift, so that small probabilities keep their bits
+// and the running maximum may lag behind by kLag (both in powers of two).
+constexpr float kLift = 6.0f, kLag = 8.0f;
+
+// One request, as the plan kernel leaves it.
+struct SeqInfo {
+  int q0, q_len, len, first_tile;  // first query row, its tokens, cached tokens, first tile read
+};
+
+__device__ __forceinline__ long shfl_up(long v, int d) { return __shfl_up_sync(~0u, v, d); }
+
+// Clears the status and the join counters, checks every request and sums the
+// tiles of all segments: starts[b] is the first tile of request b in the list.
+__global__ void __launch_bounds__(kPlanThreads)
+    attn_plan_kernel(AttnArgs a, int row_tile, unsigned* status, int* counters, int n_counters,
+                     SeqInfo* info, long* starts) {
+  pdl_enter();
+  if (threadIdx.x == 0) *status = 0;
+  for (int i = threadIdx.x; i < n_counters; i += kPlanThreads) counters[i] = 0;
+  __syncthreads();
+  __shared__ long warp_sum[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = a.heads / a.kv_heads;
+  const long cap = static_cast<long>(a.max_pages) * a.page_size;
+  long base = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+    const int b = b0 + threadIdx.x;
+    long tiles = 0;
+    if (b < a.B) {
+      SeqInfo s = {0, 0, 0, 0};
+      const int q0 = a.q_offsets ? a.q_offsets[b] : b;
+      const int q1 = a.q_offsets ? a.q_offsets[b + 1] : b + 1;
+      if (q0 < 0 || q1 < q0 || q1 > a.T || q1 - q0 > a.max_q) {
+        atomicOr(status, MOE_DEV_BAD_SEGMENT);
+      } else {
+        s.q0 = q0;
+        s.q_len = q1 - q0;
+      }
+      const int n = a.seq_lens[b];
+      s.len = static_cast<int>(n < 0 ? 0 : n > cap ? cap : n);
+      if (s.len != n) atomicOr(status, MOE_DEV_BAD_PAGE);
+      if (a.window > 0) {
+        const long lo = static_cast<long>(s.len) - s.q_len - a.window + 1;
+        s.first_tile = lo > 0 ? static_cast<int>(lo / kTile) : 0;
+      }
+      const long row_tiles = (static_cast<long>(s.q_len) * g + row_tile - 1) / row_tile;
+      // a request without cached tokens keeps one empty tile per segment: its
+      // rows still have to be written
+      long per = (s.len + kTile - 1) / kTile - s.first_tile;
+      per = per < 1 ? 1 : per;
+      tiles = row_tiles * a.kv_heads * per;
+      info[b] = s;
+    }
+    long sum = tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const long v = shfl_up(sum, d);
+      if (lane >= d) sum += v;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    long before = 0, all = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      if (w < warp) before += warp_sum[w];
+      all += warp_sum[w];
+    }
+    if (b < a.B) starts[b] = base + before + sum - tiles;
+    base += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) starts[a.B] = base;
+}
+
+// Range of the tile list that CTA c of n takes: [first(c), first(c + 1)).
+__device__ __forceinline__ long range_len(long total, int ctas) {
+  const long per = (total + ctas - 1) / ctas;
+  return per < kMinTiles ? kMinTiles : per;
+}
+
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8x8 matrix of f16 held by the warp (two neighbours per lane).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+template <int N>
+struct Words {
+  uint32_t w[N];
+};
+template <int N>
+__device__ __forceinline__ Words<N> load_words(const uint8_t* p) {
+  Words<N> r;
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
+    }
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    r.w[0] = v.x, r.w[1] = v.y;
+  } else {
+    r.w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+  return r;
+}
+
+// N scale bytes of neighbouring groups.
+template <int N>
+__device__ __forceinline__ uint32_t load_scales(const uint8_t* p) {
+  if constexpr (N == 4) return *reinterpret_cast<const uint32_t*>(p);
+  if constexpr (N == 2) return *reinterpret_cast<const uint16_t*>(p);
+  return *p;
+}
+
+template <int D>
+struct TileRegs {
+  Words<D / 32> k[2];  // key rows g, g + 8 of the tile: D/4 channels
+  Words<D / 64> v[4];  // value rows 2c, 2c+1, 2c+8, 2c+9: D/8 channels
+  uint32_t ks[2], vs[4];
+};
+
+// The codes and scales of a tile, for lane (g, c) = (lane / 4, lane % 4).
+template <int D>
+__device__ __forceinline__ void load_tile(TileRegs<D>& t, const uint8_t* block, int page_size,
+                                          int row0, int g, int c) {
+  constexpr int kRow = D / 2, kScales = D / kKvGroup;
+  constexpr int kVs = D >= 128 ? D / 128 : 1;  // scales a lane's value channels fall under
+  const KvBlock blk = kv_block(page_size, D);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = row0 + g + 8 * i;
+    t.k[i] = load_words<D / 32>(block + r * kRow + c * (D / 8));
+    t.ks[i] = load_scales<D / 64>(block + blk.k_scale + r * kScales + c * (D / 64));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = row0 + 2 * c + (i & 1) + 8 * (i >> 1);
+    t.v[i] = load_words<D / 64>(block + blk.v_code + r * kRow + g * (D / 16));
+    t.vs[i] = load_scales<kVs>(block + blk.v_scale + r * kScales + g * D / 8 / kKvGroup);
+  }
+}
+
+// kTerms = 1: q and P are one f16 each (q bf16: exact). kTerms = 2 (fp32
+// layers): q and P are a sum of two f16 each, 22 bits, and each tile's product
+// with V is added to the running sum by fp32 additions, because the matrix
+// unit's own accumulation truncates.
+template <typename T, int D, int NT, int kTerms>
+__global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 4)
+    attn_split_kernel(AttnArgs a, unsigned* status, int* counters, const SeqInfo* info,
+                      const long* starts, float* stats, float* partial, int tiles_per_page_log2) {
+  constexpr int kRows = 8 * NT;
+  constexpr int kVs = D >= 128 ? D / 128 : 1;
+  extern __shared__ float smem[];  // [kWarps][kRows][D] sums, then [kWarps][kRows][2] statistics
+  float* s_stat = smem + kWarps * kRows * D;
+  __shared__ int s_last;
+  pdl_enter();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, c = lane & 3;
+  const int group = a.heads / a.kv_heads;
+  const KvBlock blk = kv_block(a.page_size, D);
+  const long total = starts[a.B];
+  const long per = range_len(total, gridDim.x);
+  long at = blockIdx.x * per;
+  const long end = min(total, at + per);
+  if (at >= end) return;
+  // the request of the first tile: the last b with starts[b] <= at (requests
+  // without query rows have no tiles and share their start with the next)
+  int b = 0;
+  {
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (starts[mid] <= at) lo = mid;
+      else hi = mid;
+    }
+    b = lo;
+  }
+  while (at < end) {
+    while (starts[b + 1] <= at) ++b;
+    const SeqInfo sq = info[b];
+    const int rows = sq.q_len * group;
+    const int per_seg = max(1, (sq.len + kTile - 1) / kTile - sq.first_tile);
+    const long seg = (at - starts[b]) / per_seg;
+    const int t0 = static_cast<int>((at - starts[b]) - seg * per_seg);
+    const int t1 = static_cast<int>(min(static_cast<long>(per_seg), t0 + (end - at)));
+    const int row_tile = static_cast<int>(seg / a.kv_heads);
+    const int kvh = static_cast<int>(seg - static_cast<long>(row_tile) * a.kv_heads);
+    const int row0 = row_tile * kRows;
+    const long seg_start = at - t0, seg_end = seg_start + per_seg;
+
+    // this lane's score columns are rows nt*8 + 2c and + 1: their token limits
+    int last[NT][2], first[NT][2];
+    int tile_first, tile_last, all_first, all_last;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = row0 + nt * 8 + 2 * c + j;
+        // padding rows (zero queries whose columns are never written) see all
+        const int p = sq.len - sq.q_len + r / group;
+        last[nt][j] = r < rows ? p : 0x7fffffff;
+        first[nt][j] = r < rows && a.window > 0 ? max(0, p - a.window + 1) : 0;
+      }
+    {
+      const int r_end = min(rows, row0 + kRows) - 1;
+      const int p0 = sq.len - sq.q_len + row0 / group, p1 = sq.len - sq.q_len + r_end / group;
+      tile_last = p1;
+      tile_first = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
+      // tokens that every row of the tile sees
+      all_last = p0;
+      all_first = a.window > 0 ? max(0, p1 - a.window + 1) : 0;
+    }
+
+    // q^T as the B operand: column g (+ 8 nt), channels c*D/4 ..
+    uint32_t qf[kTerms][NT][D / 8];
+    float q_gain[NT];  // 2^-x of the row g (+ 8 nt) this lane loads
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = row0 + nt * 8 + g;
+      float x[D / 4];
+      if (r < rows) {
+        const int tok = r / group, h = kvh * group + (r - tok * group);
+        const T* src = static_cast<const T*>(a.q.p) + (sq.q0 + tok) * a.q.token + h * a.q.head +
+                       c * (D / 4);
+        if constexpr (sizeof(T) == 2) {
+          const Words<D / 8> w = load_words<D / 8>(reinterpret_cast<const uint8_t*>(src));
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            x[2 * i] = __uint_as_float(w.w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w.w[i] & 0xffff0000u);
+          }
+        } else {
+          const Words<D / 4> w = load_words<D / 4>(reinterpret_cast<const uint8_t*>(src));
+#pragma unroll
+          for (int i = 0; i < D / 4; ++i) x[i] = __uint_as_float(w.w[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) x[i] = 0.0f;
+      }
+      // scale the row by a power of two so that its largest element lies in
+      // [128, 256): every bit of a bf16 element then survives in f16 unless it
+      // is 2^-22 of the largest
+      float top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+      int e = static_cast<int>((__float_as_uint(top) >> 23) & 0xffu) - 127;
+      e = max(-90, min(127, e));
+      const float up = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
+      q_gain[nt] = __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const float lo = x[2 * i] * up, hi = x[2 * i + 1] * up;
+        qf[0][nt][i] = pack_f16(lo, hi);
+        if constexpr (kTerms == 2) {
+          const float2 f = unpack_f16(qf[0][nt][i]);
+          qf[1][nt][i] = pack_f16(lo - f.x, hi - f.y);
+        }
+      }
+    }
+    // the gains of this lane's score columns, with the softmax scale
+    float gain[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        gain[nt][j] = __shfl_sync(~0u, q_gain[nt], (2 * c + j) * 4) * a.scale_log2;
+
+    float o[D / 16][NT][4];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
+    float m[NT][2], base[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) m[nt][j] = -INFINITY, base[nt][j] = -kLift, l[nt][j] = 0.0f;
+
+    // tiles of this row tile that hold a visible token
+    const int tA = max(t0, tile_first / kTile - sq.first_tile);
+    const int tB = min(t1, tile_last < 0 ? 0 : tile_last / kTile + 1 - sq.first_tile);
+    const int32_t* pages = a.page_table + static_cast<long>(b) * a.max_pages;
+    TileRegs<D> next;
+    bool next_ok = false;
+    auto fetch = [&](int t) {
+      const int tile = t + sq.first_tile;
+      const int id = pages[tile >> tiles_per_page_log2];
+      next_ok = id >= 0 && id < a.num_pages;
+      if (!next_ok && lane == 0) atomicOr(status, MOE_DEV_BAD_PAGE);
+      const uint8_t* block =
+          a.cache + (static_cast<long>(next_ok ? id : 0) * a.kv_heads + kvh) * blk.bytes;
+      load_tile<D>(next, block, a.page_size,
+                   (tile & ((1 << tiles_per_page_log2) - 1)) * kTile, g, c);
+    };
+    // the kernel's warps take the tiles of the range in turn
+    int t = tA + warp;
+    if (t < tB) fetch(t);
+    for (; t < tB; t += kWarps) {
+      TileRegs<D> cur = next;
+      const bool ok = next_ok;
+      if (t + kWarps < tB) fetch(t + kWarps);
+      const int tok0 = (t + sq.first_tile) * kTile;
+      const bool whole = ok && tok0 >= all_first && tok0 + kTile - 1 <= all_last;
+
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[nt][j] = 0.0f;
+      uint32_t ks2[2][(D + 127) / 128];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < (D + 127) / 128; ++j) ks2[i][j] = e4m3x2_to_f16(cur.ks[i] >> (16 * j));
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) {  // 8 channels of each row: two k steps
+        uint32_t k0[4], k1[4];
+        e2m1_to_f16(cur.k[0].w[w], k0);
+        e2m1_to_f16(cur.k[1].w[w], k1);
+        const int sc = w / 2;  // the scale these channels fall under
+        const uint32_t s0 = sc & 1 ? f16_high_twice(ks2[0][sc / 2]) : f16_low_twice(ks2[0][sc / 2]);
+        const uint32_t s1 = sc & 1 ? f16_high_twice(ks2[1][sc / 2]) : f16_low_twice(ks2[1][sc / 2]);
+#pragma unroll
+        for (int hstep = 0; hstep < 2; ++hstep) {
+          const uint32_t af[4] = {hmul2(k0[2 * hstep], s0), hmul2(k1[2 * hstep], s1),
+                                  hmul2(k0[2 * hstep + 1], s0), hmul2(k1[2 * hstep + 1], s1)};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int term = 0; term < kTerms; ++term)
+              mma(s[nt], af, qf[term][nt][4 * w + 2 * hstep], qf[term][nt][4 * w + 2 * hstep + 1]);
+        }
+      }
+      // scores in powers of two; [j] column 2c + (j & 1), token g + 8 (j >> 1)
+      bool grow = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float x = s[nt][j] * gain[nt][j & 1];
+          if (!whole) {
+            const int tok = tok0 + g + 8 * (j >> 1);
+            if (!ok || tok < first[nt][j & 1] || tok > last[nt][j & 1]) x = -INFINITY;
+          }
+          s[nt][j] = x;
+          grow |= x > m[nt][j & 1] + kLag;
+        }
+      if (__any_sync(~0u, grow)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float f[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float x = fmaxf(fmaxf(s[nt][j], s[nt][j + 2]), m[nt][j]);
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+            const float nb = x == -INFINITY ? -kLift : x - kLift;
+            f[j] = m[nt][j] == -INFINITY ? 0.0f : exp2f(base[nt][j] - nb);
+            l[nt][j] *= f[j];
+            m[nt][j] = x;
+            base[nt][j] = nb;
+          }
+          // sums' columns are the scores' columns
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][nt][j] *= f[j & 1];
+        }
+      }
+      uint32_t pf[kTerms][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float p[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          p[j] = exp2f(s[nt][j] - base[nt][j & 1]);
+          l[nt][j & 1] += p[j];
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t w = pack_f16(p[2 * half], p[2 * half + 1]);
+          pf[0][nt][half] = transpose8x8(w);
+          if constexpr (kTerms == 2) {
+            const float2 f = unpack_f16(w);
+            pf[1][nt][half] = transpose8x8(pack_f16(p[2 * half] - f.x, p[2 * half + 1] - f.y));
+          }
+        }
+      }
+      // V^T as the A operand. A token that no row sees may be uninitialised
+      // memory: its scale is zeroed, so that 0 * NaN cannot enter the sum.
+      uint32_t vs[2][kVs];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (!whole) {
+          const int tok = tok0 + 2 * c + 8 * i;
+          if (!ok || tok < tile_first || tok > tile_last) cur.vs[2 * i] = 0;
+          if (!ok || tok + 1 < tile_first || tok + 1 > tile_last) cur.vs[2 * i + 1] = 0;
+        }
+#pragma unroll
+        for (int j = 0; j < kVs; ++j)
+          vs[i][j] = e4m3x2_to_f16(((cur.vs[2 * i] >> (8 * j)) & 0xffu) |
+                                   (((cur.vs[2 * i + 1] >> (8 * j)) & 0xffu) << 8));
+      }
+#pragma unroll
+      for (int w = 0; w < D / 64; ++w) {  // 8 channels: four m tiles
+        uint32_t h[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e2m1_to_f16(cur.v[i].w[w], h[i]);
+        const int sc = D == 256 ? w / 2 : 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t af[4] = {hmul2(__byte_perm(h[0][q], h[1][q], 0x5410), vs[0][sc]),
+                                  hmul2(__byte_perm(h[0][q], h[1][q], 0x7632), vs[0][sc]),
+                                  hmul2(__byte_perm(h[2][q], h[3][q], 0x5410), vs[1][sc]),
+                                  hmul2(__byte_perm(h[2][q], h[3][q], 0x7632), vs[1][sc])};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float(&acc)[4] = o[4 * w + q][nt];
+            if constexpr (kTerms == 1) {
+              mma(acc, af, pf[0][nt][0], pf[0][nt][1]);
+            } else {
+              float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              mma(d, af, pf[1][nt][0], pf[1][nt][1]);
+              mma(d, af, pf[0][nt][0], pf[0][nt][1]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) acc[j] += d[j];
+            }
+          }
+        }
+      }
+    }
+
+    // join the warps: sums [row][channel] and statistics (base, l) in shared memory
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float x = l[nt][j];
+        x += __shfl_xor_sync(~0u, x, 4);
+        x += __shfl_xor_sync(~0u, x, 8);
+        x += __shfl_xor_sync(~0u, x, 16);
+        const int r = nt * 8 + 2 * c + j;
+        if (g == 0) {
+          s_stat[(warp * kRows + r) * 2] = m[nt][j] == -INFINITY ? -INFINITY : base[nt][j];
+          s_stat[(warp * kRows + r) * 2 + 1] = x;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          float* dst = smem + (warp * kRows + r) * D + g * (D / 8) + 2 * i;
+          *reinterpret_cast<float2*>(dst) = make_float2(o[i][nt][j], o[i][nt][j + 2]);
+        }
+      }
+    __syncthreads();
+    const bool alone = t0 == 0 && t1 == per_seg;
+    // pieces of a segment: the CTA it begins in keeps its piece in slot 1 (its
+    // range ends inside the segment), later ones in slot 0
+    const long my_slot = 2l * blockIdx.x + (t0 == 0 ? 1 : 0);
+    for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), ch = (i % (D / 4)) * 4;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_stat[(w * kRows + r) * 2]);
+      float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float den = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float b2 = s_stat[(w * kRows + r) * 2];
+        const float f = b2 == -INFINITY ? 0.0f : exp2f(b2 - top);
+        const float4 v = *reinterpret_cast<const float4*>(smem + (w * kRows + r) * D + ch);
+        den += f * s_stat[(w * kRows + r) * 2 + 1];
+        sum.x += f * v.x, sum.y += f * v.y, sum.z += f * v.z, sum.w += f * v.w;
+      }
+      if (alone) {
+        if (row0 + r < rows) {
+          const int tok = (row0 + r) / group, h = kvh * group + (row0 + r) - tok * group;
+          const long at_row = static_cast<long>(sq.q0 + tok) * a.heads + h;
+          const float inv = den > 0.0f || den != den ? a.v_scale / den : 0.0f;
+          T* dst = static_cast<T*>(a.out) + at_row * D + ch;
+          if constexpr (sizeof(T) == 2) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x * inv, sum.y * inv);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(sum.z * inv, sum.w * inv);
+            *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                        *reinterpret_cast<const uint32_t*>(&hi));
+          } else {
+            *reinterpret_cast<float4*>(dst) =
+                make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+          }
+          if (a.lse && ch == 0)
+            a.lse[at_row] = den > 0.0f || den != den ? (top + log2f(den)) * 0.69314718f : -INFINITY;
+        }
+      } else {
+        *reinterpret_cast<float4*>(partial + (my_slot * kRows + r) * D + ch) = sum;
+        if (ch == 0) {
+          stats[(my_slot * kRows + r) * 2] = top;
+          stats[(my_slot * kRows + r) * 2 + 1] = den;
+        }
+      }
+    }
+    if (!alone) {
+      const int cta0 = static_cast<int>(seg_start / per);
+      const int cta1 = static_cast<int>((seg_end - 1) / per);
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0)
+        s_last = ptx::add_acq_rel(counters + cta0, 1) == cta1 - cta0;
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
+          const int r = i / (D / 4), ch = (i % (D / 4)) * 4;
+          if (row0 + r >= rows) continue;
+          float top = -INFINITY;
+          for (int k = cta0; k <= cta1; ++k)
+            top = fmaxf(top, __ldcg(stats + ((2l * k + (k == cta0)) * kRows + r) * 2));
+          float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          float den = 0.0f;
+          for (int k = cta0; k <= cta1; ++k) {
+            const long slot = (2l * k + (k == cta0)) * kRows + r;
+            const float2 st = __ldcg(reinterpret_cast<const float2*>(stats + slot * 2));
+            const float f = st.x == -INFINITY ? 0.0f : exp2f(st.x - top);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(partial + slot * D + ch));
+            den += f * st.y;
+            sum.x += f * v.x, sum.y += f * v.y, sum.z += f * v.z, sum.w += f * v.w;
+          }
+          const int tok = (row0 + r) / group, h = kvh * group + (row0 + r) - tok * group;
+          const long at_row = static_cast<long>(sq.q0 + tok) * a.heads + h;
+          const float inv = den > 0.0f || den != den ? a.v_scale / den : 0.0f;
+          T* dst = static_cast<T*>(a.out) + at_row * D + ch;
+          if constexpr (sizeof(T) == 2) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x * inv, sum.y * inv);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(sum.z * inv, sum.w * inv);
+            *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                        *reinterpret_cast<const uint32_t*>(&hi));
+          } else {
+            *reinterpret_cast<float4*>(dst) =
+                make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+          }
+          if (a.lse && ch == 0)
+            a.lse[at_row] = den > 0.0f || den != den ? (top + log2f(den)) * 0.69314718f : -INFINITY;
+        }
+      }
+    }
+    __syncthreads();
+    at += t1 - t0;
+  }
+}
+
+template <typename T, int D, int NT, int kTerms>
+cudaError_t launch_split(const AttnArgs& a, void* ws, const AttnLayout& L, cudaStream_t st) {
+  auto* status = reinterpret_cast<unsigned*>(static_cast<char*>(ws) + L.status);
+  auto* counters = reinterpret_cast<int*>(static_cast<char*>(ws) + L.counters);
+  auto* info = reinterpret_cast<SeqInfo*>(static_cast<char*>(ws) + L.info);
+  auto* starts = reinterpret_cast<long*>(static_cast<char*>(ws) + L.starts);
+  auto* stats = reinterpret_cast<float*>(static_cast<char*>(ws) + L.stats);
+  auto* partial = reinterpret_cast<float*>(static_cast<char*>(ws) + L.partial);
+  const int grid = a.sms * ((D == 256 || NT * kTerms > 1) ? 2 : 4);
+  cudaError_t e = launch_pdl(&attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a, 8 * NT,
+                             status, counters, grid, info, starts);
+  if (e != cudaSuccess) return e;
+  const int smem = kWarps * 8 * NT * (D + 2) * 4;
+  static std::atomic<unsigned long long> done{0};
+  e = opt_in_smem(reinterpret_cast<const void*>(&attn_split_kernel<T, D, NT, kTerms>), smem, done);
+  if (e != cudaSuccess) return e;
+  int log2 = 0;
+  while ((kTile << log2) < a.page_size) ++log2;
+  return launch_pdl(&attn_split_kernel<T, D, NT, kTerms>, dim3(grid), dim3(kThreads), smem, st, a,
+                    status, counters, const_cast<const SeqInfo*>(info),
+                    const_cast<const long*>(starts), stats, partial, log2);
+}
+
+template <int D>
+cudaError_t launch_dim(bool bf16, const AttnArgs& a, void* ws, const AttnLayout& L,
+                       cudaStream_t st) {
+  if (!bf16) return launch_split<float, D, 1, 2>(a, ws, L, st);
+  if (static_cast<long>(a.max_q) * (a.heads / a.kv_heads) <= 8)
+    return launch_split<__nv_bfloat16, D, 1, 1>(a, ws, L, st);
+  return launch_split<__nv_bfloat16, D, 2, 1>(a, ws, L, st);
+}
+
+}  // namespace
+
+AttnLayout attn_layout(const moe_attn_config* c, int B, int sms) {
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  const size_t ctas = static_cast<size_t>(sms) * kMaxCtasPerSm;
+  AttnLayout L;
+  L.status = 0;
+  L.counters = 256;
+  L.info = up(L.counters + 4 * ctas);
+  L.starts = up(L.info + sizeof(SeqInfo) * static_cast<size_t>(B));
+  L.stats = up(L.starts + 8 * (static_cast<size_t>(B) + 1));
+  // two pieces of up to 16 rows per CTA
+  L.partial = up(L.stats + 2 * ctas * 16 * 8);
+  L.total = up(L.partial + 2 * ctas * 16 * static_cast<size_t>(c->head_dim) * 4);
+  return L;
+}
+
+cudaError_t launch_kv_attention(bool bf16, const AttnArgs& a, void* ws, const AttnLayout& L,
+                                cudaStream_t st) {
+  switch (a.D) {
+    case 64:
+      return launch_dim<64>(bf16, a, ws, L, st);
+    case 128:
+      return launch_dim<128>(bf16, a, ws, L, st);
+    default:
+      return launch_dim<256>(bf16, a, ws, L, st);
+  }
+}
+
+}  // namespace moe

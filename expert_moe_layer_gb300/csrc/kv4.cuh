@@ -1,0 +1,96 @@
+// The 4-bit cache format (include/moe.h) and its conversions.
+//
+// e2m1 codes and e4m3 scales are the 4- and 8-bit floats that sm_103a converts
+// in hardware. Their product has at most 2 + 4 significant bits and lies in
+// 2^-10 .. 2688, so it is exact in f16: a stored element enters a matrix
+// instruction without any rounding.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace moe {
+
+constexpr int kKvGroup = 16;  // channels per scale
+
+// Byte offsets inside one (page, kv head) block.
+struct KvBlock {
+  uint32_t k_scale, v_code, v_scale, bytes;
+};
+__host__ __device__ constexpr KvBlock kv_block(int page_size, int D) {
+  const uint32_t codes = static_cast<uint32_t>(page_size) * D / 2;
+  const uint32_t scales = static_cast<uint32_t>(page_size) * D / kKvGroup;
+  return {codes, codes + scales, 2 * codes + scales, 2 * (codes + scales)};
+}
+
+// Two floats -> two e2m1 codes, nearest even, saturating; `lo` in the low half.
+__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
+      "cvt.u32.u8 %0, b;\n\t}"
+      : "=r"(r)
+      : "f"(hi), "f"(lo));
+  return r;
+}
+
+// One float -> e4m3, nearest even, saturating at 448.
+__device__ __forceinline__ uint32_t e4m3(float x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(x));
+  return r & 0xffu;
+}
+
+// Eight codes (one word) -> eight f16 values, two by two in channel order.
+__device__ __forceinline__ void e2m1_to_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
+// Two e4m3 scales -> f16x2 (first scale in the low half).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t two) {
+  uint32_t r;
+  const uint16_t h = static_cast<uint16_t>(two);
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16_low_twice(uint32_t h) { return __byte_perm(h, 0, 0x1010); }
+__device__ __forceinline__ uint32_t f16_high_twice(uint32_t h) { return __byte_perm(h, 0, 0x3232); }
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// 16 values of a group -> 8 code bytes and the scale byte.
+__device__ __forceinline__ uint32_t kv_store_group(const float (&x)[16], float inv_scale,
+                                                   uint32_t (&codes)[2]) {
+  float y[16], top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float t = __fmul_rn(x[i], inv_scale);
+    y[i] = t == t ? t : 0.0f;
+    top = fmaxf(top, fabsf(y[i]));
+  }
+  const uint32_t s8 = e4m3(__fmul_rn(top, 1.0f / 6.0f));
+  const float s = __half2float(__ushort_as_half(static_cast<uint16_t>(e4m3x2_to_f16(s8) & 0xffffu)));
+  codes[0] = codes[1] = 0;
+  if (s > 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      codes[i >> 2] |= e2m1x2(__fdiv_rn(y[2 * i], s), __fdiv_rn(y[2 * i + 1], s)) << (8 * (i & 3));
+  }
+  return s8;
+}
+
+}  // namespace moe

@@ -36,10 +36,15 @@ constexpr size_t kAlignBytes = 256;
 constexpr int kEncodeErrorBase = 10000;
 thread_local int g_last_cuda_error = 0;
 
+}  // namespace
+
 int fail_cuda(int code) {
   g_last_cuda_error = code;
   return MOE_ERR_CUDA;
 }
+
+namespace {
+
 int cuda_ok(cudaError_t e) { return e == cudaSuccess ? MOE_OK : fail_cuda(static_cast<int>(e)); }
 
 #define MOE_TRY(x)              \
@@ -256,6 +261,8 @@ int context_sms() {
   return static_cast<int>(r.sm.smCount);
 }
 
+}  // namespace
+
 // SMs the persistent grids run on: those of the current context where it
 // has fewer than the device (the fused decode kernel's CTAs wait on one
 // another, so its grid must fit), else the device's. Not cached: one device
@@ -269,6 +276,8 @@ int sm_count() {
   const int c = context_sms();
   return (c > 0 && c < n) ? c : n;
 }
+
+namespace {
 
 // -------------------------------------------------------------- tensor maps
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {

@@ -88,6 +88,10 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
 #define MOE_DEV_TIMEOUT 0x4u       /* a GEMM pipeline wait passed its time
                                       limit; that kernel stopped early      */
 #define MOE_DEV_BAD_SEGMENT 0x8u   /* offsets/counts inconsistent          */
+#define MOE_DEV_BAD_POSITION 0x10u /* position outside the rotary table     */
+#define MOE_DEV_BAD_SLOT 0x20u     /* cache slot outside the cache          */
+#define MOE_DEV_BAD_PAGE 0x40u     /* page id outside the cache, or a length
+                                      outside the page table                */
 
 /* Layer description. The field names follow the FusedMoE arguments the
  * pages pass (num_experts, top_k, hidden_size, intermediate_size,
@@ -466,6 +470,175 @@ MOE_API int moe_set_wait_limit_ns(uint64_t ns);
  * tensor-map encoding that failed; 0 if no call of this thread has failed.
  * Not cleared by later successful calls. No CUDA call. */
 MOE_API int moe_last_cuda_error(void);
+
+/* ------------------------------------------------------------------------ */
+/* Attention beside the MoE layer: rotary positions, a paged cache of keys
+ * and values in 4 bits, and attention over it. The source pages describe the
+ * MoE half of a decoder layer only; these entry points are the other half, so
+ * that a serving loop can run whole layers through one library. They follow
+ * the conventions above, with these differences:
+ *   - x, q, k, v may be slices of a wider tensor: they take a token stride and
+ *     a head stride in elements (multiples of 16 bytes for q of
+ *     moe_kv_attention); the channels of a head are contiguous. Outputs are
+ *     contiguous, [T, heads, head_dim].
+ *   - `ws` of moe_rope_table, moe_rope, moe_kv_append and moe_kv_read is NULL
+ *     or >= 4 bytes for the status word, which a call then clears first.
+ *
+ * Cache format. `cache` is [num_pages, num_kv_heads, B] bytes with
+ * B = page_size * head_dim * 9 / 8. A (page, kv head) block holds, in order:
+ *   key codes   [page_size, head_dim / 2]   key scales   [page_size, head_dim / 16]
+ *   value codes [page_size, head_dim / 2]   value scales [page_size, head_dim / 16]
+ * A code is a 4-bit float (e2m1: 0, .5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives), two to a byte, the lower channel in the low half. A scale is an
+ * e4m3 float shared by 16 neighbouring channels. A stored element stands for
+ * code * scale * k_scale (v_scale for values).
+ * Storing x: y = x * (1 / k_scale) in fp32 (NaN becomes 0); scale = e4m3 of
+ * max|y| * (1/6) over the 16 channels, to nearest even, at most 448; code =
+ * e2m1 of y / scale to nearest even, at most 6 in magnitude (0 where the
+ * scale is 0). Slot s of a cache is row s % page_size of page s / page_size. */
+typedef struct {
+  int num_heads;        /* query heads, a multiple of num_kv_heads, <= 512    */
+  int num_kv_heads;     /* heads of keys and values (moe_rope_table and
+                           moe_rope do not use the head counts)               */
+  int head_dim;         /* D: even, <= 512; the cache calls take 64, 128, 256 */
+  int page_size;        /* tokens per page: 16, 32, 64, 128 or 256            */
+  moe_dtype act_dtype;  /* q, k, v, out                                       */
+  int rotary_dim;       /* R: channels 0..R-1 of a head rotate; even, 0..D    */
+  int rope_layout;      /* MOE_ROPE_HALF: channel i pairs with i + R/2;
+                           MOE_ROPE_INTERLEAVED: 2i pairs with 2i + 1         */
+  int rope_positions;   /* rows of the cos/sin table (>= 1 when R > 0)        */
+  int window;           /* sliding window: a query sees its own key and the
+                           window - 1 before it; 0 = all                      */
+  float softmax_scale;  /* 0: 1 / sqrt(D)                                     */
+  float k_scale;        /* > 0 and finite: what a stored key is multiplied by */
+  float v_scale;
+} moe_attn_config;
+
+#define MOE_ROPE_HALF 0
+#define MOE_ROPE_INTERLEAVED 1
+
+/* Rotary frequencies: f_i = base^(-2i/R) radians per position for pair i, and
+ * for contexts `factor` (s) times the original one:
+ *   LINEAR  f_i / s
+ *   NTK     base * s^(R/(R-2)) in the place of base (R > 2)
+ *   PARTS   by the turns n_i = original_positions * f_i / 2pi of the pair in
+ *           the original context: f_i * w + (f_i / s) * (1 - w),
+ *           w = clamp((n_i - slow_turns) / (fast_turns - slow_turns), 0, 1)
+ *   YARN    (Peng et al., "YaRN", 2023) the same mix with a ramp over the pair
+ *           index between the pairs d(fast_turns), rounded down, and
+ *           d(slow_turns), rounded up, d(n) = R ln(original / (2pi n)) /
+ *           (2 ln base); cosines and sines times attention_factor. */
+#define MOE_ROPE_SCALE_NONE 0
+#define MOE_ROPE_SCALE_LINEAR 1
+#define MOE_ROPE_SCALE_NTK 2
+#define MOE_ROPE_SCALE_PARTS 3
+#define MOE_ROPE_SCALE_YARN 4
+
+typedef struct {
+  double base;              /* > 1                                            */
+  int kind;                 /* MOE_ROPE_SCALE_*                               */
+  double factor;            /* s >= 1 (unused by NONE)                        */
+  double original_positions; /* > 0 for PARTS and YARN                        */
+  double slow_turns;        /* 0: 1                                           */
+  double fast_turns;        /* 0: 4 (PARTS) or 32 (YARN); > slow_turns        */
+  double attention_factor;  /* 0: 0.1 ln s + 1 for YARN, else 1               */
+} moe_rope_scaling;
+
+/* Host-only validation. MOE_ERR_INVALID_ARG for what the fields' comments
+ * rule out; MOE_ERR_UNSUPPORTED for head_dim > 512 or num_heads > 512. */
+MOE_API int moe_validate_attn_config(const moe_attn_config* cfg);
+
+/* Bytes of one page over all kv heads; 0 if the config is invalid or its
+ * head_dim has no cache kernels. */
+MOE_API size_t moe_kv_page_bytes(const moe_attn_config* cfg);
+
+/* moe_rope_table: rows of cosines and sines, fp32 [n, R]: row r holds cos(p f_i)
+ * for the R/2 pairs, then sin(p f_i), p = positions[r] (int32, any value), or
+ * p = r when positions is NULL. Each angle is reduced exactly: the frequency is
+ * held as a 64-bit fraction of a turn, so p f_i mod 1 turn is an integer product
+ * that wraps. n may be up to 2^24. */
+MOE_API int moe_rope_table(const moe_attn_config* cfg, int n, const int32_t* positions,
+                           const moe_rope_scaling* scaling, float* table, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* moe_rope: out = x with each pair (a, b) of the first R channels turned to
+ * (a cos - b sin, b cos + a sin) by row positions[t] of `table` (the two
+ * products and their sum each rounded in fp32); the other channels are copied.
+ *   x         [T, num_heads, D], act_dtype, strides as above; num_heads is the
+ *             argument (a call may rotate queries or keys)
+ *   positions [T] int32, table [rope_positions, R] fp32
+ *   inverse   1: turn back (sin negated), which is also the gradient of x
+ *   out       [T, num_heads, D]. It may be x itself where x is contiguous.
+ * A position outside [0, rope_positions) sets MOE_DEV_BAD_POSITION and leaves
+ * the token's rows of `out` unwritten. */
+MOE_API int moe_rope(const moe_attn_config* cfg, int T, int num_heads, const void* x,
+                     int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions,
+                     const float* table, int inverse, void* out, void* ws, size_t ws_bytes,
+                     void* stream);
+
+/* moe_kv_append: T tokens' keys and values into the cache, one kernel.
+ * Keys are rotated as by moe_rope and rounded to act_dtype, then keys and
+ * values are stored as above. With q, the queries are rotated into q_out in the
+ * same launch.
+ *   q [T, num_heads, D] nullable (then q_out is not written), k and v
+ *   [T, num_kv_heads, D]; strides as above
+ *   positions [T], table: as moe_rope; both NULL when rotary_dim is 0
+ *   slots [T] int64: where each token goes; -1 = nowhere (a padding token: its
+ *   queries are still rotated). Two tokens must not share a slot.
+ * A slot outside [-1, num_pages * page_size) sets MOE_DEV_BAD_SLOT and a bad
+ * position MOE_DEV_BAD_POSITION; the token is then skipped. */
+MOE_API int moe_kv_append(const moe_attn_config* cfg, int T, const void* q,
+                          int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                          int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                          int64_t v_token_stride, int64_t v_head_stride,
+                          const int32_t* positions, const int64_t* slots, const float* table,
+                          void* q_out, void* cache, int64_t num_pages, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/* moe_kv_read: the values that N slots of the cache stand for, as act_dtype
+ * rows (to hand a prefix over, or to look at it).
+ *   slots [N] int64, -1 = a row of zeros; k_out, v_out [N, num_kv_heads, D]
+ * A slot outside [-1, num_pages * page_size) also reads as zeros and sets
+ * MOE_DEV_BAD_SLOT. */
+MOE_API int moe_kv_read(const moe_attn_config* cfg, int N, const int64_t* slots,
+                        const void* cache, int64_t num_pages, void* k_out, void* v_out, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/* moe_kv_attention: attention of T query tokens of num_seqs requests over the
+ * cache. Request b has the query rows q_offsets[b] .. q_offsets[b+1] - 1 and
+ * seq_lens[b] tokens in the cache, its own query tokens (appended before) last:
+ * its query i is token p = seq_lens[b] - q_len + i and sees the keys
+ * max(0, p - window + 1) .. p (0 .. p without a window). Query head h reads kv
+ * head h / (num_heads / num_kv_heads).
+ *   out[i,h] = sum_j softmax_j(softmax_scale * q[i,h] . k_j) v_j
+ * Softmax statistics and sums are fp32. A query that sees no key gives zeros.
+ *   q [T, num_heads, D], strides as above: head_dim contiguous, token and head
+ *     strides and the base multiples of 16 bytes
+ *   q_offsets [num_seqs + 1] int32, or NULL: one query token per request
+ *     (T == num_seqs)
+ *   seq_lens [num_seqs] int32
+ *   page_table [num_seqs, max_pages] int32: token t of request b is row
+ *     t % page_size of page page_table[b][t / page_size]; entries past a
+ *     request's length, or wholly before its window, are not read
+ *   max_q_len: at least the longest request's query tokens
+ *   out [T, num_heads, D]; lse [T, num_heads] fp32, nullable: the logarithm of
+ *     the softmax denominator (-inf for a query that sees no key)
+ * Query rows outside every request are not written. Device flags:
+ * MOE_DEV_BAD_SEGMENT for q_offsets that decrease, leave [0, T] or give a
+ * request more than max_q_len tokens (the request is skipped);
+ * MOE_DEV_BAD_PAGE for a page id outside [0, num_pages) (its tokens are left
+ * out), or a length below 0 or beyond the table's row (it is clamped).
+ * num_seqs and max_pages may be up to 2^18 and 2^20.
+ * ws: moe_kv_attention_workspace_size(cfg, num_seqs, T, max_q_len) bytes
+ * (0: invalid). */
+MOE_API size_t moe_kv_attention_workspace_size(const moe_attn_config* cfg, int num_seqs, int T,
+                                               int max_q_len);
+MOE_API int moe_kv_attention(const moe_attn_config* cfg, int num_seqs, int T, int max_q_len,
+                             const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                             const int32_t* q_offsets, const int32_t* seq_lens,
+                             const int32_t* page_table, int max_pages, const void* cache,
+                             int64_t num_pages, void* out, float* lse, void* ws,
+                             size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Synchronises `stream` and reads the device status word at the start of
