@@ -77,6 +77,17 @@ struct AttnLayout {
 };
 AttnLayout attn_layout(const moe_attn_config* c, int B, int sms);
 
+// One request, as the plan kernel leaves it: first query row, its tokens,
+// cached tokens, first 16-token tile that is read.
+struct SeqInfo {
+  int q0, q_len, len, first_tile;
+};
+
+// Rows of a unit of the prompt kernel, and the rows per request (query tokens
+// times heads of a group) it is used from.
+constexpr int kPromptTile = 256, kPromptRows = 64;
+cudaError_t launch_prompt(const AttnArgs& a, void* ws, const AttnLayout& L, cudaStream_t st);
+
 cudaError_t launch_kv_attention(bool bf16, const AttnArgs& a, void* ws, const AttnLayout& L,
                                 cudaStream_t st);
 

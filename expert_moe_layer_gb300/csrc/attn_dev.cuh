@@ -1,0 +1,74 @@
+// Device helpers shared by the attention kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "attn.h"
+#include "kv4.cuh"
+
+namespace moe {
+
+// P = exp2(score - maximum) is kept as f16 times 2^kLift, so that small
+// probabilities keep their bits, and the running maximum may lag behind by
+// kLag powers of two before sums are rescaled: P stays below 2^15.
+constexpr float kLift = 6.0f, kLag = 8.0f;
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+template <int N>
+struct Words {
+  uint32_t w[N];
+};
+template <int N>
+__device__ __forceinline__ Words<N> load_words(const uint8_t* p) {
+  Words<N> r;
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
+    }
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    r.w[0] = v.x, r.w[1] = v.y;
+  } else {
+    r.w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+  return r;
+}
+
+// A power of two (and its inverse) that brings a query row whose largest
+// element is `top` into [128, 256): every bit of a bf16 element then survives
+// in f16 unless the element is 2^-22 of the largest.
+__device__ __forceinline__ void row_power(float top, float& up, float& down) {
+  int e = static_cast<int>((__float_as_uint(top) >> 23) & 0xffu) - 127;
+  e = max(-90, min(127, e));
+  up = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
+  down = __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
+}
+
+// 1 / denominator times `gain`; 0 for a query that saw no key (NaN stays NaN).
+__device__ __forceinline__ float out_factor(float den, float gain) {
+  return den > 0.0f || den != den ? gain / den : 0.0f;
+}
+__device__ __forceinline__ float log_sum(float base, float den) {
+  return den > 0.0f || den != den ? (base + log2f(den)) * 0.69314718f : -INFINITY;
+}
+
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                            *reinterpret_cast<const uint32_t*>(&hi));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+
+}  // namespace moe

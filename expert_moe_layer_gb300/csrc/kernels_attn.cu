@@ -23,8 +23,7 @@
 #include <atomic>
 #include <cmath>
 
-#include "attn.h"
-#include "kv4.cuh"
+#include "attn_dev.cuh"
 #include "launch.cuh"
 #include "ptx.cuh"
 
@@ -38,21 +37,13 @@ constexpr int kMinTiles = 2 * kWarps;  // smallest range of a CTA
 constexpr int kMaxCtasPerSm = 4;
 constexpr int kPlanThreads = 1024;
 
-// P is kept as f16 times 2^kLift, so that small probabilities keep their bits
-// and the running maximum may lag behind by kLag (both in powers of two).
-constexpr float kLift = 6.0f, kLag = 8.0f;
-
-// One request, as the plan kernel leaves it.
-struct SeqInfo {
-  int q0, q_len, len, first_tile;  // first query row, its tokens, cached tokens, first tile read
-};
-
 __device__ __forceinline__ long shfl_up(long v, int d) { return __shfl_up_sync(~0u, v, d); }
 
-// Clears the status and the join counters, checks every request and sums the
-// tiles of all segments: starts[b] is the first tile of request b in the list.
+// Clears the status and the counters, checks every request and sums up the
+// work list: starts[b] is the first tile of request b in it (with `whole`, the
+// first segment: a row tile of a kv head is one unit then).
 __global__ void __launch_bounds__(kPlanThreads)
-    attn_plan_kernel(AttnArgs a, int row_tile, unsigned* status, int* counters, int n_counters,
+    attn_plan_kernel(AttnArgs a, int row_tile, bool whole, unsigned* status, int* counters, int n_counters,
                      SeqInfo* info, long* starts) {
   pdl_enter();
   if (threadIdx.x == 0) *status = 0;
@@ -87,7 +78,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       // a request without cached tokens keeps one empty tile per segment: its
       // rows still have to be written
       long per = (s.len + kTile - 1) / kTile - s.first_tile;
-      per = per < 1 ? 1 : per;
+      per = per < 1 || whole ? 1 : per;
       tiles = row_tiles * a.kv_heads * per;
       info[b] = s;
     }
@@ -130,36 +121,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float2 unpack_f16(uint32_t v) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&v));
-}
-
-template <int N>
-struct Words {
-  uint32_t w[N];
-};
-template <int N>
-__device__ __forceinline__ Words<N> load_words(const uint8_t* p) {
-  Words<N> r;
-  if constexpr (N % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
-      r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
-    }
-  } else if constexpr (N == 2) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    r.w[0] = v.x, r.w[1] = v.y;
-  } else {
-    r.w[0] = *reinterpret_cast<const uint32_t*>(p);
-  }
   return r;
 }
 
@@ -297,18 +258,13 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 
 #pragma unroll
         for (int i = 0; i < D / 4; ++i) x[i] = 0.0f;
       }
-      // scale the row by a power of two so that its largest element lies in
-      // [128, 256): every bit of a bf16 element then survives in f16 unless it
-      // is 2^-22 of the largest
       float top = 0.0f;
 #pragma unroll
       for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
       top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
       top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-      int e = static_cast<int>((__float_as_uint(top) >> 23) & 0xffu) - 127;
-      e = max(-90, min(127, e));
-      const float up = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);
-      q_gain[nt] = __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
+      float up;
+      row_power(top, up, q_gain[nt]);
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
         const float lo = x[2 * i] * up, hi = x[2 * i + 1] * up;
@@ -539,19 +495,10 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 
         if (row0 + r < rows) {
           const int tok = (row0 + r) / group, h = kvh * group + (row0 + r) - tok * group;
           const long at_row = static_cast<long>(sq.q0 + tok) * a.heads + h;
-          const float inv = den > 0.0f || den != den ? a.v_scale / den : 0.0f;
-          T* dst = static_cast<T*>(a.out) + at_row * D + ch;
-          if constexpr (sizeof(T) == 2) {
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x * inv, sum.y * inv);
-            const __nv_bfloat162 hi = __floats2bfloat162_rn(sum.z * inv, sum.w * inv);
-            *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                                                        *reinterpret_cast<const uint32_t*>(&hi));
-          } else {
-            *reinterpret_cast<float4*>(dst) =
-                make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
-          }
-          if (a.lse && ch == 0)
-            a.lse[at_row] = den > 0.0f || den != den ? (top + log2f(den)) * 0.69314718f : -INFINITY;
+          const float f = out_factor(den, a.v_scale);
+          store4(static_cast<T*>(a.out) + at_row * D + ch,
+                 make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f));
+          if (a.lse && ch == 0) a.lse[at_row] = log_sum(top, den);
         }
       } else {
         *reinterpret_cast<float4*>(partial + (my_slot * kRows + r) * D + ch) = sum;
@@ -589,25 +536,25 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 
           }
           const int tok = (row0 + r) / group, h = kvh * group + (row0 + r) - tok * group;
           const long at_row = static_cast<long>(sq.q0 + tok) * a.heads + h;
-          const float inv = den > 0.0f || den != den ? a.v_scale / den : 0.0f;
-          T* dst = static_cast<T*>(a.out) + at_row * D + ch;
-          if constexpr (sizeof(T) == 2) {
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x * inv, sum.y * inv);
-            const __nv_bfloat162 hi = __floats2bfloat162_rn(sum.z * inv, sum.w * inv);
-            *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                                                        *reinterpret_cast<const uint32_t*>(&hi));
-          } else {
-            *reinterpret_cast<float4*>(dst) =
-                make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
-          }
-          if (a.lse && ch == 0)
-            a.lse[at_row] = den > 0.0f || den != den ? (top + log2f(den)) * 0.69314718f : -INFINITY;
+          const float f = out_factor(den, a.v_scale);
+          store4(static_cast<T*>(a.out) + at_row * D + ch,
+                 make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f));
+          if (a.lse && ch == 0) a.lse[at_row] = log_sum(top, den);
         }
       }
     }
     __syncthreads();
     at += t1 - t0;
   }
+}
+
+cudaError_t launch_plan(const AttnArgs& a, int row_tile, bool whole, int n_counters, void* ws,
+                        const AttnLayout& L, cudaStream_t st) {
+  char* w = static_cast<char*>(ws);
+  return launch_pdl(&attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a, row_tile, whole,
+                    reinterpret_cast<unsigned*>(w + L.status),
+                    reinterpret_cast<int*>(w + L.counters), n_counters,
+                    reinterpret_cast<SeqInfo*>(w + L.info), reinterpret_cast<long*>(w + L.starts));
 }
 
 template <typename T, int D, int NT, int kTerms>
@@ -619,8 +566,7 @@ cudaError_t launch_split(const AttnArgs& a, void* ws, const AttnLayout& L, cudaS
   auto* stats = reinterpret_cast<float*>(static_cast<char*>(ws) + L.stats);
   auto* partial = reinterpret_cast<float*>(static_cast<char*>(ws) + L.partial);
   const int grid = a.sms * ((D == 256 || NT * kTerms > 1) ? 2 : 4);
-  cudaError_t e = launch_pdl(&attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a, 8 * NT,
-                             status, counters, grid, info, starts);
+  cudaError_t e = launch_plan(a, 8 * NT, false, grid, ws, L, st);
   if (e != cudaSuccess) return e;
   const int smem = kWarps * 8 * NT * (D + 2) * 4;
   static std::atomic<unsigned long long> done{0};
@@ -661,6 +607,12 @@ AttnLayout attn_layout(const moe_attn_config* c, int B, int sms) {
 
 cudaError_t launch_kv_attention(bool bf16, const AttnArgs& a, void* ws, const AttnLayout& L,
                                 cudaStream_t st) {
+  // From kPromptRows rows per request the matrix work, not the cache's
+  // bandwidth, is the bound: the prompt kernel.
+  if (bf16 && a.D <= 128 && static_cast<long>(a.max_q) * (a.heads / a.kv_heads) >= kPromptRows) {
+    const cudaError_t e = launch_plan(a, kPromptTile, true, 1, ws, L, st);
+    return e != cudaSuccess ? e : launch_prompt(a, ws, L, st);
+  }
   switch (a.D) {
     case 64:
       return launch_dim<64>(bf16, a, ws, L, st);

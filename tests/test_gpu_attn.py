@@ -257,7 +257,7 @@ class Case:
                            self.cache, self.out, self.lse, self.ws, stream=stream)
         return self
 
-    def check(self, rows=None, only=None):
+    def check(self, rows=None, only=None, peaked=False):
         q, out, lse = _f64(self.q), _f64(self.out), _f64(self.lse)
         for b, n in enumerate(self.lens):
             if only is not None and b not in only:
@@ -272,6 +272,8 @@ class Case:
                 sums = (n / 16 + 32) * 2.0 ** -23
                 p = 2.0 ** -11 if self.dtype == "bf16" else 2.0 ** -21
                 tol = self.u * np.abs(ref) + size * (2 * ds[..., None] + p + sums + 2.0 ** -21)
+                if peaked:  # weights far below the largest one fall under f16's last bit
+                    tol += 2.0 ** -31 * np.abs(self.v[b]).sum(0).repeat(ref.shape[1] // self.kv, axis=0)
                 err = np.abs(out[sl][i:i + 1] - ref)
                 assert (err <= tol).all(), (b, i, (err - tol).max(), err.max())
                 seen = np.isfinite(l)
@@ -359,6 +361,74 @@ def test_attention_without_offsets_or_lse_and_on_another_stream():
     c.out.fill_(1.0)
     B.moe_kv_attention(c.cfg, 3, 3, 1, c.q, None, c.d["lens"], c.d["table"], c.cache, c.out, None, c.ws)
     assert torch.equal(c.out, want)
+
+
+PROMPT = [  # heads, kv heads, D, page, lens, query tokens, window (bf16, >= 64 rows a request)
+    (8, 2, 128, 16, [40], [40], 0),                      # one half, one tile
+    (4, 1, 64, 64, [130], [50], 0),
+    (2, 2, 128, 32, [300, 129, 128], [300, 129, 1], 0),  # two halves, several tiles
+    (16, 2, 128, 64, [515, 20, 0, 90], [65, 20, 0, 33], 0),
+    (5, 1, 64, 16, [400, 31], [100, 31], 0),             # a group of five: tokens cross halves
+    (24, 1, 128, 128, [260], [30], 0),
+    (4, 2, 128, 16, [700, 260], [200, 260], 70),         # window: first tile not the first page
+    (8, 8, 64, 256, [1000], [600], 300),
+    (3, 1, 128, 16, [33, 5], [60, 40], 0),               # queries before the first token
+    (16, 16, 128, 64, [2050], [2050], 0),                # more units than SMs
+]
+
+
+@pytest.mark.parametrize("i", range(len(PROMPT)))
+def test_attention_prompt(i):
+    heads, kv, D, page, lens, qs, window = PROMPT[i]
+    c = Case(100 + i, "bf16", heads, kv, D, page, lens, qs, window)
+    assert max(qs) * heads // kv >= 64
+    c.run()
+    assert B.moe_get_status(c.ws) == (0, 0)
+    rows = None if c.T * heads < 4000 else sorted({0, 1, 63, 64, 127, 128, 129, 255, 256, 257, 500, 1000, 2047, 2048, 2049})
+    c.check(rows=rows)
+    first = (c.out.clone(), c.lse.clone())
+    c.out.fill_(1.0)
+    c.run()
+    assert torch.equal(c.out, first[0]) and torch.equal(c.lse, first[1])
+
+
+def test_attention_prompt_peaked_scores_rescale():
+    """Scores spread over hundreds: most weights are far below the largest. p is
+    kept as f16 times at least 2^6 over the maximum, its last bit is 2^-24, so a
+    weight is off by up to 2^-25 / 2^6 of the largest: sum_j |v_j| 2^-31 more."""
+    c = Case(120, "bf16", 4, 2, 128, 16, [600], [150], q_scale=40.0).run()
+    assert B.moe_get_status(c.ws) == (0, 0)
+    c.check(rows=range(0, 150, 7), peaked=True)
+
+
+def test_attention_prompt_bad_pages():
+    c = Case(121, "bf16", 4, 2, 128, 16, [200, 150], [70, 64])
+    c.run()
+    good = c.out.clone()
+    c.d["table"][0, 3] = c.cache.shape[0]
+    c.run()
+    assert B.moe_get_status(c.ws) == (5, B.DEV_BAD_PAGE)
+    assert torch.equal(c.out[70:], good[70:])
+    keep = np.r_[0:48, 64:200]
+    for i in (0, 5, 69):
+        p = 200 - 70 + i
+        k = keep[keep <= p]
+        ref, _, size, _ = A.attention(_f64(c.q)[i:i + 1], c.k[0][k], c.v[0][k], len(k), c.scale)
+        assert (np.abs(_f64(c.out)[i:i + 1] - ref) <= 2.0 ** -8 * np.abs(ref) + size * 2.0 ** -10).all()
+
+
+def test_attention_prompt_wait_limit_runs_out_then_the_next_call_is_exact():
+    c = Case(122, "bf16", 8, 2, 128, 64, [1500], [700])
+    try:
+        B.set_wait_limit_ns(4)
+        c.run()
+        rc, flags = B.moe_get_status(c.ws)
+        assert rc == 6 and flags & B.DEV_TIMEOUT, (rc, flags)
+    finally:
+        B.set_wait_limit_ns(0)
+    c.run()
+    assert B.moe_get_status(c.ws) == (0, 0)
+    c.check(rows=(0, 300, 699))
 
 
 def test_attention_flags_bad_pages_lengths_and_offsets():
