@@ -10,12 +10,14 @@
 // depend on who is last).
 //
 // Few rows read many bytes, so the cache's bandwidth bounds this kernel and
-// the arithmetic has to hide behind it. Per tile a warp loads its codes
-// straight into the registers of the matrix instruction: the k index of
+// the arithmetic has to hide behind it. A warp reads its codes straight
+// into the operands of the matrix instruction: the k index of
 // S^T = K Q^T and the m index of O^T = V^T P^T may be permuted freely as long
 // as both operands agree, so a lane takes D/4 neighbouring channels of two key
 // rows and D/8 neighbouring channels of four value rows, whole words of codes
-// under one or two scales. Codes times scales are exact in f16.
+// under one or two scales. Codes times scales are exact in f16. The codes come
+// through a ring of tiles in shared memory that belongs to the warp alone, so
+// that enough bytes are on the way without registers and without barriers.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -34,6 +36,10 @@ constexpr int kTile = 16;   // cached tokens per tile
 constexpr int kWarps = 4;   // per CTA; each takes every fourth tile of a segment
 constexpr int kThreads = kWarps * 32;
 constexpr int kMinTiles = 2 * kWarps;  // smallest range of a CTA
+// A segment's set-up (its queries, the join of the warps, its rows' stores)
+// takes a CTA as long as this many tiles; the list counts them.
+constexpr int kSetup = 8;
+constexpr int kStages = 4;  // tiles a warp has in shared memory or on the way
 constexpr int kMaxCtasPerSm = 4;
 constexpr int kPlanThreads = 1024;
 
@@ -75,11 +81,8 @@ __global__ void __launch_bounds__(kPlanThreads)
         s.first_tile = lo > 0 ? static_cast<int>(lo / kTile) : 0;
       }
       const long row_tiles = (static_cast<long>(s.q_len) * g + row_tile - 1) / row_tile;
-      // a request without cached tokens keeps one empty tile per segment: its
-      // rows still have to be written
-      long per = (s.len + kTile - 1) / kTile - s.first_tile;
-      per = per < 1 || whole ? 1 : per;
-      tiles = row_tiles * a.kv_heads * per;
+      const long per = (s.len + kTile - 1) / kTile - s.first_tile;
+      tiles = row_tiles * a.kv_heads * (whole ? 1 : kSetup + (per < 0 ? 0 : per));
       info[b] = s;
     }
     long sum = tiles;
@@ -139,24 +142,58 @@ struct TileRegs {
   uint32_t ks[2], vs[4];
 };
 
-// The codes and scales of a tile, for lane (g, c) = (lane / 4, lane % 4).
+// A tile in shared memory: the rows of key codes, value codes, key scales and
+// value scales. Value rows are swizzled (bits 5 and 6 of the offset), so that
+// the four even or odd rows that a quarter of the lanes reads lie in different
+// banks.
 template <int D>
-__device__ __forceinline__ void load_tile(TileRegs<D>& t, const uint8_t* block, int page_size,
-                                          int row0, int g, int c) {
-  constexpr int kRow = D / 2, kScales = D / kKvGroup;
-  constexpr int kVs = D >= 128 ? D / 128 : 1;  // scales a lane's value channels fall under
+struct TileBytes {
+  static constexpr int kRow = D / 2, kScales = D / kKvGroup;
+  static constexpr int kCodes = kTile * kRow, kAllScales = kTile * kScales;
+  static constexpr int kV = kCodes, kKs = 2 * kCodes, kVs = kKs + kAllScales;
+  static constexpr int kBytes = kVs + kAllScales;
+  __device__ static constexpr uint32_t value(int row, int byte) {
+    return static_cast<uint32_t>((row * kRow + byte) ^ (((row >> 1) & 3) << 5));
+  }
+};
+
+// Copies a tile (rows row0 .. row0 + 15 of a block) into a stage.
+template <int D>
+__device__ __forceinline__ void copy_tile(uint32_t stage, const uint8_t* block, int page_size,
+                                          int row0, int lane) {
+  using B = TileBytes<D>;
   const KvBlock blk = kv_block(page_size, D);
+  const uint8_t* k = block + row0 * B::kRow;
+  const uint8_t* v = k + blk.v_code;
+#pragma unroll
+  for (int i = lane; i < B::kCodes / 16; i += 32) ptx::cp_async16(stage + 16 * i, k + 16 * i);
+#pragma unroll
+  for (int i = lane; i < B::kCodes / 16; i += 32)
+    ptx::cp_async16(stage + B::kV + B::value(16 * i / B::kRow, 16 * i % B::kRow), v + 16 * i);
+  constexpr int kChunks = B::kAllScales / 16;
+  if (lane < 2 * kChunks) {
+    const uint32_t off = lane < kChunks ? blk.k_scale : blk.v_scale;
+    ptx::cp_async16(stage + B::kKs + 16 * lane,
+                    block + off + row0 * B::kScales + 16 * (lane < kChunks ? lane : lane - kChunks));
+  }
+}
+
+// The codes and scales of a staged tile for lane (g, c) = (lane / 4, lane % 4).
+template <int D>
+__device__ __forceinline__ void load_tile(TileRegs<D>& t, const uint8_t* stage, int g, int c) {
+  using B = TileBytes<D>;
+  constexpr int kVs = D >= 128 ? D / 128 : 1;  // scales a lane's value channels fall under
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int r = row0 + g + 8 * i;
-    t.k[i] = load_words<D / 32>(block + r * kRow + c * (D / 8));
-    t.ks[i] = load_scales<D / 64>(block + blk.k_scale + r * kScales + c * (D / 64));
+    const int r = g + 8 * i;
+    t.k[i] = load_words<D / 32>(stage + r * B::kRow + c * (D / 8));
+    t.ks[i] = load_scales<D / 64>(stage + B::kKs + r * B::kScales + c * (D / 64));
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = row0 + 2 * c + (i & 1) + 8 * (i >> 1);
-    t.v[i] = load_words<D / 64>(block + blk.v_code + r * kRow + g * (D / 16));
-    t.vs[i] = load_scales<kVs>(block + blk.v_scale + r * kScales + g * D / 8 / kKvGroup);
+    const int r = 2 * c + (i & 1) + 8 * (i >> 1);
+    t.v[i] = load_words<D / 64>(stage + B::kV + B::value(r, g * (D / 16)));
+    t.vs[i] = load_scales<kVs>(stage + B::kVs + r * B::kScales + g * D / 8 / kKvGroup);
   }
 }
 
@@ -164,14 +201,22 @@ __device__ __forceinline__ void load_tile(TileRegs<D>& t, const uint8_t* block, 
 // layers): q and P are a sum of two f16 each, 22 bits, and each tile's product
 // with V is added to the running sum by fp32 additions, because the matrix
 // unit's own accumulation truncates.
+template <int D, int NT>
+__host__ __device__ constexpr int split_smem() {
+  constexpr int stages = kWarps * kStages * TileBytes<D>::kBytes, sums = kWarps * 8 * NT * D * 4;
+  return (stages > sums ? stages : sums) + kWarps * 8 * NT * 8;
+}
+
 template <typename T, int D, int NT, int kTerms>
 __global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 4)
     attn_split_kernel(AttnArgs a, unsigned* status, int* counters, const SeqInfo* info,
                       const long* starts, float* stats, float* partial, int tiles_per_page_log2) {
   constexpr int kRows = 8 * NT;
   constexpr int kVs = D >= 128 ? D / 128 : 1;
-  extern __shared__ float smem[];  // [kWarps][kRows][D] sums, then [kWarps][kRows][2] statistics
-  float* s_stat = smem + kWarps * kRows * D;
+  // The warps' stages; after a segment's last tile [kWarps][kRows][D] sums in
+  // their place. Behind them [kWarps][kRows][2] statistics.
+  extern __shared__ __align__(16) float smem[];
+  float* s_stat = smem + split_smem<D, NT>() / 4 - kWarps * kRows * 2;
   __shared__ int s_last;
   pdl_enter();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -199,14 +244,16 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 
     while (starts[b + 1] <= at) ++b;
     const SeqInfo sq = info[b];
     const int rows = sq.q_len * group;
-    const int per_seg = max(1, (sq.len + kTile - 1) / kTile - sq.first_tile);
+    const int per_seg = kSetup + max(0, (sq.len + kTile - 1) / kTile - sq.first_tile);
     const long seg = (at - starts[b]) / per_seg;
-    const int t0 = static_cast<int>((at - starts[b]) - seg * per_seg);
-    const int t1 = static_cast<int>(min(static_cast<long>(per_seg), t0 + (end - at)));
+    // this CTA's part [p0, p1) of the segment's list, and of its tiles
+    const int p0 = static_cast<int>((at - starts[b]) - seg * per_seg);
+    const int p1 = static_cast<int>(min(static_cast<long>(per_seg), p0 + (end - at)));
+    const int t0 = max(0, p0 - kSetup), t1 = max(0, p1 - kSetup);
     const int row_tile = static_cast<int>(seg / a.kv_heads);
     const int kvh = static_cast<int>(seg - static_cast<long>(row_tile) * a.kv_heads);
     const int row0 = row_tile * kRows;
-    const long seg_start = at - t0, seg_end = seg_start + per_seg;
+    const long seg_start = at - p0, seg_end = seg_start + per_seg;
 
     // this lane's score columns are rows nt*8 + 2c and + 1: their token limits
     int last[NT][2], first[NT][2];
@@ -223,12 +270,12 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 
       }
     {
       const int r_end = min(rows, row0 + kRows) - 1;
-      const int p0 = sq.len - sq.q_len + row0 / group, p1 = sq.len - sq.q_len + r_end / group;
-      tile_last = p1;
-      tile_first = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
+      const int pos0 = sq.len - sq.q_len + row0 / group, pos1 = sq.len - sq.q_len + r_end / group;
+      tile_last = pos1;
+      tile_first = a.window > 0 ? max(0, pos0 - a.window + 1) : 0;
       // tokens that every row of the tile sees
-      all_last = p0;
-      all_first = a.window > 0 ? max(0, p1 - a.window + 1) : 0;
+      all_last = pos0;
+      all_first = a.window > 0 ? max(0, pos1 - a.window + 1) : 0;
     }
 
     // q^T as the B operand: column g (+ 8 nt), channels c*D/4 ..
@@ -300,25 +347,44 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 
     const int tA = max(t0, tile_first / kTile - sq.first_tile);
     const int tB = min(t1, tile_last < 0 ? 0 : tile_last / kTile + 1 - sq.first_tile);
     const int32_t* pages = a.page_table + static_cast<long>(b) * a.max_pages;
-    TileRegs<D> next;
-    bool next_ok = false;
-    auto fetch = [&](int t) {
-      const int tile = t + sq.first_tile;
-      const int id = pages[tile >> tiles_per_page_log2];
-      next_ok = id >= 0 && id < a.num_pages;
-      if (!next_ok && lane == 0) atomicOr(status, MOE_DEV_BAD_PAGE);
-      const uint8_t* block =
-          a.cache + (static_cast<long>(next_ok ? id : 0) * a.kv_heads + kvh) * blk.bytes;
-      load_tile<D>(next, block, a.page_size,
-                   (tile & ((1 << tiles_per_page_log2) - 1)) * kTile, g, c);
+    // The CTA's warps take the tiles of the range in turn. Each keeps a ring of
+    // kStages tiles: the copies run kStages - 1 tiles ahead, the page id one
+    // more.
+    uint8_t* ring = reinterpret_cast<uint8_t*>(smem) + warp * kStages * TileBytes<D>::kBytes;
+    const uint32_t ring_addr = ptx::smem_u32(ring);
+    auto page_of = [&](int t) {
+      return t < tB ? pages[(t + sq.first_tile) >> tiles_per_page_log2] : 0;
     };
-    // the kernel's warps take the tiles of the range in turn
+    uint32_t ok_bits = 0;  // by stage: the page id was good
+    auto copy = [&](int t, int stage, int id) {
+      if (t < tB) {
+        const bool ok = id >= 0 && id < a.num_pages;
+        if (!ok && lane == 0) atomicOr(status, MOE_DEV_BAD_PAGE);
+        ok_bits = (ok_bits & ~(1u << stage)) | (static_cast<uint32_t>(ok) << stage);
+        const int tile = t + sq.first_tile;
+        copy_tile<D>(ring_addr + stage * TileBytes<D>::kBytes,
+                     a.cache + (static_cast<long>(ok ? id : 0) * a.kv_heads + kvh) * blk.bytes,
+                     a.page_size, (tile & ((1 << tiles_per_page_log2) - 1)) * kTile, lane);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     int t = tA + warp;
-    if (t < tB) fetch(t);
-    for (; t < tB; t += kWarps) {
-      TileRegs<D> cur = next;
-      const bool ok = next_ok;
-      if (t + kWarps < tB) fetch(t + kWarps);
+    {
+      int ids[kStages - 1];
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) ids[i] = page_of(t + i * kWarps);
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) copy(t + i * kWarps, i, ids[i]);
+    }
+    int next_id = page_of(t + (kStages - 1) * kWarps);
+    for (int stage = 0; t < tB; t += kWarps, stage = stage + 1 == kStages ? 0 : stage + 1) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      __syncwarp();  // every lane's copies of this tile, every lane's reads of the last one
+      copy(t + (kStages - 1) * kWarps, stage == 0 ? kStages - 1 : stage - 1, next_id);
+      next_id = page_of(t + kStages * kWarps);
+      const bool ok = (ok_bits >> stage) & 1u;
+      TileRegs<D> cur;
+      load_tile<D>(cur, ring + stage * TileBytes<D>::kBytes, g, c);
       const int tok0 = (t + sq.first_tile) * kTile;
       const bool whole = ok && tok0 >= all_first && tok0 + kTile - 1 <= all_last;
 
@@ -451,7 +517,10 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 
       }
     }
 
-    // join the warps: sums [row][channel] and statistics (base, l) in shared memory
+    // join the warps: sums [row][channel] and statistics (base, l) in shared
+    // memory, in the place of the stages
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -472,10 +541,10 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 
         }
       }
     __syncthreads();
-    const bool alone = t0 == 0 && t1 == per_seg;
+    const bool alone = p0 == 0 && p1 == per_seg;
     // pieces of a segment: the CTA it begins in keeps its piece in slot 1 (its
     // range ends inside the segment), later ones in slot 0
-    const long my_slot = 2l * blockIdx.x + (t0 == 0 ? 1 : 0);
+    const long my_slot = 2l * blockIdx.x + (p0 == 0 ? 1 : 0);
     for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), ch = (i % (D / 4)) * 4;
       float top = -INFINITY;
@@ -522,10 +591,12 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 
           const int r = i / (D / 4), ch = (i % (D / 4)) * 4;
           if (row0 + r >= rows) continue;
           float top = -INFINITY;
+#pragma unroll 8
           for (int k = cta0; k <= cta1; ++k)
             top = fmaxf(top, __ldcg(stats + ((2l * k + (k == cta0)) * kRows + r) * 2));
           float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           float den = 0.0f;
+#pragma unroll 8
           for (int k = cta0; k <= cta1; ++k) {
             const long slot = (2l * k + (k == cta0)) * kRows + r;
             const float2 st = __ldcg(reinterpret_cast<const float2*>(stats + slot * 2));
@@ -544,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 
       }
     }
     __syncthreads();
-    at += t1 - t0;
+    at += p1 - p0;
   }
 }
 
@@ -568,7 +639,7 @@ cudaError_t launch_split(const AttnArgs& a, void* ws, const AttnLayout& L, cudaS
   const int grid = a.sms * ((D == 256 || NT * kTerms > 1) ? 2 : 4);
   cudaError_t e = launch_plan(a, 8 * NT, false, grid, ws, L, st);
   if (e != cudaSuccess) return e;
-  const int smem = kWarps * 8 * NT * (D + 2) * 4;
+  constexpr int smem = split_smem<D, NT>();
   static std::atomic<unsigned long long> done{0};
   e = opt_in_smem(reinterpret_cast<const void*>(&attn_split_kernel<T, D, NT, kTerms>), smem, done);
   if (e != cudaSuccess) return e;
