@@ -24,6 +24,12 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 template <int N>
 struct Words {
   uint32_t w[N];

@@ -2,7 +2,7 @@
 //
 // A work unit is a tile of 16 cached tokens of one (request, row tile, kv
 // head) segment; a row is one (query token, query head of the group) pair and
-// a row tile has 8 or 16 of them. All segments' tiles form one list, which is
+// a row tile has 4, 8 or 16 of them. All segments' tiles form one list, which is
 // cut into equal ranges, one per CTA, so that requests of any lengths fill the
 // GPU evenly. A plan kernel sums the segments' sizes; a CTA whose range covers
 // a segment writes its rows, others leave fp32 partial sums and statistics,
@@ -38,7 +38,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kMinTiles = 2 * kWarps;  // smallest range of a CTA
 // A segment's set-up (its queries, the join of the warps, its rows' stores)
 // takes a CTA as long as this many tiles; the list counts them.
-constexpr int kSetup = 8;
+constexpr int kSetup = 14;
 constexpr int kStages = 4;  // tiles a warp has in shared memory or on the way
 constexpr int kMaxCtasPerSm = 4;
 constexpr int kPlanThreads = 1024;
@@ -197,26 +197,39 @@ __device__ __forceinline__ void load_tile(TileRegs<D>& t, const uint8_t* stage, 
   }
 }
 
+template <int D, int kRows>
+__host__ __device__ constexpr int split_smem() {
+  constexpr int stages = kWarps * kStages * TileBytes<D>::kBytes, sums = kWarps * kRows * D * 4;
+  return (stages > sums ? stages : sums) + kWarps * kRows * 8;
+}
+template <int D, int kRows, int kTerms>
+__host__ __device__ constexpr int ctas_per_sm() {
+  return D == 256 || kRows == 16 || kTerms == 2 ? 2 : 4;
+}
+
+// kRows is 4, 8 or 16. The matrix instruction pairs neighbouring k indices in
+// a register, and codes come as pairs of neighbouring channels of one token, so
+// for O^T the k index runs over (token, parity of the channel) and the m index
+// over channel pairs: P of a token stands at one parity and zero at the other,
+// one set of columns for even and one for odd channels. No value has to change
+// places then. With 4 rows, both sets fit the instruction's 8 columns.
+//
 // kTerms = 1: q and P are one f16 each (q bf16: exact). kTerms = 2 (fp32
 // layers): q and P are a sum of two f16 each, 22 bits, and each tile's product
 // with V is added to the running sum by fp32 additions, because the matrix
 // unit's own accumulation truncates.
-template <int D, int NT>
-__host__ __device__ constexpr int split_smem() {
-  constexpr int stages = kWarps * kStages * TileBytes<D>::kBytes, sums = kWarps * 8 * NT * D * 4;
-  return (stages > sums ? stages : sums) + kWarps * 8 * NT * 8;
-}
-
-template <typename T, int D, int NT, int kTerms>
-__global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 4)
+template <typename T, int D, int kRows, int kTerms>
+__global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
     attn_split_kernel(AttnArgs a, unsigned* status, int* counters, const SeqInfo* info,
                       const long* starts, float* stats, float* partial, int tiles_per_page_log2) {
-  constexpr int kRows = 8 * NT;
+  constexpr bool kBoth = kRows == 4;             // columns 4-7 repeat rows 0-3
+  constexpr int NT = kBoth ? 1 : kRows / 8;      // column tiles of the scores
+  constexpr int NP = kBoth ? 1 : 2 * NT;         // column tiles of the sums
   constexpr int kVs = D >= 128 ? D / 128 : 1;
   // The warps' stages; after a segment's last tile [kWarps][kRows][D] sums in
   // their place. Behind them [kWarps][kRows][2] statistics.
   extern __shared__ __align__(16) float smem[];
-  float* s_stat = smem + split_smem<D, NT>() / 4 - kWarps * kRows * 2;
+  float* s_stat = smem + split_smem<D, kRows>() / 4 - kWarps * kRows * 2;
   __shared__ int s_last;
   pdl_enter();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -262,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int r = row0 + nt * 8 + 2 * c + j;
+        const int r = row0 + nt * 8 + (kBoth ? (2 * c + j) & 3 : 2 * c + j);
         // padding rows (zero queries whose columns are never written) see all
         const int p = sq.len - sq.q_len + r / group;
         last[nt][j] = r < rows ? p : 0x7fffffff;
@@ -283,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 
     float q_gain[NT];  // 2^-x of the row g (+ 8 nt) this lane loads
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = row0 + nt * 8 + g;
+      const int r = row0 + nt * 8 + (kBoth ? g & 3 : g);
       float x[D / 4];
       if (r < rows) {
         const int tok = r / group, h = kvh * group + (r - tok * group);
@@ -330,13 +343,13 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 
       for (int j = 0; j < 2; ++j)
         gain[nt][j] = __shfl_sync(~0u, q_gain[nt], (2 * c + j) * 4) * a.scale_log2;
 
-    float o[D / 16][NT][4];
+    float o[D / 32][NP][4];
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i)
+    for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int np = 0; np < NP; ++np)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
+        for (int j = 0; j < 4; ++j) o[i][np][j] = 0.0f;
     float m[NT][2], base[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -442,16 +455,18 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 
             x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
             x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
             const float nb = x == -INFINITY ? -kLift : x - kLift;
-            f[j] = m[nt][j] == -INFINITY ? 0.0f : exp2f(base[nt][j] - nb);
+            f[j] = m[nt][j] == -INFINITY ? 0.0f : ex2(base[nt][j] - nb);
             l[nt][j] *= f[j];
             m[nt][j] = x;
             base[nt][j] = nb;
           }
           // sums' columns are the scores' columns
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i)
+          for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[i][nt][j] *= f[j & 1];
+            for (int np = nt * (NP / NT); np < (nt + 1) * (NP / NT); ++np)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[i][np][j] *= f[j & 1];
         }
       }
       uint32_t pf[kTerms][NT][2];
@@ -460,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 
         float p[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          p[j] = exp2f(s[nt][j] - base[nt][j & 1]);
+          p[j] = ex2(s[nt][j] - base[nt][j & 1]);
           l[nt][j & 1] += p[j];
         }
 #pragma unroll
@@ -475,40 +490,57 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 
       }
       // V^T as the A operand. A token that no row sees may be uninitialised
       // memory: its scale is zeroed, so that 0 * NaN cannot enter the sum.
-      uint32_t vs[2][kVs];
+      uint32_t vs[4][kVs];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 4; ++i) {
         if (!whole) {
-          const int tok = tok0 + 2 * c + 8 * i;
-          if (!ok || tok < tile_first || tok > tile_last) cur.vs[2 * i] = 0;
-          if (!ok || tok + 1 < tile_first || tok + 1 > tile_last) cur.vs[2 * i + 1] = 0;
+          const int tok = tok0 + 2 * c + (i & 1) + 8 * (i >> 1);
+          if (!ok || tok < tile_first || tok > tile_last) cur.vs[i] = 0;
         }
 #pragma unroll
         for (int j = 0; j < kVs; ++j)
-          vs[i][j] = e4m3x2_to_f16(((cur.vs[2 * i] >> (8 * j)) & 0xffu) |
-                                   (((cur.vs[2 * i + 1] >> (8 * j)) & 0xffu) << 8));
+          vs[i][j] = e4m3x2_to_f16(((cur.vs[i] >> (8 * j)) & 0xffu) * 0x101u);
       }
+      // P at the columns of one parity: of the even channels, then of the odd
+      uint32_t pb[kTerms][2][NP][2];  // [term][half of the tokens][column tile][token 2c, 2c + 1]
 #pragma unroll
-      for (int w = 0; w < D / 64; ++w) {  // 8 channels: four m tiles
+      for (int term = 0; term < kTerms; ++term)
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int np = 0; np < NP; ++np) {
+            const uint32_t w = pf[term][kBoth ? 0 : np / 2][half];
+            const bool odd = kBoth ? g >= 4 : np & 1;
+            pb[term][half][np][0] = __byte_perm(w, 0, odd ? 0x1044 : 0x4410);
+            pb[term][half][np][1] = __byte_perm(w, 0, odd ? 0x3244 : 0x4432);
+          }
+#pragma unroll
+      for (int w = 0; w < D / 64; ++w) {  // 8 channels: two m tiles
         uint32_t h[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) e2m1_to_f16(cur.v[i].w[w], h[i]);
         const int sc = D == 256 ? w / 2 : 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t af[4] = {hmul2(__byte_perm(h[0][q], h[1][q], 0x5410), vs[0][sc]),
-                                  hmul2(__byte_perm(h[0][q], h[1][q], 0x7632), vs[0][sc]),
-                                  hmul2(__byte_perm(h[2][q], h[3][q], 0x5410), vs[1][sc]),
-                                  hmul2(__byte_perm(h[2][q], h[3][q], 0x7632), vs[1][sc])};
+        for (int i = 0; i < 4; ++i) {
+          e2m1_to_f16(cur.v[i].w[w], h[i]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float(&acc)[4] = o[4 * w + q][nt];
+          for (int q = 0; q < 4; ++q) h[i][q] = hmul2(h[i][q], vs[i][sc]);
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t af[2][4] = {{h[0][2 * q], h[0][2 * q + 1], h[1][2 * q], h[1][2 * q + 1]},
+                                     {h[2][2 * q], h[2][2 * q + 1], h[3][2 * q], h[3][2 * q + 1]}};
+#pragma unroll
+          for (int np = 0; np < NP; ++np) {
+            float(&acc)[4] = o[2 * w + q][np];
             if constexpr (kTerms == 1) {
-              mma(acc, af, pf[0][nt][0], pf[0][nt][1]);
+              mma(acc, af[0], pb[0][0][np][0], pb[0][0][np][1]);
+              mma(acc, af[1], pb[0][1][np][0], pb[0][1][np][1]);
             } else {
               float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-              mma(d, af, pf[1][nt][0], pf[1][nt][1]);
-              mma(d, af, pf[0][nt][0], pf[0][nt][1]);
+#pragma unroll
+              for (int term = kTerms - 1; term >= 0; --term) {
+                mma(d, af[0], pb[term][0][np][0], pb[term][0][np][1]);
+                mma(d, af[1], pb[term][1][np][0], pb[term][1][np][1]);
+              }
 #pragma unroll
               for (int j = 0; j < 4; ++j) acc[j] += d[j];
             }
@@ -529,16 +561,22 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 
         x += __shfl_xor_sync(~0u, x, 4);
         x += __shfl_xor_sync(~0u, x, 8);
         x += __shfl_xor_sync(~0u, x, 16);
-        const int r = nt * 8 + 2 * c + j;
-        if (g == 0) {
+        const int r = kBoth ? (2 * c + j) & 3 : nt * 8 + 2 * c + j;
+        if (g == 0 && (!kBoth || c < 2)) {
           s_stat[(warp * kRows + r) * 2] = m[nt][j] == -INFINITY ? -INFINITY : base[nt][j];
           s_stat[(warp * kRows + r) * 2 + 1] = x;
         }
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          float* dst = smem + (warp * kRows + r) * D + g * (D / 8) + 2 * i;
-          *reinterpret_cast<float2*>(dst) = make_float2(o[i][nt][j], o[i][nt][j + 2]);
-        }
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int up = 0; up < 2; ++up) {
+            float* dst = smem + (warp * kRows + r) * D + g * (D / 8) + 4 * i + 2 * up;
+            if constexpr (kBoth)
+              dst[c >> 1] = o[i][0][2 * up + j];
+            else
+              *reinterpret_cast<float2*>(dst) =
+                  make_float2(o[i][2 * nt][2 * up + j], o[i][2 * nt + 1][2 * up + j]);
+          }
       }
     __syncthreads();
     const bool alone = p0 == 0 && p1 == per_seg;
@@ -555,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float b2 = s_stat[(w * kRows + r) * 2];
-        const float f = b2 == -INFINITY ? 0.0f : exp2f(b2 - top);
+        const float f = b2 == -INFINITY ? 0.0f : ex2(b2 - top);
         const float4 v = *reinterpret_cast<const float4*>(smem + (w * kRows + r) * D + ch);
         den += f * s_stat[(w * kRows + r) * 2 + 1];
         sum.x += f * v.x, sum.y += f * v.y, sum.z += f * v.z, sum.w += f * v.w;
@@ -600,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || NT * kTerms > 1) ? 2 : 
           for (int k = cta0; k <= cta1; ++k) {
             const long slot = (2l * k + (k == cta0)) * kRows + r;
             const float2 st = __ldcg(reinterpret_cast<const float2*>(stats + slot * 2));
-            const float f = st.x == -INFINITY ? 0.0f : exp2f(st.x - top);
+            const float f = st.x == -INFINITY ? 0.0f : ex2(st.x - top);
             const float4 v = __ldcg(reinterpret_cast<const float4*>(partial + slot * D + ch));
             den += f * st.y;
             sum.x += f * v.x, sum.y += f * v.y, sum.z += f * v.z, sum.w += f * v.w;
@@ -628,7 +666,7 @@ cudaError_t launch_plan(const AttnArgs& a, int row_tile, bool whole, int n_count
                     reinterpret_cast<SeqInfo*>(w + L.info), reinterpret_cast<long*>(w + L.starts));
 }
 
-template <typename T, int D, int NT, int kTerms>
+template <typename T, int D, int kRows, int kTerms>
 cudaError_t launch_split(const AttnArgs& a, void* ws, const AttnLayout& L, cudaStream_t st) {
   auto* status = reinterpret_cast<unsigned*>(static_cast<char*>(ws) + L.status);
   auto* counters = reinterpret_cast<int*>(static_cast<char*>(ws) + L.counters);
@@ -636,16 +674,16 @@ cudaError_t launch_split(const AttnArgs& a, void* ws, const AttnLayout& L, cudaS
   auto* starts = reinterpret_cast<long*>(static_cast<char*>(ws) + L.starts);
   auto* stats = reinterpret_cast<float*>(static_cast<char*>(ws) + L.stats);
   auto* partial = reinterpret_cast<float*>(static_cast<char*>(ws) + L.partial);
-  const int grid = a.sms * ((D == 256 || NT * kTerms > 1) ? 2 : 4);
-  cudaError_t e = launch_plan(a, 8 * NT, false, grid, ws, L, st);
+  const int grid = a.sms * ctas_per_sm<D, kRows, kTerms>();
+  cudaError_t e = launch_plan(a, kRows, false, grid, ws, L, st);
   if (e != cudaSuccess) return e;
-  constexpr int smem = split_smem<D, NT>();
+  constexpr int smem = split_smem<D, kRows>();
   static std::atomic<unsigned long long> done{0};
-  e = opt_in_smem(reinterpret_cast<const void*>(&attn_split_kernel<T, D, NT, kTerms>), smem, done);
+  e = opt_in_smem(reinterpret_cast<const void*>(&attn_split_kernel<T, D, kRows, kTerms>), smem, done);
   if (e != cudaSuccess) return e;
   int log2 = 0;
   while ((kTile << log2) < a.page_size) ++log2;
-  return launch_pdl(&attn_split_kernel<T, D, NT, kTerms>, dim3(grid), dim3(kThreads), smem, st, a,
+  return launch_pdl(&attn_split_kernel<T, D, kRows, kTerms>, dim3(grid), dim3(kThreads), smem, st, a,
                     status, counters, const_cast<const SeqInfo*>(info),
                     const_cast<const long*>(starts), stats, partial, log2);
 }
@@ -653,10 +691,13 @@ cudaError_t launch_split(const AttnArgs& a, void* ws, const AttnLayout& L, cudaS
 template <int D>
 cudaError_t launch_dim(bool bf16, const AttnArgs& a, void* ws, const AttnLayout& L,
                        cudaStream_t st) {
-  if (!bf16) return launch_split<float, D, 1, 2>(a, ws, L, st);
-  if (static_cast<long>(a.max_q) * (a.heads / a.kv_heads) <= 8)
-    return launch_split<__nv_bfloat16, D, 1, 1>(a, ws, L, st);
-  return launch_split<__nv_bfloat16, D, 2, 1>(a, ws, L, st);
+  const long rows = static_cast<long>(a.max_q) * (a.heads / a.kv_heads);
+  if (!bf16)
+    return rows <= 4 ? launch_split<float, D, 4, 2>(a, ws, L, st)
+                     : launch_split<float, D, 8, 2>(a, ws, L, st);
+  return rows <= 4   ? launch_split<__nv_bfloat16, D, 4, 1>(a, ws, L, st)
+         : rows <= 8 ? launch_split<__nv_bfloat16, D, 8, 1>(a, ws, L, st)
+                     : launch_split<__nv_bfloat16, D, 16, 1>(a, ws, L, st);
 }
 
 }  // namespace
