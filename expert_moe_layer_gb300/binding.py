@@ -186,6 +186,9 @@ def lib(build: bool = True, debug: bool | None = None) -> ctypes.CDLL:
     """Load libmoe.so, or libmoe_debug.so inside ``debug_library()`` (or with
     debug=True), building it in place first if missing or stale."""
     dbg = _use_debug if debug is None else debug
+    L = _libs.get(dbg)
+    if L is not None:
+        return L
     with _lock:
         L = _libs.get(dbg)
         if L is None:
@@ -236,7 +239,7 @@ def _p(t):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -373,20 +376,35 @@ def moe_forward_timed(cfg, T, x, router_w, router_bias, w13, w2, shared_w13, sha
 
 
 # ------------------------------------------------------------------ attention
-def _typed(name, t, dtype, shape):
+def _dtypes():
+    """torch's types under the names used here (torch is imported on first use)."""
+    import torch
+    return {"f32": torch.float32, "bf16": torch.bfloat16, "i32": torch.int32,
+            "i64": torch.int64, "u8": torch.uint8, MOE_F32: torch.float32,
+            MOE_BF16: torch.bfloat16}
+
+
+_DT: dict = {}
+
+
+def _dt(key):
+    if not _DT:
+        _DT.update(_dtypes())
+    return _DT[key]
+
+
+def _typed(name, t, key, shape):
     """Device pointer of a contiguous tensor of that type and shape (None
     passes through; a None in the shape is not checked)."""
     if t is None:
         return None
-    if str(t.dtype) != dtype:
-        raise ValueError(f"{name} must be {dtype}; got {t.dtype}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have shape {shape}; got {tuple(t.shape)}")
+    if t.dtype is not _dt(key):
+        raise ValueError(f"{name} must be {_dt(key)}; got {t.dtype}")
+    have = t.shape
+    if have != shape and (len(have) != len(shape) or
+                          any(n is not None and n != m for n, m in zip(shape, have))):
+        raise ValueError(f"{name} must have shape {shape}; got {tuple(have)}")
     return _p(t)
-
-
-def _act(cfg):
-    return "torch.bfloat16" if cfg.act_dtype == MOE_BF16 else "torch.float32"
 
 
 def _rows(name, t, cfg, T, heads):
@@ -394,9 +412,9 @@ def _rows(name, t, cfg, T, heads):
     whose channels are contiguous; tokens and heads may be strided."""
     if t is None:
         return None, 0, 0
-    if str(t.dtype) != _act(cfg):
-        raise ValueError(f"{name} must be {_act(cfg)}; got {t.dtype}")
-    if tuple(t.shape) != (T, heads, cfg.head_dim):
+    if t.dtype is not _dt(cfg.act_dtype):
+        raise ValueError(f"{name} must be {_dt(cfg.act_dtype)}; got {t.dtype}")
+    if t.shape != (T, heads, cfg.head_dim):
         raise ValueError(f"{name} must have shape {(T, heads, cfg.head_dim)}; "
                          f"got {tuple(t.shape)}")
     if not t.is_cuda:
@@ -410,7 +428,8 @@ def _rows(name, t, cfg, T, heads):
 def _cache(cache, cfg):
     """(pointer, pages) of a cache tensor [pages, kv heads, block bytes]."""
     block = cfg.page_size * cfg.head_dim * 9 // 8
-    return _typed("cache", cache, "torch.uint8", (None, cfg.num_kv_heads, block)), cache.shape[0]
+    shape = cache.shape
+    return _typed("cache", cache, "u8", (shape[0], cfg.num_kv_heads, block)), shape[0]
 
 
 def validate_attn_config(cfg: AttnConfig) -> int:
@@ -427,8 +446,8 @@ def kv_attention_workspace_size(cfg, num_seqs, T, max_q_len) -> int:
 
 def moe_rope_table(cfg, n, positions, scaling, table, ws=None, stream=None):
     _check("moe_rope_table", lib().moe_rope_table(
-        ctypes.byref(cfg), n, _typed("positions", positions, "torch.int32", (n,)),
-        ctypes.byref(scaling), _typed("table", table, "torch.float32", (n, cfg.rotary_dim)),
+        ctypes.byref(cfg), n, _typed("positions", positions, "i32", (n,)),
+        ctypes.byref(scaling), _typed("table", table, "f32", (n, cfg.rotary_dim)),
         _p(ws), _nbytes(ws), _stream(stream)))
 
 
@@ -436,9 +455,9 @@ def moe_rope(cfg, T, x, positions, table, out, inverse=False, ws=None, stream=No
     heads = x.shape[1] if x.dim() == 3 else 0
     _check("moe_rope", lib().moe_rope(
         ctypes.byref(cfg), T, heads, *_rows("x", x, cfg, T, heads),
-        _typed("positions", positions, "torch.int32", (T,)),
-        _typed("table", table, "torch.float32", (cfg.rope_positions, cfg.rotary_dim)),
-        int(bool(inverse)), _typed("out", out, _act(cfg), (T, heads, cfg.head_dim)), _p(ws),
+        _typed("positions", positions, "i32", (T,)),
+        _typed("table", table, "f32", (cfg.rope_positions, cfg.rotary_dim)),
+        int(bool(inverse)), _typed("out", out, cfg.act_dtype, (T, heads, cfg.head_dim)), _p(ws),
         _nbytes(ws), _stream(stream)))
 
 
@@ -446,30 +465,31 @@ def moe_kv_append(cfg, T, q, k, v, positions, slots, table, q_out, cache, ws=Non
     _check("moe_kv_append", lib().moe_kv_append(
         ctypes.byref(cfg), T, *_rows("q", q, cfg, T, cfg.num_heads),
         *_rows("k", k, cfg, T, cfg.num_kv_heads), *_rows("v", v, cfg, T, cfg.num_kv_heads),
-        _typed("positions", positions, "torch.int32", (T,)),
-        _typed("slots", slots, "torch.int64", (T,)),
-        _typed("table", table, "torch.float32", (cfg.rope_positions, cfg.rotary_dim)),
-        _typed("q_out", q_out, _act(cfg), (T, cfg.num_heads, cfg.head_dim)),
+        _typed("positions", positions, "i32", (T,)),
+        _typed("slots", slots, "i64", (T,)),
+        _typed("table", table, "f32", (cfg.rope_positions, cfg.rotary_dim)),
+        _typed("q_out", q_out, cfg.act_dtype, (T, cfg.num_heads, cfg.head_dim)),
         *_cache(cache, cfg), _p(ws), _nbytes(ws), _stream(stream)))
 
 
 def moe_kv_read(cfg, N, slots, cache, k_out, v_out, ws=None, stream=None):
     shape = (N, cfg.num_kv_heads, cfg.head_dim)
     _check("moe_kv_read", lib().moe_kv_read(
-        ctypes.byref(cfg), N, _typed("slots", slots, "torch.int64", (N,)), *_cache(cache, cfg),
-        _typed("k_out", k_out, _act(cfg), shape), _typed("v_out", v_out, _act(cfg), shape),
+        ctypes.byref(cfg), N, _typed("slots", slots, "i64", (N,)), *_cache(cache, cfg),
+        _typed("k_out", k_out, cfg.act_dtype, shape), _typed("v_out", v_out, cfg.act_dtype, shape),
         _p(ws), _nbytes(ws), _stream(stream)))
 
 
 def moe_kv_attention(cfg, num_seqs, T, max_q_len, q, q_offsets, seq_lens, page_table, cache, out,
                      lse, ws, stream=None):
+    max_pages = page_table.shape[-1]
     _check("moe_kv_attention", lib().moe_kv_attention(
         ctypes.byref(cfg), num_seqs, T, max_q_len, *_rows("q", q, cfg, T, cfg.num_heads),
-        _typed("q_offsets", q_offsets, "torch.int32", (num_seqs + 1,)),
-        _typed("seq_lens", seq_lens, "torch.int32", (num_seqs,)),
-        _typed("page_table", page_table, "torch.int32", (num_seqs, None)), page_table.shape[1],
-        *_cache(cache, cfg), _typed("out", out, _act(cfg), (T, cfg.num_heads, cfg.head_dim)),
-        _typed("lse", lse, "torch.float32", (T, cfg.num_heads)), _p(ws), _nbytes(ws),
+        _typed("q_offsets", q_offsets, "i32", (num_seqs + 1,)),
+        _typed("seq_lens", seq_lens, "i32", (num_seqs,)),
+        _typed("page_table", page_table, "i32", (num_seqs, max_pages)), max_pages,
+        *_cache(cache, cfg), _typed("out", out, cfg.act_dtype, (T, cfg.num_heads, cfg.head_dim)),
+        _typed("lse", lse, "f32", (T, cfg.num_heads)), _p(ws), _nbytes(ws),
         _stream(stream)))
 
 

@@ -42,40 +42,37 @@ constexpr int kSetup = 14;
 constexpr int kStages = 4;  // tiles a warp has in shared memory or on the way
 constexpr int kMaxCtasPerSm = 4;
 constexpr int kPlanThreads = 1024;
+constexpr int kInlineSeqs = 256;  // up to so many requests are planned by every CTA
 
-__device__ __forceinline__ long shfl_up(long v, int d) { return __shfl_up_sync(~0u, v, d); }
-
-// Clears the status and the counters, checks every request and sums up the
-// work list: starts[b] is the first tile of request b in it (with `whole`, the
-// first segment: a row tile of a kv head is one unit then).
-__global__ void __launch_bounds__(kPlanThreads)
-    attn_plan_kernel(AttnArgs a, int row_tile, bool whole, unsigned* status, int* counters, int n_counters,
-                     SeqInfo* info, long* starts) {
-  pdl_enter();
-  if (threadIdx.x == 0) *status = 0;
-  for (int i = threadIdx.x; i < n_counters; i += kPlanThreads) counters[i] = 0;
-  __syncthreads();
-  __shared__ long warp_sum[32];
+// Checks every request and sums up the work list with a block of N threads:
+// starts[b] is the first tile of request b in it (with `whole`, the first
+// segment: a row tile of a kv head is one unit then). Each thread gets the
+// MOE_DEV_* flags of the requests it checked.
+template <int N>
+__device__ __forceinline__ unsigned sum_work(const AttnArgs& a, int row_tile, bool whole,
+                                             SeqInfo* info, long* starts) {
+  __shared__ long warp_sum[N / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = a.heads / a.kv_heads;
   const long cap = static_cast<long>(a.max_pages) * a.page_size;
+  unsigned flags = 0;
   long base = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+  for (int b0 = 0; b0 < a.B; b0 += N) {
     const int b = b0 + threadIdx.x;
     long tiles = 0;
     if (b < a.B) {
       SeqInfo s = {0, 0, 0, 0};
       const int q0 = a.q_offsets ? a.q_offsets[b] : b;
       const int q1 = a.q_offsets ? a.q_offsets[b + 1] : b + 1;
+      const int n = a.seq_lens[b];
       if (q0 < 0 || q1 < q0 || q1 > a.T || q1 - q0 > a.max_q) {
-        atomicOr(status, MOE_DEV_BAD_SEGMENT);
+        flags |= MOE_DEV_BAD_SEGMENT;
       } else {
         s.q0 = q0;
         s.q_len = q1 - q0;
       }
-      const int n = a.seq_lens[b];
       s.len = static_cast<int>(n < 0 ? 0 : n > cap ? cap : n);
-      if (s.len != n) atomicOr(status, MOE_DEV_BAD_PAGE);
+      if (s.len != n) flags |= MOE_DEV_BAD_PAGE;
       if (a.window > 0) {
         const long lo = static_cast<long>(s.len) - s.q_len - a.window + 1;
         s.first_tile = lo > 0 ? static_cast<int>(lo / kTile) : 0;
@@ -88,13 +85,14 @@ __global__ void __launch_bounds__(kPlanThreads)
     long sum = tiles;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
-      const long v = shfl_up(sum, d);
+      const long v = __shfl_up_sync(~0u, sum, d);
       if (lane >= d) sum += v;
     }
     if (lane == 31) warp_sum[warp] = sum;
     __syncthreads();
     long before = 0, all = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
+#pragma unroll
+    for (int w = 0; w < N / 32; ++w) {
       if (w < warp) before += warp_sum[w];
       all += warp_sum[w];
     }
@@ -103,9 +101,27 @@ __global__ void __launch_bounds__(kPlanThreads)
     __syncthreads();
   }
   if (threadIdx.x == 0) starts[a.B] = base;
+  return flags;
 }
 
-// Range of the tile list that CTA c of n takes: [first(c), first(c + 1)).
+// Clears the status and the counters, and with `info` sums up the work. (For
+// few requests every CTA of the split kernel does that itself, sooner than a
+// kernel before it could hand it over; its first loads then overlap this one.)
+__global__ void __launch_bounds__(kPlanThreads)
+    attn_plan_kernel(AttnArgs a, int row_tile, bool whole, unsigned* status, int* counters,
+                     int n_counters, SeqInfo* info, long* starts) {
+  pdl_enter();
+  if (threadIdx.x == 0) *status = 0;
+  for (int i = threadIdx.x; i < n_counters; i += blockDim.x) counters[i] = 0;
+  if (!info) return;
+  __syncthreads();
+  const unsigned flags = sum_work<kPlanThreads>(a, row_tile, whole, info, starts);
+  if (flags) atomicOr(status, flags);
+}
+
+// Tiles per CTA: CTA c takes [c * per, (c + 1) * per) of the list, but a cut
+// that falls into a segment's first kSetup entries, which stand for no tiles,
+// moves to its beginning.
 __device__ __forceinline__ long range_len(long total, int ctas) {
   const long per = (total + ctas - 1) / ctas;
   return per < kMinTiles ? kMinTiles : per;
@@ -200,11 +216,13 @@ __device__ __forceinline__ void load_tile(TileRegs<D>& t, const uint8_t* stage, 
 template <int D, int kRows>
 __host__ __device__ constexpr int split_smem() {
   constexpr int stages = kWarps * kStages * TileBytes<D>::kBytes, sums = kWarps * kRows * D * 4;
-  return (stages > sums ? stages : sums) + kWarps * kRows * 8;
+  constexpr int join = kAttnMaxSms * (kRows == 16 ? 2 : kMaxCtasPerSm) * kRows * 8;
+  constexpr int most = stages > sums ? stages : sums;
+  return (most > join ? most : join) + kWarps * kRows * 8;
 }
 template <int D, int kRows, int kTerms>
 __host__ __device__ constexpr int ctas_per_sm() {
-  return D == 256 || kRows == 16 || kTerms == 2 ? 2 : 4;
+  return D == 256 || kRows == 16 || kTerms == 2 ? 2 : kMaxCtasPerSm;
 }
 
 // kRows is 4, 8 or 16. The matrix instruction pairs neighbouring k indices in
@@ -218,10 +236,10 @@ __host__ __device__ constexpr int ctas_per_sm() {
 // layers): q and P are a sum of two f16 each, 22 bits, and each tile's product
 // with V is added to the running sum by fp32 additions, because the matrix
 // unit's own accumulation truncates.
-template <typename T, int D, int kRows, int kTerms>
+template <typename T, int D, int kRows, int kTerms, bool kInline>
 __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
-    attn_split_kernel(AttnArgs a, unsigned* status, int* counters, const SeqInfo* info,
-                      const long* starts, float* stats, float* partial, int tiles_per_page_log2) {
+    attn_split_kernel(AttnArgs a, unsigned* status, int* counters, const SeqInfo* info_in,
+                      const long* starts_in, float* stats, float* partial, int tiles_per_page_log2) {
   constexpr bool kBoth = kRows == 4;             // columns 4-7 repeat rows 0-3
   constexpr int NT = kBoth ? 1 : kRows / 8;      // column tiles of the scores
   constexpr int NP = kBoth ? 1 : 2 * NT;         // column tiles of the sums
@@ -231,7 +249,20 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
   extern __shared__ __align__(16) float smem[];
   float* s_stat = smem + split_smem<D, kRows>() / 4 - kWarps * kRows * 2;
   __shared__ int s_last;
-  pdl_enter();
+  const SeqInfo* info = info_in;
+  const long* starts = starts_in;
+  bool entered = !kInline;
+  unsigned flags = 0;
+  if constexpr (kInline) {
+    __shared__ SeqInfo s_info[kInlineSeqs];
+    __shared__ long s_starts[kInlineSeqs + 1];
+    flags = sum_work<kThreads>(a, kRows, false, s_info, s_starts);
+    __syncthreads();
+    info = s_info;
+    starts = s_starts;
+  } else {
+    pdl_enter();
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
   const int group = a.heads / a.kv_heads;
@@ -240,7 +271,6 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
   const long per = range_len(total, gridDim.x);
   long at = blockIdx.x * per;
   const long end = min(total, at + per);
-  if (at >= end) return;
   // the request of the first tile: the last b with starts[b] <= at (requests
   // without query rows have no tiles and share their start with the next)
   int b = 0;
@@ -259,14 +289,16 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
     const int rows = sq.q_len * group;
     const int per_seg = kSetup + max(0, (sq.len + kTile - 1) / kTile - sq.first_tile);
     const long seg = (at - starts[b]) / per_seg;
+    const long seg_start = starts[b] + seg * per_seg, seg_end = seg_start + per_seg;
+    if (at - seg_start < kSetup) at = seg_start;
+    if (end - seg_start < kSetup) break;  // a later CTA takes all of it
     // this CTA's part [p0, p1) of the segment's list, and of its tiles
-    const int p0 = static_cast<int>((at - starts[b]) - seg * per_seg);
-    const int p1 = static_cast<int>(min(static_cast<long>(per_seg), p0 + (end - at)));
-    const int t0 = max(0, p0 - kSetup), t1 = max(0, p1 - kSetup);
+    const int p0 = static_cast<int>(at - seg_start);
+    const int p1 = static_cast<int>(min(seg_end, end) - seg_start);
+    const int t0 = max(0, p0 - kSetup), t1 = p1 - kSetup;
     const int row_tile = static_cast<int>(seg / a.kv_heads);
     const int kvh = static_cast<int>(seg - static_cast<long>(row_tile) * a.kv_heads);
     const int row0 = row_tile * kRows;
-    const long seg_start = at - p0, seg_end = seg_start + per_seg;
 
     // this lane's score columns are rows nt*8 + 2c and + 1: their token limits
     int last[NT][2], first[NT][2];
@@ -386,6 +418,13 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
       int ids[kStages - 1];
 #pragma unroll
       for (int i = 0; i < kStages - 1; ++i) ids[i] = page_of(t + i * kWarps);
+      if (!entered) {
+        // status and counters are clear from here on; everything else that is
+        // read was written before the kernel that clears them
+        pdl_enter();
+        if (blockIdx.x == 0 && flags) atomicOr(status, flags);
+        entered = true;
+      }
 #pragma unroll
       for (int i = 0; i < kStages - 1; ++i) copy(t + i * kWarps, i, ids[i]);
     }
@@ -616,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
       }
     }
     if (!alone) {
-      const int cta0 = static_cast<int>(seg_start / per);
+      const int cta0 = static_cast<int>((seg_start + kSetup - 1) / per);
       const int cta1 = static_cast<int>((seg_end - 1) / per);
       __threadfence();
       __syncthreads();
@@ -625,67 +664,100 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
       __syncthreads();
       if (s_last) {
         __threadfence();
+        // every piece's statistics into shared memory, then its weight
+        const int n = cta1 - cta0 + 1;
+        float* w = smem;                 // [kRows][n] bases, then weights
+        float* dens = smem + kRows * n;  // [kRows][n]
+        for (int i = threadIdx.x; i < kRows * n; i += kThreads) {
+          const int r = i / n, k = i - r * n;
+          const long slot = (2l * (cta0 + k) + (k == 0)) * kRows + r;
+          const float2 st = __ldcg(reinterpret_cast<const float2*>(stats + slot * 2));
+          w[i] = st.x;
+          dens[i] = st.y;
+        }
+        __syncthreads();
+        for (int r = warp; r < kRows; r += kWarps) {
+          float top = -INFINITY, den = 0.0f;
+          for (int k = lane; k < n; k += 32) top = fmaxf(top, w[r * n + k]);
+#pragma unroll
+          for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+          for (int k = lane; k < n; k += 32) {
+            const float b2 = w[r * n + k];
+            const float f = b2 == -INFINITY ? 0.0f : ex2(b2 - top);
+            w[r * n + k] = f;
+            den += f * dens[r * n + k];
+          }
+#pragma unroll
+          for (int d = 16; d > 0; d /= 2) den += __shfl_xor_sync(~0u, den, d);
+          __syncwarp();
+          if (lane == 0) s_stat[2 * r] = top, s_stat[2 * r + 1] = den;
+        }
+        __syncthreads();
         for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
           const int r = i / (D / 4), ch = (i % (D / 4)) * 4;
           if (row0 + r >= rows) continue;
-          float top = -INFINITY;
-#pragma unroll 8
-          for (int k = cta0; k <= cta1; ++k)
-            top = fmaxf(top, __ldcg(stats + ((2l * k + (k == cta0)) * kRows + r) * 2));
           float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          float den = 0.0f;
-#pragma unroll 8
-          for (int k = cta0; k <= cta1; ++k) {
-            const long slot = (2l * k + (k == cta0)) * kRows + r;
-            const float2 st = __ldcg(reinterpret_cast<const float2*>(stats + slot * 2));
-            const float f = st.x == -INFINITY ? 0.0f : ex2(st.x - top);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(partial + slot * D + ch));
-            den += f * st.y;
+          const float* src = partial + (2l * cta0 * kRows + r) * D + ch;
+#pragma unroll 16
+          for (int k = 0; k < n; ++k) {
+            const long slot = 2l * k + (k == 0);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + slot * kRows * D));
+            const float f = w[r * n + k];
             sum.x += f * v.x, sum.y += f * v.y, sum.z += f * v.z, sum.w += f * v.w;
           }
           const int tok = (row0 + r) / group, h = kvh * group + (row0 + r) - tok * group;
           const long at_row = static_cast<long>(sq.q0 + tok) * a.heads + h;
-          const float f = out_factor(den, a.v_scale);
+          const float f = out_factor(s_stat[2 * r + 1], a.v_scale);
           store4(static_cast<T*>(a.out) + at_row * D + ch,
                  make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f));
-          if (a.lse && ch == 0) a.lse[at_row] = log_sum(top, den);
+          if (a.lse && ch == 0) a.lse[at_row] = log_sum(s_stat[2 * r], s_stat[2 * r + 1]);
         }
       }
     }
     __syncthreads();
-    at += p1 - p0;
+    at = seg_start + p1;
+  }
+  if (!entered) {
+    pdl_enter();
+    if (blockIdx.x == 0 && flags) atomicOr(status, flags);
   }
 }
 
-cudaError_t launch_plan(const AttnArgs& a, int row_tile, bool whole, int n_counters, void* ws,
-                        const AttnLayout& L, cudaStream_t st) {
+cudaError_t launch_plan(const AttnArgs& a, int row_tile, bool whole, int n_counters, bool sum,
+                        void* ws, const AttnLayout& L, cudaStream_t st) {
   char* w = static_cast<char*>(ws);
   return launch_pdl(&attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a, row_tile, whole,
                     reinterpret_cast<unsigned*>(w + L.status),
                     reinterpret_cast<int*>(w + L.counters), n_counters,
-                    reinterpret_cast<SeqInfo*>(w + L.info), reinterpret_cast<long*>(w + L.starts));
+                    sum ? reinterpret_cast<SeqInfo*>(w + L.info) : nullptr,
+                    reinterpret_cast<long*>(w + L.starts));
 }
 
-template <typename T, int D, int kRows, int kTerms>
-cudaError_t launch_split(const AttnArgs& a, void* ws, const AttnLayout& L, cudaStream_t st) {
-  auto* status = reinterpret_cast<unsigned*>(static_cast<char*>(ws) + L.status);
-  auto* counters = reinterpret_cast<int*>(static_cast<char*>(ws) + L.counters);
-  auto* info = reinterpret_cast<SeqInfo*>(static_cast<char*>(ws) + L.info);
-  auto* starts = reinterpret_cast<long*>(static_cast<char*>(ws) + L.starts);
-  auto* stats = reinterpret_cast<float*>(static_cast<char*>(ws) + L.stats);
-  auto* partial = reinterpret_cast<float*>(static_cast<char*>(ws) + L.partial);
+template <typename T, int D, int kRows, int kTerms, bool kInline>
+cudaError_t launch_split_as(const AttnArgs& a, void* ws, const AttnLayout& L, cudaStream_t st) {
+  auto* kern = &attn_split_kernel<T, D, kRows, kTerms, kInline>;
   const int grid = a.sms * ctas_per_sm<D, kRows, kTerms>();
-  cudaError_t e = launch_plan(a, kRows, false, grid, ws, L, st);
+  cudaError_t e = launch_plan(a, kRows, false, grid, !kInline, ws, L, st);
   if (e != cudaSuccess) return e;
   constexpr int smem = split_smem<D, kRows>();
   static std::atomic<unsigned long long> done{0};
-  e = opt_in_smem(reinterpret_cast<const void*>(&attn_split_kernel<T, D, kRows, kTerms>), smem, done);
+  e = opt_in_smem(reinterpret_cast<const void*>(kern), smem, done);
   if (e != cudaSuccess) return e;
   int log2 = 0;
   while ((kTile << log2) < a.page_size) ++log2;
-  return launch_pdl(&attn_split_kernel<T, D, kRows, kTerms>, dim3(grid), dim3(kThreads), smem, st, a,
-                    status, counters, const_cast<const SeqInfo*>(info),
-                    const_cast<const long*>(starts), stats, partial, log2);
+  char* w = static_cast<char*>(ws);
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, a,
+                    reinterpret_cast<unsigned*>(w + L.status),
+                    reinterpret_cast<int*>(w + L.counters),
+                    reinterpret_cast<const SeqInfo*>(w + L.info),
+                    reinterpret_cast<const long*>(w + L.starts),
+                    reinterpret_cast<float*>(w + L.stats), reinterpret_cast<float*>(w + L.partial),
+                    log2);
+}
+template <typename T, int D, int kRows, int kTerms>
+cudaError_t launch_split(const AttnArgs& a, void* ws, const AttnLayout& L, cudaStream_t st) {
+  return a.B <= kInlineSeqs ? launch_split_as<T, D, kRows, kTerms, true>(a, ws, L, st)
+                            : launch_split_as<T, D, kRows, kTerms, false>(a, ws, L, st);
 }
 
 template <int D>
@@ -722,7 +794,7 @@ cudaError_t launch_kv_attention(bool bf16, const AttnArgs& a, void* ws, const At
   // From kPromptRows rows per request the matrix work, not the cache's
   // bandwidth, is the bound: the prompt kernel.
   if (bf16 && a.D <= 128 && static_cast<long>(a.max_q) * (a.heads / a.kv_heads) >= kPromptRows) {
-    const cudaError_t e = launch_plan(a, kPromptTile, true, 1, ws, L, st);
+    const cudaError_t e = launch_plan(a, kPromptTile, true, 1, true, ws, L, st);
     return e != cudaSuccess ? e : launch_prompt(a, ws, L, st);
   }
   switch (a.D) {

@@ -207,6 +207,6 @@ def test_binding_checks_types_shapes_and_devices():
     with pytest.raises(ValueError, match="must have shape"):
         B.moe_kv_append(cfg, 5, q, q, q, pos, pos, None, q, q)
     with pytest.raises(ValueError, match="must be torch.int64"):
-        B._typed("slots", pos, "torch.int64", (4,))
+        B._typed("slots", pos, "i64", (4,))
     with pytest.raises(KeyError):
         B.make_attn_config(8, 8, 128, act_dtype="f16")
