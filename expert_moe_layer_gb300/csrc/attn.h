@@ -29,7 +29,7 @@ struct RopeArgs {
   void* q_out = nullptr;
   uint8_t* cache = nullptr;
   long n_slots = 0;
-  int page_size = 0;
+  int page_shift = 0;  // log2 of the page size
   float k_inv = 1.0f, v_inv = 1.0f;  // 1 / k_scale, 1 / v_scale
   unsigned* status = nullptr;
 };
@@ -37,7 +37,7 @@ struct RopeArgs {
 // Rotation of q into q_out and, with kv_heads > 0, the append of k and v.
 cudaError_t launch_rope(bool bf16, const RopeArgs& a, cudaStream_t st);
 
-constexpr int kMaxPairs = 256;
+constexpr int kMaxPairs = 256;  // a block of the table kernel has as many threads
 // Turns per position of each pair, as 64-bit fractions of a turn.
 struct RopeTurns {
   unsigned long long f[kMaxPairs];
@@ -46,7 +46,7 @@ cudaError_t launch_rope_table(const RopeTurns& turns, int pairs, float gain, int
                               const int32_t* positions, float* table, cudaStream_t st);
 
 cudaError_t launch_kv_read(bool bf16, int N, const int64_t* slots, const uint8_t* cache,
-                           long n_slots, int kv_heads, int D, int page_size, float k_scale,
+                           long n_slots, int kv_heads, int D, int page_shift, float k_scale,
                            float v_scale, void* k_out, void* v_out, unsigned* status,
                            cudaStream_t st);
 

@@ -26,6 +26,11 @@ int cuda_ok(cudaError_t e) { return e == cudaSuccess ? MOE_OK : fail_cuda(static
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 int ebytes(const moe_attn_config* c) { return c->act_dtype == MOE_BF16 ? 2 : 4; }
+int page_shift(const moe_attn_config* c) {
+  int n = 0;
+  while ((1 << n) < c->page_size) ++n;
+  return n;
+}
 bool scale_ok(float s) { return std::isfinite(s) && s > 0.0f && std::isfinite(1.0f / s); }
 
 // What the rotary calls use: everything but the head counts.
@@ -238,7 +243,7 @@ int moe_kv_append(const moe_attn_config* cfg, int T, const void* q, int64_t q_to
   a.table_rows = cfg->rope_positions;
   a.interleaved = cfg->rope_layout == MOE_ROPE_INTERLEAVED;
   a.q_out = q_out, a.cache = static_cast<uint8_t*>(cache);
-  a.page_size = cfg->page_size, a.n_slots = static_cast<long>(num_pages) * cfg->page_size;
+  a.page_shift = page_shift(cfg), a.n_slots = static_cast<long>(num_pages) * cfg->page_size;
   a.k_inv = 1.0f / cfg->k_scale, a.v_inv = 1.0f / cfg->v_scale;
   return cuda_ok(launch_rope(cfg->act_dtype == MOE_BF16, a, st));
 }
@@ -260,7 +265,7 @@ int moe_kv_read(const moe_attn_config* cfg, int N, const int64_t* slots, const v
   return cuda_ok(launch_kv_read(cfg->act_dtype == MOE_BF16, N, slots,
                                 static_cast<const uint8_t*>(cache),
                                 static_cast<long>(num_pages) * cfg->page_size, cfg->num_kv_heads,
-                                cfg->head_dim, cfg->page_size, cfg->k_scale, cfg->v_scale, k_out,
+                                cfg->head_dim, page_shift(cfg), cfg->k_scale, cfg->v_scale, k_out,
                                 v_out, status, st));
 }
 

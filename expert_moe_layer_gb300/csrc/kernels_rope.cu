@@ -1,12 +1,14 @@
 // Rotary positions, the append to the 4-bit paged cache, and reading it back.
 //
 // All of it is elementwise over rows, so memory bounds it at prompt sizes and
-// launch latency at decode sizes. A thread takes 32 channels of a head (two
-// groups of 16): the two halves of 16 pairs for the half layout, 32 neighbours
-// for the interleaved one. Either way these are the pairs 16u .. 16u + 15, so
-// their cosines and sines are loaded once and used for several heads, a key's
-// rotation and its quantisation happen in registers, and a row rotated in
-// place is read and written by one thread only.
+// launch latency at decode sizes. A thread takes two chunks of 16 bytes of a
+// head, half the rotated channels apart: the two sides of the half layout's
+// pairs, or neighbouring pairs of the interleaved one. Neighbouring lanes hold
+// neighbouring chunks, so that every access covers whole sectors. (With 32
+// bytes per lane and chunk, the two 16-byte accesses to a sector went out
+// apart: 38.6 us for 8192 x 40 heads of 128 instead of @ROPE@.) The cosines and
+// sines are loaded once and used for several heads; a row rotated in place is
+// read and written by one thread only.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -40,42 +42,45 @@ __device__ __forceinline__ __nv_bfloat16 from_f(float v) {
   return __float2bfloat16_rn(v);
 }
 
-// 16 consecutive elements, 16-byte aligned.
-__device__ __forceinline__ void load16(const float* p, float (&x)[16]) {
+// One 16-byte chunk: 8 bf16 or 4 fp32 elements.
+__device__ __forceinline__ void load_chunk(const float* p, float (&x)[4]) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+}
+__device__ __forceinline__ void load_chunk(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 v = reinterpret_cast<const float4*>(p)[i];
-    x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+  for (int j = 0; j < 4; ++j) {
+    x[2 * j] = __uint_as_float(w[j] << 16);
+    x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&x)[16]) {
+__device__ __forceinline__ void store_chunk(float* p, const float (&x)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void store_chunk(__nv_bfloat16* p, const float (&x)[8]) {
+  uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 v = reinterpret_cast<const uint4*>(p)[i];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-      x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+    w[j] = *reinterpret_cast<const uint32_t*>(&b);
   }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void store16(float* p, const float (&x)[16]) {
+
+// N consecutive floats, aligned to their size or to 16 bytes.
+template <int N>
+__device__ __forceinline__ void load_floats(const float* p, float* x) {
+  if constexpr (N == 2) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    x[0] = v.x, x[1] = v.y;
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    reinterpret_cast<float4*>(p)[i] =
-        make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-}
-__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&x)[16]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(x[8 * i + 2 * j], x[8 * i + 2 * j + 1]);
-      w[j] = *reinterpret_cast<const uint32_t*>(&b);
+    for (int i = 0; i < N / 4; ++i) {
+      const float4 v = reinterpret_cast<const float4*>(p)[i];
+      x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
     }
-    reinterpret_cast<uint4*>(p)[i] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -87,20 +92,44 @@ __device__ __forceinline__ void turn(float a, float b, float c, float s, float& 
   v = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
 }
 
-// Where a token's group of 16 channels is stored.
-template <typename T>
-__device__ __forceinline__ void store_group(const RopeArgs& a, bool value, long slot, int head,
-                                            int group, float (&x)[16]) {
-  const KvBlock blk = kv_block(a.page_size, a.D);
-  const long page = slot / a.page_size;
-  const int row = static_cast<int>(slot - page * a.page_size);
-  uint8_t* base = a.cache + (page * a.kv_heads + head) * static_cast<long>(blk.bytes);
-  uint32_t codes[2];
-  const uint32_t s8 = kv_store_group(x, value ? a.v_inv : a.k_inv, codes);
-  *reinterpret_cast<uint2*>(base + (value ? blk.v_code : 0u) + row * (a.D / 2) + group * 8) =
-      make_uint2(codes[0], codes[1]);
-  base[(value ? blk.v_scale : blk.k_scale) + row * (a.D / kKvGroup) + group] =
-      static_cast<uint8_t>(s8);
+// The (page, kv head) block and row of a slot.
+struct Place {
+  uint8_t* block;  // of kv head 0
+  int row;
+};
+__device__ __forceinline__ Place place_of(const RopeArgs& a, long slot) {
+  const long page = slot >> a.page_shift;
+  return {a.cache + page * a.kv_heads * static_cast<long>(kv_block(1 << a.page_shift, a.D).bytes),
+          static_cast<int>(slot) & ((1 << a.page_shift) - 1)};
+}
+// Stores V channels from `ch`; the 16 / V neighbouring lanes of the group's
+// channels do the same together.
+template <int V>
+__device__ __forceinline__ void store_codes(const RopeArgs& a, bool value, Place at, int head,
+                                            int ch, const float (&x)[V], unsigned lanes) {
+  const KvBlock blk = kv_block(1 << a.page_shift, a.D);
+  uint8_t* base = at.block + head * static_cast<long>(blk.bytes);
+  float y[V], top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float t = __fmul_rn(x[i], value ? a.v_inv : a.k_inv);
+    y[i] = t == t ? t : 0.0f;
+    top = fmaxf(top, fabsf(y[i]));
+  }
+#pragma unroll
+  for (int d = 1; d < kKvGroup / V; d *= 2) top = fmaxf(top, __shfl_xor_sync(lanes, top, d));
+  uint32_t codes[(V + 7) / 8];
+  const uint32_t s8 = kv_codes<V>(y, top, codes);
+  uint8_t* dst = base + (value ? blk.v_code : 0u) + at.row * (a.D / 2) + ch / 2;
+  if constexpr (V == 16)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(codes[0], codes[1]);
+  else if constexpr (V == 8)
+    *reinterpret_cast<uint32_t*>(dst) = codes[0];
+  else
+    *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(codes[0]);
+  if (ch % kKvGroup == 0)
+    base[(value ? blk.v_scale : blk.k_scale) + at.row * (a.D / kKvGroup) + ch / kKvGroup] =
+        static_cast<uint8_t>(s8);
 }
 
 // A chunk is up to `hb` heads of q, then of k, then of v, of one token.
@@ -138,63 +167,74 @@ __device__ __forceinline__ long slot_of(const RopeArgs& a, int t) {
 template <typename T, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int hb, int cq, int ck,
                                                         unsigned total) {
+  constexpr int V = 16 / sizeof(T);     // elements of a chunk
+  constexpr int kSharers = kKvGroup / V;  // lanes that share a scale
   pdl_enter();
   const unsigned idx = blockIdx.x * kThreads + threadIdx.x;
   if (idx >= total) return;
-  const unsigned units = a.D / 32;
+  const unsigned units = a.D / (2 * V);
   const int u = static_cast<int>(idx % units);
   const Chunk c = chunk_of(a, idx / units, hb, cq, ck);
   long slot = 0;
   if (c.kind && (slot = slot_of(a, c.t)) < 0) return;
   bool ok = true;
-  const int pairs = a.R / 2;
-  const bool turns = c.kind != 2 && 16 * u < pairs;
-  float cs[16], sn[16];
+  const float* row = table_row(a, c.t, ok);
+  if (!ok) return;
+  const int pairs = a.R / 2, turned = pairs / V;  // units that rotate
+  const bool turns = c.kind != 2 && u < turned;
+  // first channels of the two chunks
+  int c0 = V * u, c1 = a.D / 2 + V * u;
   if (c.kind != 2) {
-    const float* row = table_row(a, c.t, ok);
-    if (!ok) return;
-    if (turns) {
-      load16(row + 16 * u, cs);
-      load16(row + pairs + 16 * u, sn);
-      if (a.inverse)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sn[i] = -sn[i];
-    }
-  } else if (a.R > 0) {  // a token with a bad position is not stored at all
-    table_row(a, c.t, ok);
-    if (!ok) return;
+    c0 = turns ? V * u : a.R + V * (u - turned);
+    c1 = c0 + (turns ? pairs : (a.D - a.R) / 2);
   }
-  // first channels of the two groups
-  int c0 = 32 * u, c1 = 32 * u + 16;
-  if (!kInterleaved && turns) c0 = 16 * u, c1 = pairs + 16 * u;
+  float cs[V], sn[V];
+  if (turns) {
+    if (kInterleaved) {
+      load_floats<V / 2>(row + c0 / 2, cs);
+      load_floats<V / 2>(row + c1 / 2, cs + V / 2);
+      load_floats<V / 2>(row + pairs + c0 / 2, sn);
+      load_floats<V / 2>(row + pairs + c1 / 2, sn + V / 2);
+    } else {
+      load_floats<V>(row + c0, cs);
+      load_floats<V>(row + pairs + c0, sn);
+    }
+    if (a.inverse)
+#pragma unroll
+      for (int i = 0; i < V; ++i) sn[i] = -sn[i];
+  }
   const Rows rows = c.kind == 0 ? a.q : c.kind == 1 ? a.k : a.v;
   const T* src = static_cast<const T*>(rows.p) + c.t * rows.token;
-#pragma unroll 2
+  Place at = {nullptr, 0};
+  if (c.kind) at = place_of(a, slot);
+  const int lane = threadIdx.x & 31;
+  const unsigned lanes = ((1u << kSharers) - 1u) << (lane & ~(kSharers - 1));
+#pragma unroll 4
   for (int h = c.h0; h < c.h1; ++h) {
-    float x[16], y[16];
-    load16(src + h * rows.head + c0, x);
-    load16(src + h * rows.head + c1, y);
+    float x[V], y[V];
+    load_chunk(src + h * rows.head + c0, x);
+    load_chunk(src + h * rows.head + c1, y);
     if (turns) {
       if (kInterleaved) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < V / 2; ++i) {
           turn(x[2 * i], x[2 * i + 1], cs[i], sn[i], x[2 * i], x[2 * i + 1]);
-          turn(y[2 * i], y[2 * i + 1], cs[8 + i], sn[8 + i], y[2 * i], y[2 * i + 1]);
+          turn(y[2 * i], y[2 * i + 1], cs[V / 2 + i], sn[V / 2 + i], y[2 * i], y[2 * i + 1]);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) turn(x[i], y[i], cs[i], sn[i], x[i], y[i]);
+        for (int i = 0; i < V; ++i) turn(x[i], y[i], cs[i], sn[i], x[i], y[i]);
       }
     }
     if (c.kind == 0) {
       T* dst = static_cast<T*>(a.q_out) + (static_cast<long>(c.t) * a.q_heads + h) * a.D;
-      store16(dst + c0, x);
-      store16(dst + c1, y);
+      store_chunk(dst + c0, x);
+      store_chunk(dst + c1, y);
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = to_f(from_f<T>(x[i])), y[i] = to_f(from_f<T>(y[i]));
-      store_group<T>(a, c.kind == 2, slot, h, c0 / kKvGroup, x);
-      store_group<T>(a, c.kind == 2, slot, h, c1 / kKvGroup, y);
+      for (int i = 0; i < V; ++i) x[i] = to_f(from_f<T>(x[i])), y[i] = to_f(from_f<T>(y[i]));
+      store_codes<V>(a, c.kind == 2, at, h, c0, x, lanes);
+      store_codes<V>(a, c.kind == 2, at, h, c1, y, lanes);
     }
   }
 }
@@ -249,81 +289,86 @@ __global__ void __launch_bounds__(kThreads) rope_any_kernel(RopeArgs a, int hb, 
       }
       x[j] = to_f(from_f<T>(v));
     }
-    store_group<T>(a, c.kind == 2, slot, h, u, x);
+    store_codes<16>(a, c.kind == 2, place_of(a, slot), h, 16 * u, x, 0);
   }
 }
 
 // A frequency is a 64-bit fraction of a turn per position, so the angle's
 // fraction of a turn is an integer product modulo 2^64: exact for every int32
 // position, where an fp32 angle would lose all its bits at far positions and
-// fp64 arithmetic is slow on this part. The fraction's leading 24 bits go
-// through sincospif, the rest corrects its result to first order.
+// fp64 arithmetic is slow on this part. In units of half a turn the fraction's
+// leading 23 bits go through sincospif, the next 23 correct its result to first
+// order; both become floats by an addition to 1.5 * 2^23 (64-bit conversions
+// run at a fraction of the rate: 45 us for 131072 x 64 pairs instead of @TABLE@).
 __global__ void __launch_bounds__(kThreads) rope_table_kernel(RopeTurns turns, int pairs,
                                                               float gain, int n,
                                                               const int32_t* positions,
                                                               float* table, int rows_per_block) {
   pdl_enter();
-  const int lanes = kThreads / pairs;  // rows a block writes at a time (0: more pairs than threads)
-  const int r0 = blockIdx.x * rows_per_block, r1 = min(n, r0 + rows_per_block);
-  const int first = lanes ? threadIdx.x % pairs : threadIdx.x;
-  if (lanes && static_cast<int>(threadIdx.x) >= lanes * pairs) return;
-  for (int i = first; i < pairs; i += lanes ? pairs : kThreads) {
-    const unsigned long long f = turns.f[i];
-    for (int r = r0 + (lanes ? static_cast<int>(threadIdx.x) / pairs : 0); r < r1;
-         r += lanes ? lanes : 1) {
-      const long long pos = positions ? positions[r] : r;
-      const long long t = static_cast<long long>(f * static_cast<unsigned long long>(pos));
-      const float head = __ll2float_rn(t);
-      const float rest = __ll2float_rn(t - __float2ll_rn(head)) * 0x1p-63f * 3.14159265f;
-      float s, c;
-      sincospif(head * 0x1p-63f, &s, &c);
-      float* row = table + static_cast<long>(r) * (2 * pairs);
-      row[i] = gain * fmaf(-s, rest, c);
-      row[pairs + i] = gain * fmaf(c, rest, s);
-    }
+  const int lanes = kThreads / pairs;  // rows a block writes at a time
+  if (static_cast<int>(threadIdx.x) >= lanes * pairs) return;
+  const int i = threadIdx.x % pairs;
+  const unsigned long long f = turns.f[i];
+  const int r1 = min(n, (static_cast<int>(blockIdx.x) + 1) * rows_per_block);
+#pragma unroll 4
+  for (int r = blockIdx.x * rows_per_block + threadIdx.x / pairs; r < r1; r += lanes) {
+    const long long pos = positions ? positions[r] : r;
+    const unsigned long long t = f * static_cast<unsigned long long>(pos);
+    const unsigned long long near = (t + (1ull << 40)) & ~((1ull << 41) - 1);
+    const int lead = static_cast<int>(static_cast<long long>(near) >> 41);      // 23 bits, signed
+    const int rest = static_cast<int>(static_cast<long long>(t - near) >> 18);  // 23 bits, signed
+    const float head = __int_as_float(0x4b400000 + lead) - 0x1.8p23f;
+    const float tail = (__int_as_float(0x4b400000 + rest) - 0x1.8p23f) * (3.14159265f * 0x1p-45f);
+    float s, c;
+    sincospif(head * 0x1p-22f, &s, &c);
+    float* row = table + static_cast<long>(r) * (2 * pairs);
+    row[i] = gain * fmaf(-s, tail, c);
+    row[pairs + i] = gain * fmaf(c, tail, s);
   }
 }
 
-// One thread per (slot, head, group of 16 channels): keys and values.
+// One thread per (slot, head, 16 bytes of output): keys, then values.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     kv_read_kernel(int N, const int64_t* slots, const uint8_t* cache, long n_slots, int kv_heads,
-                   int D, int page_size, float k_scale, float v_scale, T* k_out, T* v_out,
+                   int D, int page_shift, float k_scale, float v_scale, T* k_out, T* v_out,
                    unsigned* status) {
+  constexpr int V = 16 / sizeof(T);
   pdl_enter();
-  const unsigned groups = D / kKvGroup;
+  const unsigned chunks = D / V;
   const unsigned idx = blockIdx.x * kThreads + threadIdx.x;
-  const unsigned g = idx % groups, rest = idx / groups;
+  const unsigned ch = idx % chunks * V, rest = idx / chunks;
   const unsigned h = rest % kv_heads, i = rest / kv_heads;
   if (i >= static_cast<unsigned>(N)) return;
   const long slot = slots[i];
   const bool ok = slot >= 0 && slot < n_slots;
   if (!ok && slot != -1 && status) atomicOr(status, MOE_DEV_BAD_SLOT);
-  const KvBlock blk = kv_block(page_size, D);
-  const long page = ok ? slot / page_size : 0;
-  const int row = ok ? static_cast<int>(slot - page * page_size) : 0;
+  const KvBlock blk = kv_block(1 << page_shift, D);
+  const long page = ok ? slot >> page_shift : 0;
+  const int row = ok ? static_cast<int>(slot) & ((1 << page_shift) - 1) : 0;
   const uint8_t* base = cache + (page * kv_heads + h) * static_cast<long>(blk.bytes);
-  const long at = (static_cast<long>(i) * kv_heads + h) * D + g * kKvGroup;
+  const long at = (static_cast<long>(i) * kv_heads + h) * D + ch;
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
-    float x[16] = {};
-    if (ok) {
-      const uint2 w = *reinterpret_cast<const uint2*>(base + (kv ? blk.v_code : 0u) +
-                                                      row * (D / 2) + g * 8);
-      const uint32_t s2 = base[(kv ? blk.v_scale : blk.k_scale) + row * groups + g];
-      const uint32_t s = f16_low_twice(e4m3x2_to_f16(s2));
-      uint32_t p[8];
-      e2m1_to_f16(w.x, *reinterpret_cast<uint32_t(*)[4]>(p));
-      e2m1_to_f16(w.y, *reinterpret_cast<uint32_t(*)[4]>(p + 4));
+    const uint8_t* src = base + (kv ? blk.v_code : 0u) + row * (D / 2) + ch / 2;
+    uint32_t w;
+    if constexpr (V == 8)
+      w = *reinterpret_cast<const uint32_t*>(src);
+    else
+      w = *reinterpret_cast<const uint16_t*>(src);
+    const uint32_t s2 = base[(kv ? blk.v_scale : blk.k_scale) + row * (D / kKvGroup) + ch / kKvGroup];
+    const uint32_t s = f16_low_twice(e4m3x2_to_f16(s2));
+    uint32_t p[4];
+    e2m1_to_f16(w, p);
+    float x[V];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t q = hmul2(p[j], s);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&q));
-        x[2 * j] = f.x * (kv ? v_scale : k_scale);
-        x[2 * j + 1] = f.y * (kv ? v_scale : k_scale);
-      }
+    for (int j = 0; j < V / 2; ++j) {
+      const uint32_t q = hmul2(p[j], s);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&q));
+      x[2 * j] = ok ? f.x * (kv ? v_scale : k_scale) : 0.0f;
+      x[2 * j + 1] = ok ? f.y * (kv ? v_scale : k_scale) : 0.0f;
     }
-    store16((kv ? v_out : k_out) + at, x);
+    store_chunk((kv ? v_out : k_out) + at, x);
   }
 }
 
@@ -340,7 +385,7 @@ cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t st) {
                                         reinterpret_cast<uintptr_t>(a.q_out) % 16 == 0)) &&
                     (a.kv_heads == 0 || (rows_aligned(a.k, eb) && rows_aligned(a.v, eb))) &&
                     reinterpret_cast<uintptr_t>(a.table) % 16 == 0;
-  const long units = fast ? a.D / 32 : (a.D + 15) / 16;
+  const long units = fast ? a.D / (32 / eb) : (a.D + 15) / 16;
   // heads per thread: 4 once that still gives every SM its 2048 threads
   const long all = units * a.T * (a.q_heads + 2l * a.kv_heads);
   const int hb = all / 4 >= 152l * 2048 ? 4 : 1;
@@ -365,26 +410,26 @@ cudaError_t launch_rope_table(const RopeTurns& turns, int pairs, float gain, int
                               const int32_t* positions, float* table, cudaStream_t st) {
   // enough rows per block to use each thread's frequency several times, few
   // enough to give every SM work
-  const int lanes = pairs <= kThreads ? kThreads / pairs : 1;
-  int rows = n / (152 * 8);
+  const int lanes = kThreads / pairs;
+  int rows = n / (152 * 16);
   rows = (rows < lanes ? lanes : rows + lanes - 1) / lanes * lanes;
   return launch_pdl(&rope_table_kernel, dim3((n + rows - 1) / rows), dim3(kThreads), 0, st, turns,
                     pairs, gain, n, positions, table, rows);
 }
 
 cudaError_t launch_kv_read(bool bf16, int N, const int64_t* slots, const uint8_t* cache,
-                           long n_slots, int kv_heads, int D, int page_size, float k_scale,
+                           long n_slots, int kv_heads, int D, int page_shift, float k_scale,
                            float v_scale, void* k_out, void* v_out, unsigned* status,
                            cudaStream_t st) {
-  const long total = static_cast<long>(N) * kv_heads * (D / kKvGroup);
+  const long total = static_cast<long>(N) * kv_heads * (D / (bf16 ? 8 : 4));
   const dim3 grid(static_cast<unsigned>((total + kThreads - 1) / kThreads));
   if (bf16)
     return launch_pdl(&kv_read_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, N, slots,
-                      cache, n_slots, kv_heads, D, page_size, k_scale, v_scale,
+                      cache, n_slots, kv_heads, D, page_shift, k_scale, v_scale,
                       static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out),
                       status);
   return launch_pdl(&kv_read_kernel<float>, grid, dim3(kThreads), 0, st, N, slots, cache, n_slots,
-                    kv_heads, D, page_size, k_scale, v_scale, static_cast<float*>(k_out),
+                    kv_heads, D, page_shift, k_scale, v_scale, static_cast<float*>(k_out),
                     static_cast<float*>(v_out), status);
 }
 

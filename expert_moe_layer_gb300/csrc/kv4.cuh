@@ -72,22 +72,18 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// 16 values of a group -> 8 code bytes and the scale byte.
-__device__ __forceinline__ uint32_t kv_store_group(const float (&x)[16], float inv_scale,
-                                                   uint32_t (&codes)[2]) {
-  float y[16], top = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float t = __fmul_rn(x[i], inv_scale);
-    y[i] = t == t ? t : 0.0f;
-    top = fmaxf(top, fabsf(y[i]));
-  }
+// V of the 16 scaled values of a group (NaN already replaced) whose largest
+// magnitude is `top` -> codes, eight to a word, and the scale byte.
+template <int V>
+__device__ __forceinline__ uint32_t kv_codes(const float (&y)[V], float top,
+                                             uint32_t (&codes)[(V + 7) / 8]) {
   const uint32_t s8 = e4m3(__fmul_rn(top, 1.0f / 6.0f));
   const float s = __half2float(__ushort_as_half(static_cast<uint16_t>(e4m3x2_to_f16(s8) & 0xffffu)));
-  codes[0] = codes[1] = 0;
+#pragma unroll
+  for (int i = 0; i < (V + 7) / 8; ++i) codes[i] = 0;
   if (s > 0.0f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < V / 2; ++i)
       codes[i >> 2] |= e2m1x2(__fdiv_rn(y[2 * i], s), __fdiv_rn(y[2 * i + 1], s)) << (8 * (i & 3));
   }
   return s8;
