@@ -43,12 +43,11 @@ __device__ __forceinline__ __nv_bfloat16 from_f(float v) {
 }
 
 // One 16-byte chunk: 8 bf16 or 4 fp32 elements.
-__device__ __forceinline__ void load_chunk(const float* p, float (&x)[4]) {
-  const float4 v = *reinterpret_cast<const float4*>(p);
-  x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+__device__ __forceinline__ void unpack_chunk(uint4 v, float (&x)[4]) {
+  x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y);
+  x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
 }
-__device__ __forceinline__ void load_chunk(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack_chunk(uint4 v, float (&x)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -113,7 +112,7 @@ __device__ __forceinline__ void store_codes(const RopeArgs& a, bool value, Place
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const float t = __fmul_rn(x[i], value ? a.v_inv : a.k_inv);
-    y[i] = t == t ? t : 0.0f;
+    y[i] = t == t ? fminf(fmaxf(t, -kKvMost), kKvMost) : 0.0f;
     top = fmaxf(top, fabsf(y[i]));
   }
 #pragma unroll
@@ -132,18 +131,19 @@ __device__ __forceinline__ void store_codes(const RopeArgs& a, bool value, Place
         static_cast<uint8_t>(s8);
 }
 
-// A chunk is up to `hb` heads of q, then of k, then of v, of one token.
+// Up to `hb` heads of k, of v or of q of one token. The kinds follow one
+// another over the whole grid, so that no warp has to do two of them.
 struct Chunk {
   int t, kind, h0, h1;  // kind: 0 q, 1 k, 2 v
 };
-__device__ __forceinline__ Chunk chunk_of(const RopeArgs& a, unsigned rest, int hb, int cq, int ck) {
-  const unsigned per = cq + 2 * ck;
+__device__ __forceinline__ Chunk chunk_of(const RopeArgs& a, unsigned i, int hb, int cq, int ck) {
+  const unsigned nk = static_cast<unsigned>(a.T) * ck;
   Chunk c;
-  c.t = static_cast<int>(rest / per);
-  int i = static_cast<int>(rest - c.t * per);
-  c.kind = i < cq ? 0 : i < cq + ck ? 1 : 2;
-  i -= c.kind == 0 ? 0 : c.kind == 1 ? cq : cq + ck;
-  c.h0 = i * hb;
+  c.kind = i < nk ? 1 : i < 2 * nk ? 2 : 0;
+  i -= c.kind == 1 ? 0 : c.kind == 2 ? nk : 2 * nk;
+  const unsigned per = c.kind ? ck : cq;
+  c.t = static_cast<int>(i / per);
+  c.h0 = static_cast<int>(i - c.t * per) * hb;
   c.h1 = min(c.h0 + hb, c.kind ? a.kv_heads : a.q_heads);
   return c;
 }
@@ -164,8 +164,8 @@ __device__ __forceinline__ long slot_of(const RopeArgs& a, int t) {
 }
 
 // D and R multiples of 32, 16-byte aligned rows.
-template <typename T, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int hb, int cq, int ck,
+template <typename T, bool kInterleaved, int kHeads>
+__global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int cq, int ck,
                                                         unsigned total) {
   constexpr int V = 16 / sizeof(T);     // elements of a chunk
   constexpr int kSharers = kKvGroup / V;  // lanes that share a scale
@@ -174,12 +174,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int hb, int 
   if (idx >= total) return;
   const unsigned units = a.D / (2 * V);
   const int u = static_cast<int>(idx % units);
-  const Chunk c = chunk_of(a, idx / units, hb, cq, ck);
-  long slot = 0;
-  if (c.kind && (slot = slot_of(a, c.t)) < 0) return;
-  bool ok = true;
-  const float* row = table_row(a, c.t, ok);
-  if (!ok) return;
+  const Chunk c = chunk_of(a, idx / units, kHeads, cq, ck);
   const int pairs = a.R / 2, turned = pairs / V;  // units that rotate
   const bool turns = c.kind != 2 && u < turned;
   // first channels of the two chunks
@@ -188,6 +183,22 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int hb, int 
     c0 = turns ? V * u : a.R + V * (u - turned);
     c1 = c0 + (turns ? pairs : (a.D - a.R) / 2);
   }
+  // the rows first: they depend on nothing that has to be fetched before
+  const Rows rows = c.kind == 0 ? a.q : c.kind == 1 ? a.k : a.v;
+  const T* src = static_cast<const T*>(rows.p) + c.t * rows.token + c.h0 * rows.head;
+  uint4 raw[kHeads][2];
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    if (c.h0 + i < c.h1) {
+      raw[i][0] = *reinterpret_cast<const uint4*>(src + i * rows.head + c0);
+      raw[i][1] = *reinterpret_cast<const uint4*>(src + i * rows.head + c1);
+    }
+  }
+  long slot = 0;
+  if (c.kind && (slot = slot_of(a, c.t)) < 0) return;
+  bool ok = true;
+  const float* row = table_row(a, c.t, ok);
+  if (!ok) return;
   float cs[V], sn[V];
   if (turns) {
     if (kInterleaved) {
@@ -203,17 +214,17 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int hb, int 
 #pragma unroll
       for (int i = 0; i < V; ++i) sn[i] = -sn[i];
   }
-  const Rows rows = c.kind == 0 ? a.q : c.kind == 1 ? a.k : a.v;
-  const T* src = static_cast<const T*>(rows.p) + c.t * rows.token;
   Place at = {nullptr, 0};
   if (c.kind) at = place_of(a, slot);
   const int lane = threadIdx.x & 31;
   const unsigned lanes = ((1u << kSharers) - 1u) << (lane & ~(kSharers - 1));
-#pragma unroll 4
-  for (int h = c.h0; h < c.h1; ++h) {
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    const int h = c.h0 + i;
+    if (h >= c.h1) break;
     float x[V], y[V];
-    load_chunk(src + h * rows.head + c0, x);
-    load_chunk(src + h * rows.head + c1, y);
+    unpack_chunk(raw[i][0], x);
+    unpack_chunk(raw[i][1], y);
     if (turns) {
       if (kInterleaved) {
 #pragma unroll
@@ -393,11 +404,12 @@ cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t st) {
   const long total = units * a.T * (cq + 2l * ck);
   if (total == 0) return cudaSuccess;
   if (total > 0xffffff00l) return cudaErrorInvalidValue;
-  auto kern = !fast            ? &rope_any_kernel<T>
-              : a.interleaved ? &rope_kernel<T, true>
-                              : &rope_kernel<T, false>;
-  return launch_pdl(kern, dim3(static_cast<unsigned>((total + kThreads - 1) / kThreads)),
-                    dim3(kThreads), 0, st, a, hb, cq, ck, static_cast<unsigned>(total));
+  const dim3 grid(static_cast<unsigned>((total + kThreads - 1) / kThreads)), block(kThreads);
+  const unsigned n = static_cast<unsigned>(total);
+  if (!fast) return launch_pdl(&rope_any_kernel<T>, grid, block, 0, st, a, hb, cq, ck, n);
+  auto* kern = a.interleaved ? (hb == 1 ? &rope_kernel<T, true, 1> : &rope_kernel<T, true, 4>)
+                             : (hb == 1 ? &rope_kernel<T, false, 1> : &rope_kernel<T, false, 4>);
+  return launch_pdl(kern, grid, block, 0, st, a, cq, ck, n);
 }
 
 }  // namespace

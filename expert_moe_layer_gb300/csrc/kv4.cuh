@@ -72,19 +72,35 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// V of the 16 scaled values of a group (NaN already replaced) whose largest
-// magnitude is `top` -> codes, eight to a word, and the scale byte.
+// Values are cut off here before they are stored: beyond 6 * 448, the largest
+// value that a code and a scale can hold, and infinities become finite.
+constexpr float kKvMost = 4096.0f;
+
+// V of the 16 scaled values of a group (NaN already replaced, cut off at
+// kKvMost) whose largest magnitude is `top` -> codes, eight to a word, and the
+// scale byte. The quotients have to be rounded correctly: for 16-bit inputs many
+// lie exactly between two codes. They are made from the correctly rounded
+// reciprocal, the product with it and one correction by the exact remainder
+// (Markstein, 1990), three operations where a division takes some fifteen;
+// the scale is between 2^-9 and 448, so nothing leaves the normal range that
+// would not round to the code 0.
 template <int V>
 __device__ __forceinline__ uint32_t kv_codes(const float (&y)[V], float top,
                                              uint32_t (&codes)[(V + 7) / 8]) {
   const uint32_t s8 = e4m3(__fmul_rn(top, 1.0f / 6.0f));
   const float s = __half2float(__ushort_as_half(static_cast<uint16_t>(e4m3x2_to_f16(s8) & 0xffffu)));
+  const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
 #pragma unroll
   for (int i = 0; i < (V + 7) / 8; ++i) codes[i] = 0;
-  if (s > 0.0f) {
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i)
-      codes[i >> 2] |= e2m1x2(__fdiv_rn(y[2 * i], s), __fdiv_rn(y[2 * i + 1], s)) << (8 * (i & 3));
+  for (int i = 0; i < V / 2; ++i) {
+    float q[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float p = __fmul_rn(y[2 * i + j], r);
+      q[j] = __fmaf_rn(__fmaf_rn(-p, s, y[2 * i + j]), r, p);
+    }
+    codes[i >> 2] |= e2m1x2(q[0], q[1]) << (8 * (i & 3));
   }
   return s8;
 }
