@@ -47,6 +47,7 @@ constexpr int kThreads = 512;                 // whole groups of four warps (thr
 constexpr int kSoftRegs = 152, kMmaRegs = 80;
 constexpr int kBadRing = 4;  // tiles whose bad-page bits are kept: a fill warp is at most
                              // two tiles ahead of the slower half
+constexpr float kMostP = 16384.0f;  // 2^(kLift + kLag)
 constexpr uint32_t kColsS = 0, kColsO = 256;  // columns of S (128 each half) and of O
 
 template <int D>
@@ -101,6 +102,34 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// Two fp32 values in a 64-bit register, and the instructions on both at once.
+__device__ __forceinline__ uint64_t pair_b32(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair_f32(float lo, float hi) {
+  return pair_b32(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ void unpair_f32(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
@@ -297,37 +326,54 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool whole = tok0 >= all_first && tok0 + kKeys - 1 <= all_last &&
                              (bad.x | bad.y | bad.z | bad.w) == 0;
           uint32_t pk[kKeys / 2];
-          float sum, mx;
+          float sum;
+          bool over;  // a P has outgrown the lag allowed to the maximum
+          auto visible = [&](int c, uint32_t(&v)[32]) {
+            const uint32_t bits = c == 0 ? bad.x : c == 1 ? bad.y : c == 2 ? bad.z : bad.w;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int key = tok0 + 32 * c + i;
+              if (key < first || key > last || ((bits >> i) & 1u)) v[i] = 0xff800000u;
+            }
+          };
           auto pass = [&](bool masked) {
-            sum = 0.0f;
-            mx = -INFINITY;
+            const uint64_t gain2 = pair_f32(gain, gain), off2 = pair_f32(-mbase, -mbase);
+            uint64_t sums[2] = {0, 0};
+            uint32_t top = 0;
 #pragma unroll
             for (int c = 0; c < kKeys / 32; ++c) {
               uint32_t v[32];
               tmem_ld32(ts + 32 * c, v);
-              if (masked) {
-                const uint32_t bits = c == 0 ? bad.x : c == 1 ? bad.y : c == 2 ? bad.z : bad.w;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const int key = tok0 + 32 * c + i;
-                  if (key < first || key > last || ((bits >> i) & 1u)) v[i] = 0xff800000u;
-                }
-              }
+              if (masked) visible(c, v);
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                const float s0 = __uint_as_float(v[2 * i]), s1 = __uint_as_float(v[2 * i + 1]);
-                mx = fmaxf(mx, fmaxf(s0, s1));
-                const float p0 = ex2(fmaf(s0, gain, -mbase)), p1 = ex2(fmaf(s1, gain, -mbase));
-                sum += p0 + p1;
+                float x0, x1;
+                unpair_f32(fma_f32x2(pair_b32(v[2 * i], v[2 * i + 1]), gain2, off2), x0, x1);
+                const float p0 = ex2(x0), p1 = ex2(x1);
+                sums[i & 1] = add_f32x2(sums[i & 1], pair_f32(p0, p1));
                 pk[16 * c + i] = pack_f16(p0, p1);
+                top = max_f16x2(top, pk[16 * c + i]);
               }
             }
+            float s0, s1;
+            unpair_f32(add_f32x2(sums[0], sums[1]), s0, s1);
+            sum = s0 + s1;
+            const float2 t2 = unpack_f16(top);
+            over = fmaxf(t2.x, t2.y) > kMostP;
           };
           if (whole) pass(false);
           else pass(true);
-          const float top_x = mx * gain;
-          if (__any_sync(~0u, top_x > m + kLag)) {
-            const float nm = fmaxf(m, top_x);
+          if (__any_sync(~0u, over || m == -INFINITY)) {
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < kKeys / 32; ++c) {
+              uint32_t v[32];
+              tmem_ld32(ts + 32 * c, v);
+              if (!whole) visible(c, v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(v[i]));
+            }
+            const float nm = fmaxf(m, mx * gain);
             const float nb = nm == -INFINITY ? -kLift : nm - kLift;
             const float f = m == -INFINITY ? 0.0f : ex2(mbase - nb);
             l *= f;
