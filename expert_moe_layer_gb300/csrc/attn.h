@@ -73,22 +73,23 @@ struct AttnArgs {
 constexpr int kAttnMaxSms = 160;
 
 struct AttnLayout {
-  size_t status, counters, info, starts, stats, partial, total;
+  size_t status, counters, info, starts, row_tiles, firsts, stats, partial, total;
 };
-AttnLayout attn_layout(const moe_attn_config* c, int B, int sms);
+AttnLayout attn_layout(const moe_attn_config* c, int B, int T, int max_q);
 
-// One request, as the plan kernel leaves it: first query row, its tokens,
-// cached tokens, first 16-token tile that is read.
+// One request, checked: first query row, its tokens, cached tokens, the first
+// key that one of its queries sees.
 struct SeqInfo {
-  int q0, q_len, len, first_tile;
+  int q0, q_len, len, first_key;
 };
 
-// Rows of a unit of the prompt kernel, and the rows per request (query tokens
-// times heads of a group) it is used from.
-constexpr int kPromptTile = 256, kPromptRows = 64;
+// Rows of a row tile of the prompt kernel (query tokens times heads of a
+// group), and the rows per request it is used from.
+constexpr int prompt_tile(int head_dim) { return head_dim == 256 ? 128 : 256; }
+constexpr int kPromptRows = 64;
 cudaError_t launch_prompt(const AttnArgs& a, void* ws, const AttnLayout& L, cudaStream_t st);
 
-cudaError_t launch_kv_attention(bool bf16, const AttnArgs& a, void* ws, const AttnLayout& L,
-                                cudaStream_t st);
+cudaError_t launch_kv_attention(const moe_attn_config* c, const AttnArgs& a, void* ws,
+                                const AttnLayout& L, cudaStream_t st);
 
 }  // namespace moe

@@ -279,7 +279,7 @@ static int validate_attention(const moe_attn_config* cfg, int num_seqs, int T, i
 size_t moe_kv_attention_workspace_size(const moe_attn_config* cfg, int num_seqs, int T,
                                        int max_q_len) {
   if (validate_attention(cfg, num_seqs, T, max_q_len) != MOE_OK) return 0;
-  return attn_layout(cfg, num_seqs, kAttnMaxSms).total;
+  return attn_layout(cfg, num_seqs, T, max_q_len).total;
 }
 
 int moe_kv_attention(const moe_attn_config* cfg, int num_seqs, int T, int max_q_len,
@@ -301,7 +301,7 @@ int moe_kv_attention(const moe_attn_config* cfg, int num_seqs, int T, int max_q_
       !aligned(page_table, 4) || !aligned(q_offsets, 4) || !aligned(lse, 4))
     return MOE_ERR_INVALID_ARG;
   MOE_TRY(validate_cache(cache, num_pages));
-  const AttnLayout L = attn_layout(cfg, num_seqs, kAttnMaxSms);
+  const AttnLayout L = attn_layout(cfg, num_seqs, T, max_q_len);
   if (!ws || ws_bytes < L.total || !aligned(ws, 16)) return MOE_ERR_WORKSPACE;
   AttnArgs a;
   a.sms = sm_count();
@@ -320,8 +320,7 @@ int moe_kv_attention(const moe_attn_config* cfg, int num_seqs, int T, int max_q_
   a.max_pages = max_pages;
   a.cache = static_cast<const uint8_t*>(cache), a.num_pages = static_cast<long>(num_pages);
   a.out = out, a.lse = lse;
-  return cuda_ok(launch_kv_attention(cfg->act_dtype == MOE_BF16, a, ws, L,
-                                     static_cast<cudaStream_t>(stream)));
+  return cuda_ok(launch_kv_attention(cfg, a, ws, L, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

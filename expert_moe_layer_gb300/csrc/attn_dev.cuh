@@ -30,6 +30,51 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// What request b asks for, checked; flags collects MOE_DEV_* bits.
+__device__ __forceinline__ SeqInfo seq_info(const AttnArgs& a, int b, unsigned& flags) {
+  SeqInfo s = {0, 0, 0, 0};
+  const int q0 = a.q_offsets ? a.q_offsets[b] : b;
+  const int q1 = a.q_offsets ? a.q_offsets[b + 1] : b + 1;
+  const int n = a.seq_lens[b];
+  if (q0 < 0 || q1 < q0 || q1 > a.T || q1 - q0 > a.max_q) {
+    flags |= MOE_DEV_BAD_SEGMENT;
+  } else {
+    s.q0 = q0;
+    s.q_len = q1 - q0;
+  }
+  const long cap = static_cast<long>(a.max_pages) * a.page_size;
+  s.len = static_cast<int>(n < 0 ? 0 : n > cap ? cap : n);
+  if (s.len != n) flags |= MOE_DEV_BAD_PAGE;
+  if (a.window > 0) {
+    const long lo = static_cast<long>(s.len) - s.q_len - a.window + 1;
+    s.first_key = lo > 0 ? static_cast<int>(lo) : 0;
+  }
+  return s;
+}
+
+// Sum of the values of the threads before this one in a block of N threads,
+// plus `base`, to which the block's sum is added.
+template <int N>
+__device__ __forceinline__ long block_scan(long v, long* warp_sum, long& base) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long sum = v;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const long u = __shfl_up_sync(~0u, sum, d);
+    if (lane >= d) sum += u;
+  }
+  if (lane == 31) warp_sum[warp] = sum;
+  __syncthreads();
+  long before = base;
+#pragma unroll
+  for (int w = 0; w < N / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    base += warp_sum[w];
+  }
+  __syncthreads();
+  return before + sum - v;
+}
+
 template <int N>
 struct Words {
   uint32_t w[N];

@@ -45,60 +45,27 @@ constexpr int kPlanThreads = 1024;
 constexpr int kInlineSeqs = 256;  // up to so many requests are planned by every CTA
 
 // Checks every request and sums up the work list with a block of N threads:
-// starts[b] is the first tile of request b in it (with `whole`, the first
-// segment: a row tile of a kv head is one unit then). Each thread gets the
-// MOE_DEV_* flags of the requests it checked.
+// starts[b] is the first tile of request b in it. Each thread gets the MOE_DEV_*
+// flags of the requests it checked.
 template <int N>
-__device__ __forceinline__ unsigned sum_work(const AttnArgs& a, int row_tile, bool whole,
-                                             SeqInfo* info, long* starts) {
+__device__ __forceinline__ unsigned sum_work(const AttnArgs& a, int row_tile, SeqInfo* info,
+                                             long* starts) {
   __shared__ long warp_sum[N / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = a.heads / a.kv_heads;
-  const long cap = static_cast<long>(a.max_pages) * a.page_size;
   unsigned flags = 0;
   long base = 0;
   for (int b0 = 0; b0 < a.B; b0 += N) {
     const int b = b0 + threadIdx.x;
     long tiles = 0;
     if (b < a.B) {
-      SeqInfo s = {0, 0, 0, 0};
-      const int q0 = a.q_offsets ? a.q_offsets[b] : b;
-      const int q1 = a.q_offsets ? a.q_offsets[b + 1] : b + 1;
-      const int n = a.seq_lens[b];
-      if (q0 < 0 || q1 < q0 || q1 > a.T || q1 - q0 > a.max_q) {
-        flags |= MOE_DEV_BAD_SEGMENT;
-      } else {
-        s.q0 = q0;
-        s.q_len = q1 - q0;
-      }
-      s.len = static_cast<int>(n < 0 ? 0 : n > cap ? cap : n);
-      if (s.len != n) flags |= MOE_DEV_BAD_PAGE;
-      if (a.window > 0) {
-        const long lo = static_cast<long>(s.len) - s.q_len - a.window + 1;
-        s.first_tile = lo > 0 ? static_cast<int>(lo / kTile) : 0;
-      }
-      const long row_tiles = (static_cast<long>(s.q_len) * g + row_tile - 1) / row_tile;
-      const long per = (s.len + kTile - 1) / kTile - s.first_tile;
-      tiles = row_tiles * a.kv_heads * (whole ? 1 : kSetup + (per < 0 ? 0 : per));
+      const SeqInfo s = seq_info(a, b, flags);
       info[b] = s;
+      const long row_tiles = (static_cast<long>(s.q_len) * g + row_tile - 1) / row_tile;
+      const int per = (s.len + kTile - 1) / kTile - s.first_key / kTile;
+      tiles = row_tiles * a.kv_heads * (kSetup + (per < 0 ? 0 : per));
     }
-    long sum = tiles;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const long v = __shfl_up_sync(~0u, sum, d);
-      if (lane >= d) sum += v;
-    }
-    if (lane == 31) warp_sum[warp] = sum;
-    __syncthreads();
-    long before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < N / 32; ++w) {
-      if (w < warp) before += warp_sum[w];
-      all += warp_sum[w];
-    }
-    if (b < a.B) starts[b] = base + before + sum - tiles;
-    base += all;
-    __syncthreads();
+    const long before = block_scan<N>(tiles, warp_sum, base);
+    if (b < a.B) starts[b] = before;
   }
   if (threadIdx.x == 0) starts[a.B] = base;
   return flags;
@@ -108,14 +75,14 @@ __device__ __forceinline__ unsigned sum_work(const AttnArgs& a, int row_tile, bo
 // few requests every CTA of the split kernel does that itself, sooner than a
 // kernel before it could hand it over; its first loads then overlap this one.)
 __global__ void __launch_bounds__(kPlanThreads)
-    attn_plan_kernel(AttnArgs a, int row_tile, bool whole, unsigned* status, int* counters,
-                     int n_counters, SeqInfo* info, long* starts) {
+    attn_plan_kernel(AttnArgs a, int row_tile, unsigned* status, int* counters, int n_counters,
+                     SeqInfo* info, long* starts) {
   pdl_enter();
   if (threadIdx.x == 0) *status = 0;
   for (int i = threadIdx.x; i < n_counters; i += blockDim.x) counters[i] = 0;
   if (!info) return;
   __syncthreads();
-  const unsigned flags = sum_work<kPlanThreads>(a, row_tile, whole, info, starts);
+  const unsigned flags = sum_work<kPlanThreads>(a, row_tile, info, starts);
   if (flags) atomicOr(status, flags);
 }
 
@@ -256,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
   if constexpr (kInline) {
     __shared__ SeqInfo s_info[kInlineSeqs];
     __shared__ long s_starts[kInlineSeqs + 1];
-    flags = sum_work<kThreads>(a, kRows, false, s_info, s_starts);
+    flags = sum_work<kThreads>(a, kRows, s_info, s_starts);
     __syncthreads();
     info = s_info;
     starts = s_starts;
@@ -286,8 +253,9 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
   while (at < end) {
     while (starts[b + 1] <= at) ++b;
     const SeqInfo sq = info[b];
+    const int first_tile = sq.first_key / kTile;
     const int rows = sq.q_len * group;
-    const int per_seg = kSetup + max(0, (sq.len + kTile - 1) / kTile - sq.first_tile);
+    const int per_seg = kSetup + max(0, (sq.len + kTile - 1) / kTile - first_tile);
     const long seg = (at - starts[b]) / per_seg;
     const long seg_start = starts[b] + seg * per_seg, seg_end = seg_start + per_seg;
     if (at - seg_start < kSetup) at = seg_start;
@@ -389,8 +357,8 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
       for (int j = 0; j < 2; ++j) m[nt][j] = -INFINITY, base[nt][j] = -kLift, l[nt][j] = 0.0f;
 
     // tiles of this row tile that hold a visible token
-    const int tA = max(t0, tile_first / kTile - sq.first_tile);
-    const int tB = min(t1, tile_last < 0 ? 0 : tile_last / kTile + 1 - sq.first_tile);
+    const int tA = max(t0, tile_first / kTile - first_tile);
+    const int tB = min(t1, tile_last < 0 ? 0 : tile_last / kTile + 1 - first_tile);
     const int32_t* pages = a.page_table + static_cast<long>(b) * a.max_pages;
     // The CTA's warps take the tiles of the range in turn. Each keeps a ring of
     // kStages tiles: the copies run kStages - 1 tiles ahead, the page id one
@@ -398,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
     uint8_t* ring = reinterpret_cast<uint8_t*>(smem) + warp * kStages * TileBytes<D>::kBytes;
     const uint32_t ring_addr = ptx::smem_u32(ring);
     auto page_of = [&](int t) {
-      return t < tB ? pages[(t + sq.first_tile) >> tiles_per_page_log2] : 0;
+      return t < tB ? pages[(t + first_tile) >> tiles_per_page_log2] : 0;
     };
     uint32_t ok_bits = 0;  // by stage: the page id was good
     auto copy = [&](int t, int stage, int id) {
@@ -406,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
         const bool ok = id >= 0 && id < a.num_pages;
         if (!ok && lane == 0) atomicOr(status, MOE_DEV_BAD_PAGE);
         ok_bits = (ok_bits & ~(1u << stage)) | (static_cast<uint32_t>(ok) << stage);
-        const int tile = t + sq.first_tile;
+        const int tile = t + first_tile;
         copy_tile<D>(ring_addr + stage * TileBytes<D>::kBytes,
                      a.cache + (static_cast<long>(ok ? id : 0) * a.kv_heads + kvh) * blk.bytes,
                      a.page_size, (tile & ((1 << tiles_per_page_log2) - 1)) * kTile, lane);
@@ -437,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
       const bool ok = (ok_bits >> stage) & 1u;
       TileRegs<D> cur;
       load_tile<D>(cur, ring + stage * TileBytes<D>::kBytes, g, c);
-      const int tok0 = (t + sq.first_tile) * kTile;
+      const int tok0 = (t + first_tile) * kTile;
       const bool whole = ok && tok0 >= all_first && tok0 + kTile - 1 <= all_last;
 
       float s[NT][4];
@@ -723,21 +691,17 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
   }
 }
 
-cudaError_t launch_plan(const AttnArgs& a, int row_tile, bool whole, int n_counters, bool sum,
-                        void* ws, const AttnLayout& L, cudaStream_t st) {
-  char* w = static_cast<char*>(ws);
-  return launch_pdl(&attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a, row_tile, whole,
-                    reinterpret_cast<unsigned*>(w + L.status),
-                    reinterpret_cast<int*>(w + L.counters), n_counters,
-                    sum ? reinterpret_cast<SeqInfo*>(w + L.info) : nullptr,
-                    reinterpret_cast<long*>(w + L.starts));
-}
-
 template <typename T, int D, int kRows, int kTerms, bool kInline>
 cudaError_t launch_split_as(const AttnArgs& a, void* ws, const AttnLayout& L, cudaStream_t st) {
   auto* kern = &attn_split_kernel<T, D, kRows, kTerms, kInline>;
   const int grid = a.sms * ctas_per_sm<D, kRows, kTerms>();
-  cudaError_t e = launch_plan(a, kRows, false, grid, !kInline, ws, L, st);
+  char* w = static_cast<char*>(ws);
+  auto* status = reinterpret_cast<unsigned*>(w + L.status);
+  auto* counters = reinterpret_cast<int*>(w + L.counters);
+  auto* info = reinterpret_cast<SeqInfo*>(w + L.info);
+  auto* starts = reinterpret_cast<long*>(w + L.starts);
+  cudaError_t e = launch_pdl(&attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a, kRows, status,
+                             counters, grid, kInline ? nullptr : info, starts);
   if (e != cudaSuccess) return e;
   constexpr int smem = split_smem<D, kRows>();
   static std::atomic<unsigned long long> done{0};
@@ -745,12 +709,8 @@ cudaError_t launch_split_as(const AttnArgs& a, void* ws, const AttnLayout& L, cu
   if (e != cudaSuccess) return e;
   int log2 = 0;
   while ((kTile << log2) < a.page_size) ++log2;
-  char* w = static_cast<char*>(ws);
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, a,
-                    reinterpret_cast<unsigned*>(w + L.status),
-                    reinterpret_cast<int*>(w + L.counters),
-                    reinterpret_cast<const SeqInfo*>(w + L.info),
-                    reinterpret_cast<const long*>(w + L.starts),
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, a, status, counters,
+                    const_cast<const SeqInfo*>(info), const_cast<const long*>(starts),
                     reinterpret_cast<float*>(w + L.stats), reinterpret_cast<float*>(w + L.partial),
                     log2);
 }
@@ -774,29 +734,41 @@ cudaError_t launch_dim(bool bf16, const AttnArgs& a, void* ws, const AttnLayout&
 
 }  // namespace
 
-AttnLayout attn_layout(const moe_attn_config* c, int B, int sms) {
+// From kPromptRows rows per request the matrix work, not the cache's
+// bandwidth, is the bound: the prompt kernel (bf16).
+bool uses_prompt_kernel(const moe_attn_config* c, int max_q) {
+  return c->act_dtype == MOE_BF16 &&
+         static_cast<long>(max_q) * (c->num_heads / c->num_kv_heads) >= kPromptRows;
+}
+
+AttnLayout attn_layout(const moe_attn_config* c, int B, int T, int max_q) {
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-  const size_t ctas = static_cast<size_t>(sms) * kMaxCtasPerSm;
+  const bool prompt = uses_prompt_kernel(c, max_q);
+  const size_t ctas = static_cast<size_t>(kAttnMaxSms) * (prompt ? 1 : kMaxCtasPerSm);
+  // each request's last row tile may be partly filled
+  const size_t group = c->num_heads / c->num_kv_heads;
+  const size_t row_tiles =
+      prompt ? static_cast<size_t>(T) * group / prompt_tile(c->head_dim) + B : 0;
+  const size_t lists = prompt ? row_tiles : static_cast<size_t>(B);
+  // two pieces per CTA, of up to 16 rows or of a whole row tile
+  const size_t piece_rows = 2 * ctas * (prompt ? prompt_tile(c->head_dim) : 16);
   AttnLayout L;
   L.status = 0;
   L.counters = 256;
-  L.info = up(L.counters + 4 * ctas);
+  L.info = up(L.counters + 2 * 4 * ctas);
   L.starts = up(L.info + sizeof(SeqInfo) * static_cast<size_t>(B));
-  L.stats = up(L.starts + 8 * (static_cast<size_t>(B) + 1));
-  // two pieces of up to 16 rows per CTA
-  L.partial = up(L.stats + 2 * ctas * 16 * 8);
-  L.total = up(L.partial + 2 * ctas * 16 * static_cast<size_t>(c->head_dim) * 4);
+  L.row_tiles = up(L.starts + 8 * (lists + 1));
+  L.firsts = up(L.row_tiles + (prompt ? 8 * row_tiles : 0));
+  L.stats = up(L.firsts + (prompt ? 4 * (static_cast<size_t>(B) + 1) : 0));
+  L.partial = up(L.stats + piece_rows * 8);
+  L.total = up(L.partial + piece_rows * static_cast<size_t>(c->head_dim) * 4);
   return L;
 }
 
-cudaError_t launch_kv_attention(bool bf16, const AttnArgs& a, void* ws, const AttnLayout& L,
-                                cudaStream_t st) {
-  // From kPromptRows rows per request the matrix work, not the cache's
-  // bandwidth, is the bound: the prompt kernel.
-  if (bf16 && a.D <= 128 && static_cast<long>(a.max_q) * (a.heads / a.kv_heads) >= kPromptRows) {
-    const cudaError_t e = launch_plan(a, kPromptTile, true, 1, true, ws, L, st);
-    return e != cudaSuccess ? e : launch_prompt(a, ws, L, st);
-  }
+cudaError_t launch_kv_attention(const moe_attn_config* c, const AttnArgs& a, void* ws,
+                                const AttnLayout& L, cudaStream_t st) {
+  if (uses_prompt_kernel(c, a.max_q)) return launch_prompt(a, ws, L, st);
+  const bool bf16 = c->act_dtype == MOE_BF16;
   switch (a.D) {
     case 64:
       return launch_dim<64>(bf16, a, ws, L, st);

@@ -2,21 +2,26 @@
 //
 // Many query tokens share a request's keys, so matrix work bounds this kernel:
 // 4 D operations per (row, key) on the tcgen05 tensor cores, and one
-// exponential. A unit is 256 rows of one (request, kv head); a row is one
-// (query token, head of the group) pair, so that a group's heads share every
-// dequantised key. Per 128 keys:
+// exponential. A row is one (query token, head of the group) pair, so that a
+// group's heads share every dequantised key; a row tile is one or two halves of
+// 128 rows. Per tile of 128 keys (64 with 256 channels):
 //   - four warps turn codes and scales into f16 (exactly) in shared memory, K
 //     as rows of channels, V transposed to rows of tokens, both in the 128-byte
 //     swizzle that the matrix unit reads, two stages deep;
-//   - one thread issues S = Q K^T and O += P V for the two halves of 128 rows
-//     in turn, S and O in tensor memory, P read from tensor memory in the place
-//     of the S it came from;
-//   - four warps per half take S (a thread holds a whole row: no shuffles),
-//     mask, exponentiate and write P, one half while the other's products run.
-// The running maximum may lag behind (kLag): a tile is exponentiated on the
-// old one in a single pass over S, and done again, with O rescaled, in the
-// rare case that a row's maximum has outgrown it. Units are drawn from a
-// counter, a request's longest rows first.
+//   - one thread issues S = Q K^T and O += P V for the halves in turn, S and O
+//     in tensor memory, P read from tensor memory in the place of the S it came
+//     from;
+//   - four warps per half take S (a thread holds a row: no shuffles), mask,
+//     exponentiate and write P, one half while the other's products run.
+// The running maximum may lag behind (kLag), so that a pass over S needs no
+// maximum beforehand; in the rare case that a row has outgrown it, the maximum
+// moves up by whole powers of two, and O, the sums and the tile's earlier P are
+// scaled down exactly.
+//
+// The tiles of all (row tile, kv head) segments form one list, cut into equal
+// ranges, one per CTA, as in the split kernel: causal lengths differ, and a
+// short chunk after a long context has few row tiles. Pieces of a segment leave
+// fp32 sums, and the last CTA joins them in CTA order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -35,58 +40,79 @@ MOE_WAIT_LIMIT_SETTER(set_wait_limit_attn)
 
 namespace {
 
-constexpr int kHalf = 128;                    // rows of a half, lanes of tensor memory
-constexpr int kKeys = 128;                    // keys per tile
+constexpr int kHalf = 128;  // rows of a half, lanes of tensor memory
 constexpr int kSoftWarps = 8, kFillWarps = 4;
 constexpr int kMmaWarp = kSoftWarps + kFillWarps;
-constexpr int kWarpsAll = kMmaWarp + 1;       // warps with a role
-constexpr int kThreads = 512;                 // whole groups of four warps (three idle ones)
+constexpr int kThreads = 512;  // whole groups of four warps (three idle ones)
 // Registers per thread: launched with 128 each (65,536 in all); the matrix
-// warp's group gives most of its share to the two softmax groups:
+// warp's group gives some of its share to the two softmax groups:
 // 128 * (2 * 152 + 128 + 80) = 65,536.
 constexpr int kSoftRegs = 152, kMmaRegs = 80;
 constexpr int kBadRing = 4;  // tiles whose bad-page bits are kept: a fill warp is at most
                              // two tiles ahead of the slower half
-constexpr float kMostP = 16384.0f;  // 2^(kLift + kLag)
-constexpr uint32_t kColsS = 0, kColsO = 256;  // columns of S (128 each half) and of O
+constexpr int kSetup = 4;    // list entries of a segment beside its tiles: its set-up and store
+constexpr int kMinTiles = 8;  // smallest range of a CTA
+constexpr int kPlanThreads = 1024;
+constexpr float kMostP = 16384.0f;              // 2^(kLift + kLag)
+constexpr uint32_t kColsS = 0, kColsO = 256;  // columns of S and of O
 
 template <int D>
-struct Smem {
-  static constexpr int kQ = kHalf * D * 2;   // one half's queries
-  static constexpr int kK = kKeys * D * 2;   // one stage of keys, or of values
-  static constexpr int kBytes = 2 * kQ + 4 * kK + 1024;
+struct Shape {
+  static constexpr int kTile = prompt_tile(D);      // rows of a row tile
+  static constexpr int kHalves = kTile / kHalf;
+  static constexpr int kKeys = D == 256 ? 64 : 128;  // keys per tile
+  static constexpr int kQ = kHalf * D * 2;          // bytes of one half's queries
+  static constexpr int kK = kKeys * D * 2;          // of one stage of keys, or of values
+  static constexpr int kBytes = kHalves * kQ + 4 * kK + 1024;
 };
 
 struct Bars {
-  uint64_t unit_full[2], unit_empty[2], q_ready[2], k_full[2], k_empty[2], v_full[2], v_empty[2],
-      s_full[2], p_ready[2], o_done[2], drain;
+  uint64_t q_ready[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2],
+      o_done[2], written[2], joined[2], drain;
 };
 
-// 32 consecutive columns of this warp's 32 lanes.
+// 32 consecutive columns of this warp's 32 lanes. The values are there after
+// tmem_landed.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
-      "%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void tmem_landed(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+        "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+        "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),
+        "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
+        "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+      :
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
-      "%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31]), "r"(taddr)
+      "%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
@@ -147,74 +173,189 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 // Byte offset of 16-byte chunk `chunk` of row `row` in a 128-byte-swizzled
 // operand whose panels (64 f16 wide) hold `rows` rows.
 __device__ __forceinline__ uint32_t swizzled(int row, int chunk, int rows) {
   return (chunk >> 3) * rows * 128 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
 
-// What every role derives from a unit number.
-struct Unit {
+// A row tile of the list: its request and its first row there.
+struct RowTile {
+  int b, row0;
+};
+
+// Clears the status and the counters and builds the list: firsts[b] is the
+// first row tile of request b, starts[r] the first entry of row tile r, whose
+// segments, one per kv head, have kSetup entries and their key tiles each.
+template <int D>
+__global__ void __launch_bounds__(kPlanThreads)
+    prompt_plan_kernel(AttnArgs a, int max_row_tiles, unsigned* status, int* counters,
+                       int n_counters, SeqInfo* info, int* firsts, RowTile* row_tiles,
+                       long* starts) {
+  using H = Shape<D>;
+  __shared__ long warp_sum[kPlanThreads / 32];
+  pdl_enter();
+  if (threadIdx.x == 0) *status = 0;
+  for (int i = threadIdx.x; i < n_counters; i += kPlanThreads) counters[i] = 0;
+  __syncthreads();
+  const int group = a.heads / a.kv_heads;
+  unsigned flags = 0;
+  long total = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+    const int b = b0 + threadIdx.x;
+    long n = 0;
+    if (b < a.B) {
+      const SeqInfo s = seq_info(a, b, flags);
+      info[b] = s;
+      n = (static_cast<long>(s.q_len) * group + H::kTile - 1) / H::kTile;
+    }
+    const long before = block_scan<kPlanThreads>(n, warp_sum, total);
+    // offsets that overlap could ask for more row tiles than T rows have
+    if (b < a.B) firsts[b] = static_cast<int>(min(before, static_cast<long>(max_row_tiles)));
+  }
+  if (total > max_row_tiles) flags |= MOE_DEV_BAD_SEGMENT;
+  const int n_tiles = static_cast<int>(min(total, static_cast<long>(max_row_tiles)));
+  if (threadIdx.x == 0) firsts[a.B] = n_tiles;
+  __syncthreads();
+  long entries = 0;
+  for (int r0 = 0; r0 < n_tiles; r0 += kPlanThreads) {
+    const int r = r0 + threadIdx.x;
+    long n = 0;
+    if (r < n_tiles) {
+      int lo = 0, hi = a.B;  // the last request whose first row tile is at most r
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (firsts[mid] <= r) lo = mid;
+        else hi = mid;
+      }
+      const SeqInfo s = info[lo];
+      const int row0 = (r - firsts[lo]) * H::kTile;
+      row_tiles[r] = {lo, row0};
+      const int last = min(s.q_len * group, row0 + H::kTile) - 1;
+      const int before = s.len - s.q_len;
+      const int first_key = a.window > 0 ? max(0, before + row0 / group - a.window + 1) : 0;
+      const int end_key = before + last / group + 1;
+      const int tiles =
+          end_key <= 0 ? 0 : (end_key + H::kKeys - 1) / H::kKeys - first_key / H::kKeys;
+      n = static_cast<long>(a.kv_heads) * (kSetup + tiles);
+    }
+    const long before = block_scan<kPlanThreads>(n, warp_sum, entries);
+    if (r < n_tiles) starts[r] = before;
+  }
+  if (threadIdx.x == 0) starts[n_tiles] = entries;
+  if (flags) atomicOr(status, flags);
+}
+
+// A CTA's part of a segment.
+struct Piece {
   int b, kvh, row0, rows, halves;  // rows: of the request
-  int lo, hi, tiles;               // keys [lo, hi) are seen by some row; tiles from lo / kKeys
+  int lo, hi;                      // keys [lo, hi) are seen by some row
+  int first, tiles;                // its key tiles
+  bool alone;                      // it is the whole segment
+  bool head;                       // the segment begins with it
+  int cta0, cta1;                  // CTAs of the segment's pieces
   SeqInfo sq;
 };
-__device__ __forceinline__ Unit unit_of(const AttnArgs& a, long u, const SeqInfo* info,
-                                        const long* starts) {
-  int lo = 0, hi = a.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (starts[mid] <= u) lo = mid;
-    else hi = mid;
+
+// Walks a CTA's range of the list. Every warp keeps one; a cut that falls into
+// a segment's first kSetup entries moves to its beginning.
+template <int D>
+struct Cursor {
+  using H = Shape<D>;
+  long at, end, per;
+  int r;
+  __device__ __forceinline__ void begin(const long* starts, int n_tiles, int lane) {
+    const long total = starts[n_tiles];
+    per = (total + gridDim.x - 1) / gridDim.x;
+    if (per < kMinTiles) per = kMinTiles;
+    at = blockIdx.x * per;
+    end = min(total, at + per);
+    int lo = 0, hi = n_tiles;  // the last row tile that starts at or before `at`
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, probe = lo + lane * step;
+      const unsigned below = __ballot_sync(~0u, probe < hi && starts[probe] <= at);
+      const int k = below ? 31 - __clz(below) : 0;
+      lo += k * step;
+      hi = min(hi, lo + step);
+    }
+    r = lo;
   }
-  Unit r;
-  r.b = lo;
-  r.sq = info[lo];
-  const int group = a.heads / a.kv_heads;
-  r.rows = r.sq.q_len * group;
-  const long local = u - starts[lo];
-  const int row_tiles = (r.rows + kPromptTile - 1) / kPromptTile;
-  r.kvh = static_cast<int>(local % a.kv_heads);
-  r.row0 = (row_tiles - 1 - static_cast<int>(local / a.kv_heads)) * kPromptTile;
-  const int last = min(r.rows, r.row0 + kPromptTile) - 1;
-  r.halves = last >= r.row0 + kHalf ? 2 : 1;
-  const int before = r.sq.len - r.sq.q_len;
-  const int p0 = before + r.row0 / group, p1 = before + last / group;
-  r.lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
-  r.hi = p1 + 1;
-  r.tiles = r.hi <= 0 ? 0 : (r.hi + kKeys - 1) / kKeys - r.lo / kKeys;
-  return r;
+  __device__ __forceinline__ bool next(const AttnArgs& a, const SeqInfo* info,
+                                       const RowTile* row_tiles, const long* starts, Piece& p) {
+    if (at >= end) return false;
+    while (starts[r + 1] <= at) ++r;
+    const RowTile rt = row_tiles[r];
+    p.b = rt.b;
+    p.row0 = rt.row0;
+    p.sq = info[rt.b];
+    const int group = a.heads / a.kv_heads;
+    p.rows = p.sq.q_len * group;
+    const int last = min(p.rows, p.row0 + H::kTile) - 1;
+    p.halves = last >= p.row0 + kHalf ? 2 : 1;
+    const int before = p.sq.len - p.sq.q_len;
+    p.lo = a.window > 0 ? max(0, before + p.row0 / group - a.window + 1) : 0;
+    p.hi = before + last / group + 1;
+    const int tiles = p.hi <= 0 ? 0 : (p.hi + H::kKeys - 1) / H::kKeys - p.lo / H::kKeys;
+    const int len = kSetup + tiles, snap = kSetup + (tiles > 0);
+    p.kvh = static_cast<int>((at - starts[r]) / len);
+    const long seg = starts[r] + static_cast<long>(p.kvh) * len;
+    if (at - seg < snap) at = seg;
+    if (end - seg < snap) return false;  // a later CTA takes all of it
+    const int p0 = static_cast<int>(at - seg), p1 = static_cast<int>(min(seg + len, end) - seg);
+    const int t0 = max(0, p0 - kSetup);
+    p.first = p.lo / H::kKeys + t0;
+    p.tiles = p1 - kSetup - t0;
+    p.head = p0 == 0;
+    p.alone = p0 == 0 && p1 == len;
+    p.cta0 = static_cast<int>((seg + kSetup) / per);
+    p.cta1 = static_cast<int>((seg + len - 1) / per);
+    at = seg + p1;
+    return true;
+  }
+};
+
+// One row of bf16 output from N sums and their factor.
+template <int N>
+__device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float* v, float f) {
+#pragma unroll
+  for (int i = 0; i < N / 8; ++i) {
+    uint32_t h[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const __nv_bfloat162 b2 =
+          __floats2bfloat162_rn(v[8 * i + 2 * q] * f, v[8 * i + 2 * q + 1] * f);
+      h[q] = *reinterpret_cast<const uint32_t*>(&b2);
+    }
+    reinterpret_cast<uint4*>(dst)[i] = make_uint4(h[0], h[1], h[2], h[3]);
+  }
 }
 
 template <int D>
-struct RawTile {
-  Words<D / 8> k;   // one key row
-  uint32_t ks[D / 64];
-  uint2 v[8];       // 16 channels of eight value rows
-  uint32_t vs[2];   // and their scales
-  uint32_t bad;     // key rows of this warp on a bad page
-};
-
-template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_prompt_kernel(AttnArgs a, unsigned* status, const SeqInfo* info, const long* starts,
-                       int* ticket) {
-  using S = Smem<D>;
+    attn_prompt_kernel(AttnArgs a, unsigned* status, int* counters, const SeqInfo* info,
+                       const int* firsts, const RowTile* row_tiles, const long* starts,
+                       float2* stats, float4* partial) {
+  using H = Shape<D>;
+  constexpr int kKeys = H::kKeys;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars bars;
-  __shared__ int s_units[2];
   __shared__ __align__(16) uint32_t s_bad[kBadRing][4];
   __shared__ uint32_t s_tmem;
+  __shared__ int s_last[2];
   __shared__ volatile int s_abort;
   const uint32_t base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sm_q = base, sm_k = base + 2 * S::kQ, sm_v = sm_k + 2 * S::kK;
+  const uint32_t sm_q = base, sm_k = base + H::kHalves * H::kQ, sm_v = sm_k + 2 * H::kK;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto bar = [&](const uint64_t& b) { return ptx::smem_u32(&b); };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(bar(bars.unit_full[i]), 1);
-      ptx::mbar_init(bar(bars.unit_empty[i]), kWarpsAll);
       ptx::mbar_init(bar(bars.q_ready[i]), 4);
       ptx::mbar_init(bar(bars.k_full[i]), kFillWarps);
       ptx::mbar_init(bar(bars.k_empty[i]), 1);
@@ -223,6 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(bar(bars.s_full[i]), 1);
       ptx::mbar_init(bar(bars.p_ready[i]), 4);
       ptx::mbar_init(bar(bars.o_done[i]), 1);
+      ptx::mbar_init(bar(bars.written[i]), 4);
+      ptx::mbar_init(bar(bars.joined[i]), 1);
     }
     ptx::mbar_init(bar(bars.drain), 1);
     ptx::fence_barrier_init();
@@ -237,7 +380,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = s_tmem;
   pdl_enter();
-  const long total = starts[a.B];
   const int group = a.heads / a.kv_heads;
   auto wait = [&](const uint64_t& b, uint32_t parity) {
     return ptx::mbar_wait(bar(b), parity, &s_abort, status);
@@ -247,17 +389,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait_warp = [&](const uint64_t& b, uint32_t parity) {
     return __all_sync(~0u, wait(b, parity)) != 0;
   };
-  // The next unit of the ring for a warp of any role (-1: none, or a timeout).
-  uint32_t turn = 0;
-  auto next_unit = [&]() -> long {
-    const uint32_t slot = turn & 1, parity = (turn >> 1) & 1;
-    ++turn;
-    if (!wait_warp(bars.unit_full[slot], parity)) return -1;
-    const int u = *reinterpret_cast<volatile int*>(&s_units[slot]);
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(bar(bars.unit_empty[slot]));
-    return u;
-  };
+  Cursor<D> cur;
+  Piece t;
+  auto begin = [&] { cur.begin(starts, firsts[a.B], lane); };
+  auto next = [&] { return cur.next(a, info, row_tiles, starts, t); };
 
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
@@ -265,26 +400,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int x = warp >> 2;
     const int row_l = (warp & 3) * 32 + lane;  // row of the half, lane of tensor memory
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
-    const uint32_t ts = tmem + lanes + kColsS + x * kHalf, to = tmem + lanes + kColsO + x * D;
-    uint32_t s_phase = 0, o_phase = 0, tile_no = 0;
-    for (;;) {
-      const long u = next_unit();
-      if (u < 0) break;
-      const Unit t = unit_of(a, u, info, starts);
+    const uint32_t ts = tmem + lanes + kColsS + x * kKeys, to = tmem + lanes + kColsO + x * D;
+    uint32_t s_phase = 0, o_phase = 0, join_phase = 0, tile_no = 0;
+    begin();
+    while (x < H::kHalves && next()) {
+      if (x >= t.halves) {
+        tile_no += t.tiles;
+        continue;
+      }
       const int r = t.row0 + x * kHalf + row_l;
       const bool live = r < t.rows;
       const int tok = r / group, head = t.kvh * group + (r - tok * group);
-      if (x < t.halves && t.tiles > 0) {
-        // this row's queries, scaled to f16
+      const long at_row = static_cast<long>(t.sq.q0 + tok) * a.heads + head;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + at_row * D;
+      if (t.tiles == 0) {  // no row of the segment sees a key
+        if (live) {
+          for (int i = 0; i < D / 8; ++i)
+            reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
+          if (a.lse) a.lse[at_row] = -INFINITY;
+        }
+        continue;
+      }
+      float gain;
+      {  // this row's queries, scaled to f16
         const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q.p) +
                                    (t.sq.q0 + (live ? tok : 0)) * a.q.token +
                                    (live ? head : 0) * a.q.head;
-        uint4 w[D / 8];
         float top = 0.0f;
-#pragma unroll
+#pragma unroll 8
         for (int i = 0; i < D / 8; ++i) {
-          w[i] = live ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0, 0, 0, 0);
-          const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          const uint4 w = live ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0, 0, 0, 0);
+          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[j] << 16)),
@@ -292,242 +438,320 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float up, down;
         row_power(top, up, down);
-        const float gain = down * a.scale_log2;
-#pragma unroll
+        gain = down * a.scale_log2;
+#pragma unroll 8
         for (int i = 0; i < D / 8; ++i) {
-          const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          const uint4 w = live ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0, 0, 0, 0);
+          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
           uint32_t h[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             h[j] = pack_f16(__uint_as_float(v[j] << 16) * up,
                             __uint_as_float(v[j] & 0xffff0000u) * up);
-          sts128(sm_q + x * S::kQ + swizzled(row_l, i, kHalf), h[0], h[1], h[2], h[3]);
+          sts128(sm_q + x * H::kQ + swizzled(row_l, i, kHalf), h[0], h[1], h[2], h[3]);
         }
         ptx::fence_proxy_async();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(bars.q_ready[x]));
-
-        const int p = t.sq.len - t.sq.q_len + tok;
-        const int last = live ? p : 0x7fffffff;
-        const int first = live && a.window > 0 ? p - a.window + 1 : 0;
-        // keys that every row of the half sees
-        const int r_lo = t.row0 + x * kHalf, r_hi = min(t.rows, r_lo + kHalf) - 1;
-        const int all_last = t.sq.len - t.sq.q_len + r_lo / group;
-        const int all_first =
-            a.window > 0 ? t.sq.len - t.sq.q_len + r_hi / group - a.window + 1 : 0;
-        float m = -INFINITY, mbase = -kLift, l = 0.0f;
-        bool ok = true;
-        for (int j = 0; j < t.tiles; ++j, ++tile_no) {
-          if (!(ok = wait_warp(bars.s_full[x], s_phase))) break;
-          s_phase ^= 1;
-          ptx::tc_fence_after();
-          const int tok0 = (t.lo / kKeys + j) * kKeys;
-          const uint4 bad = lds128(ptx::smem_u32(s_bad[tile_no % kBadRing]));
-          const bool whole = tok0 >= all_first && tok0 + kKeys - 1 <= all_last &&
-                             (bad.x | bad.y | bad.z | bad.w) == 0;
-          uint32_t pk[kKeys / 2];
-          float sum;
-          bool over;  // a P has outgrown the lag allowed to the maximum
-          auto visible = [&](int c, uint32_t(&v)[32]) {
-            const uint32_t bits = c == 0 ? bad.x : c == 1 ? bad.y : c == 2 ? bad.z : bad.w;
+      }
+      const int p = t.sq.len - t.sq.q_len + tok;
+      const int last = live ? p : 0x7fffffff;
+      const int first = live && a.window > 0 ? p - a.window + 1 : 0;
+      // keys that every row of the half sees
+      const int r_lo = t.row0 + x * kHalf, r_hi = min(t.rows, r_lo + kHalf) - 1;
+      const int all_last = t.sq.len - t.sq.q_len + r_lo / group;
+      const int all_first = a.window > 0 ? t.sq.len - t.sq.q_len + r_hi / group - a.window + 1 : 0;
+      float m = -INFINITY, mbase = -kLift;  // m: a whole number
+      uint64_t l2[2] = {0, 0};              // partial sums of P
+      const uint64_t gain2 = pair_f32(gain, gain);
+      bool ok = true;
+      for (int j = 0; j < t.tiles; ++j, ++tile_no) {
+        if (!(ok = wait_warp(bars.s_full[x], s_phase))) break;
+        s_phase ^= 1;
+        ptx::tc_fence_after();
+        const int tok0 = (t.first + j) * kKeys;
+        const uint32_t bad_at = ptx::smem_u32(s_bad[tile_no % kBadRing]);
+        const uint4 bad = lds128(bad_at);
+        const bool whole = tok0 >= all_first && tok0 + kKeys - 1 <= all_last &&
+                           (bad.x | bad.y | bad.z | bad.w) == 0;
+        uint32_t v[2][32];
+        tmem_ld32(ts, v[0]);
+#pragma unroll 1
+        for (int c2 = 0; c2 < kKeys / 64; ++c2) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int key = tok0 + 32 * c + i;
-              if (key < first || key > last || ((bits >> i) & 1u)) v[i] = 0xff800000u;
+          for (int e = 0; e < 2; ++e) {
+            const int c = 2 * c2 + e;
+            uint32_t(&s)[32] = v[e];
+            tmem_landed(s);
+            // the next columns come while these are worked on
+            if (e == 0 || c2 + 1 < kKeys / 64) tmem_ld32(ts + 32 * (c + 1), v[e ^ 1]);
+            if (!whole) {
+              const uint32_t bits = lds32(bad_at + 4 * c);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const int key = tok0 + 32 * c + i;
+                if (key < first || key > last || ((bits >> i) & 1u)) s[i] = 0xff800000u;
+              }
             }
-          };
-          auto pass = [&](bool masked) {
-            const uint64_t gain2 = pair_f32(gain, gain), off2 = pair_f32(-mbase, -mbase);
-            uint64_t sums[2] = {0, 0};
-            uint32_t top = 0;
-#pragma unroll
-            for (int c = 0; c < kKeys / 32; ++c) {
-              uint32_t v[32];
-              tmem_ld32(ts + 32 * c, v);
-              if (masked) visible(c, v);
+            uint32_t pk[16], top = 0;
+            uint64_t add[2] = {0, 0};
+            auto expo = [&] {
+              const uint64_t off2 = pair_f32(-mbase, -mbase);
+              add[0] = add[1] = 0;
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 float x0, x1;
-                unpair_f32(fma_f32x2(pair_b32(v[2 * i], v[2 * i + 1]), gain2, off2), x0, x1);
+                unpair_f32(fma_f32x2(pair_b32(s[2 * i], s[2 * i + 1]), gain2, off2), x0, x1);
                 const float p0 = ex2(x0), p1 = ex2(x1);
-                sums[i & 1] = add_f32x2(sums[i & 1], pair_f32(p0, p1));
-                pk[16 * c + i] = pack_f16(p0, p1);
-                top = max_f16x2(top, pk[16 * c + i]);
+                add[i & 1] = add_f32x2(add[i & 1], pair_f32(p0, p1));
+                pk[i] = pack_f16(p0, p1);
+                top = max_f16x2(top, pk[i]);
               }
-            }
-            float s0, s1;
-            unpair_f32(add_f32x2(sums[0], sums[1]), s0, s1);
-            sum = s0 + s1;
+            };
+            expo();
             const float2 t2 = unpack_f16(top);
-            over = fmaxf(t2.x, t2.y) > kMostP;
-          };
-          if (whole) pass(false);
-          else pass(true);
-          if (__any_sync(~0u, over || m == -INFINITY)) {
-            float mx = -INFINITY;
+            if (__any_sync(~0u, fmaxf(t2.x, t2.y) > kMostP || m == -INFINITY)) {
+              if (e == 0 || c2 + 1 < kKeys / 64) tmem_landed(v[e ^ 1]);
+              float mx = __uint_as_float(s[0]);
+#pragma unroll
+              for (int i = 1; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(s[i]));
+              const float nm = fmaxf(m, ceilf(mx * gain));
+              const float nb = nm == -INFINITY ? -kLift : nm - kLift;
+              const float f = m == -INFINITY ? 0.0f : ex2(mbase - nb);
+              m = nm;
+              mbase = nb;
+              l2[0] = fma_f32x2(l2[0], pair_f32(f, f), 0);
+              l2[1] = fma_f32x2(l2[1], pair_f32(f, f), 0);
+              tmem_wait_st();
 #pragma unroll 1
-            for (int c = 0; c < kKeys / 32; ++c) {
-              uint32_t v[32];
-              tmem_ld32(ts + 32 * c, v);
-              if (!whole) visible(c, v);
+              for (int q = 0; q < c; q += 2) {  // P of this tile's earlier columns
+                uint32_t w[32];
+                tmem_ld32(ts + 16 * q, w);
+                tmem_landed(w);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(v[i]));
-            }
-            const float nm = fmaxf(m, mx * gain);
-            const float nb = nm == -INFINITY ? -kLift : nm - kLift;
-            const float f = m == -INFINITY ? 0.0f : ex2(mbase - nb);
-            l *= f;
-            m = nm;
-            mbase = nb;
-            if (j > 0) {  // the products of the tiles before have all landed (s_full)
+                for (int i = 0; i < 32; ++i) {
+                  if (q + 1 == c && i >= 16) break;
+                  const float2 g2 = unpack_f16(w[i]);
+                  w[i] = pack_f16(g2.x * f, g2.y * f);
+                }
+                if (q + 1 < c) {
+                  tmem_st32(ts + 16 * q, w);
+                } else {
+                  uint32_t w16[16];
 #pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t v[32];
-                tmem_ld32(to + 32 * c, v);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-                tmem_st32(to + 32 * c, v);
+                  for (int i = 0; i < 16; ++i) w16[i] = w[i];
+                  tmem_st16(ts + 16 * q, w16);
+                }
               }
+              if (j > 0) {  // the products of the tiles before have all landed (s_full)
+#pragma unroll 1
+                for (int q = 0; q < D / 32; ++q) {
+                  uint32_t w[32];
+                  tmem_ld32(to + 32 * q, w);
+                  tmem_landed(w);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
+                  tmem_st32(to + 32 * q, w);
+                }
+              }
+              expo();
             }
-            if (whole) pass(false);
-            else pass(true);
+            l2[0] = add_f32x2(l2[0], add[0]);
+            l2[1] = add_f32x2(l2[1], add[1]);
+            tmem_st16(ts + 16 * c, pk);
           }
-          l += sum;
-#pragma unroll
-          for (int c = 0; c < kKeys / 64; ++c) tmem_st32(ts + 32 * c, pk + 32 * c);
-          tmem_wait_st();
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bar(bars.p_ready[x]));
         }
-        if (!ok || !wait_warp(bars.o_done[x], o_phase)) break;
-        o_phase ^= 1;
-        ptx::tc_fence_after();
+        tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(bars.p_ready[x]));
+      }
+      if (!ok || !wait_warp(bars.o_done[x], o_phase)) break;
+      o_phase ^= 1;
+      ptx::tc_fence_after();
+      float l;
+      {
+        float l0, l1;
+        unpair_f32(add_f32x2(l2[0], l2[1]), l0, l1);
+        l = l0 + l1;
+      }
+      if (t.alone) {
         const float f = out_factor(l, a.v_scale);
-        const long at_row = static_cast<long>(t.sq.q0 + tok) * a.heads + head;
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + at_row * D;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t v[32];
           tmem_ld32(to + 32 * c, v);
-          if (live) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t h[4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const __nv_bfloat162 b2 =
-                    __floats2bfloat162_rn(__uint_as_float(v[8 * i + 2 * q]) * f,
-                                          __uint_as_float(v[8 * i + 2 * q + 1]) * f);
-                h[q] = *reinterpret_cast<const uint32_t*>(&b2);
-              }
-              *reinterpret_cast<uint4*>(dst + 32 * c + 8 * i) = make_uint4(h[0], h[1], h[2], h[3]);
-            }
-          }
+          tmem_landed(v);
+          if (live) store_row<32>(dst + 32 * c, reinterpret_cast<const float*>(v), f);
         }
         if (live && a.lse) a.lse[at_row] = log_sum(mbase, l);
         ptx::tc_fence_before();
-      } else if (x < t.halves) {
-        // no row of the unit sees a key
-        if (live) {
-          const long at_row = static_cast<long>(t.sq.q0 + tok) * a.heads + head;
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at_row * D);
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0, 0, 0, 0);
-          if (a.lse) a.lse[at_row] = -INFINITY;
-        }
-      } else {
-        tile_no += t.tiles;
+        continue;
       }
+      // A piece: sums [D / 4][row] and statistics [row] to the workspace, lanes
+      // at neighbouring rows. The CTA a segment begins in keeps its piece in
+      // slot 1, later ones in slot 0.
+      auto slot_of = [&](int cta) {
+        return (2l * cta + (cta == t.cta0)) * H::kHalves + x;
+      };
+      {
+        const long slot = slot_of(blockIdx.x);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(to + 32 * c, v);
+          tmem_landed(v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            partial[(slot * (D / 4) + 8 * c + i) * kHalf + row_l] =
+                make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                            __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+        }
+        stats[slot * kHalf + row_l] = make_float2(m == -INFINITY ? -INFINITY : mbase, l);
+      }
+      ptx::tc_fence_before();
+      __threadfence();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(bars.written[x]));
+      if ((warp & 3) == 0) {
+        if (!wait_warp(bars.written[x], join_phase)) break;
+        if (lane == 0) {
+          __threadfence();
+          *reinterpret_cast<volatile int*>(&s_last[x]) =
+              ptx::add_acq_rel(counters + 2 * t.cta0 + x, 1) == t.cta1 - t.cta0;
+          ptx::mbar_arrive(bar(bars.joined[x]));
+        }
+      }
+      if (!wait_warp(bars.joined[x], join_phase)) break;
+      join_phase ^= 1;
+      if (!*reinterpret_cast<volatile int*>(&s_last[x])) continue;
+      __threadfence();
+      float top = -INFINITY, den = 0.0f;
+#pragma unroll 4
+      for (int k = t.cta0; k <= t.cta1; ++k)
+        top = fmaxf(top, __ldcg(&stats[slot_of(k) * kHalf + row_l]).x);
+      auto weight = [&](float b2) { return b2 == -INFINITY ? 0.0f : ex2(b2 - top); };
+      for (int k = t.cta0; k <= t.cta1; ++k) {
+        const float2 st = __ldcg(&stats[slot_of(k) * kHalf + row_l]);
+        den += weight(st.x) * st.y;
+      }
+      const float f = out_factor(den, a.v_scale);
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        float sum[32] = {};
+#pragma unroll 1
+        for (int k = t.cta0; k <= t.cta1; ++k) {
+          const long slot = slot_of(k);
+          const float w = weight(__ldcg(&stats[slot * kHalf + row_l]).x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 v = __ldcg(&partial[(slot * (D / 4) + 8 * c + i) * kHalf + row_l]);
+            sum[4 * i] += w * v.x, sum[4 * i + 1] += w * v.y;
+            sum[4 * i + 2] += w * v.z, sum[4 * i + 3] += w * v.w;
+          }
+        }
+        if (live) store_row<32>(dst + 32 * c, sum, f);
+      }
+      if (live && a.lse) a.lse[at_row] = log_sum(top, den);
     }
   } else if (warp < kMmaWarp) {
     // ------------------------------------------------- codes to f16 operands
-    const int ft = threadIdx.x - kSoftWarps * 32;   // 0..127: key row of the tile
-    const int fw = warp - kSoftWarps;
-    // values: eight tokens from vt, 16 channels from vc (D = 64: half the threads)
-    const int vt = ((lane & 7) + 8 * (fw & 1)) * 8, vg = (lane >> 3) + 4 * (fw >> 1);
+    const int ft = threadIdx.x - kSoftWarps * 32, fw = warp - kSoftWarps;
+    // keys: a row, or a half of its 256 channels
+    constexpr int kParts = 128 / kKeys, kChans = D / kParts;
+    const int kr = ft % kKeys, kpart = ft / kKeys;
+    // values: eight tokens from vt, 16 channels from 16 * vg. Eight neighbouring
+    // lanes have different tokens and the same channels: their 16-byte stores
+    // fall on the eight chunks of one 128-byte row.
+    constexpr int kGroups = kKeys / 8;
+    const int vt = (kGroups == 16 ? (lane & 7) + 8 * (fw & 1) : lane & 7) * 8;
+    const int vg = kGroups == 16 ? (lane >> 3) + 4 * (fw >> 1) : ft >> 3;
     const bool has_v = vg < D / kKvGroup;
     const KvBlock blk = kv_block(a.page_size, D);
     const int page_mask = a.page_size - 1, page_shift = 31 - __clz(a.page_size);
-    uint32_t kc = 0, produced = 0;
-    for (;;) {
-      if (fw == 0 && lane == 0) {  // draw a unit for everybody
-        const uint32_t slot = produced & 1;
-        if (wait(bars.unit_empty[slot], ((produced >> 1) & 1) ^ 1)) {
-          const long u = atomicAdd(ticket, 1);
-          *reinterpret_cast<volatile int*>(&s_units[slot]) = u < total ? static_cast<int>(u) : -1;
-        } else {
-          *reinterpret_cast<volatile int*>(&s_units[slot]) = -1;
-        }
-        ptx::mbar_arrive(bar(bars.unit_full[slot]));
-        ++produced;
-      }
-      __syncwarp();
-      const long u = next_unit();
-      if (u < 0) break;
-      const Unit t = unit_of(a, u, info, starts);
+    uint32_t kc = 0;
+    begin();
+    while (next()) {
       const int32_t* pages = a.page_table + static_cast<long>(t.b) * a.max_pages;
-      RawTile<D> raw;
-      auto fetch = [&](int j) {
-        const int tok0 = (t.lo / kKeys + j) * kKeys;
-        // the block of keys key .. key + more, of which some row sees one
-        auto block_of = [&](int key, int more, bool& ok) -> const uint8_t* {
-          const int id = key < t.hi && key + more >= t.lo ? pages[key >> page_shift] : 0;
-          ok = id >= 0 && id < a.num_pages;
-          return a.cache + (static_cast<long>(ok ? id : 0) * a.kv_heads + t.kvh) * blk.bytes;
-        };
-        bool ok;
-        const uint8_t* p = block_of(tok0 + ft, 0, ok);
-        const int kr = (tok0 + ft) & page_mask;
-        raw.k = load_words<D / 8>(p + kr * (D / 2));
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i)
-          raw.ks[i] = *reinterpret_cast<const uint32_t*>(p + blk.k_scale + kr * (D / 16) + 4 * i);
-        raw.bad = __ballot_sync(~0u, !ok);
-        if (has_v) {
-          p = block_of(tok0 + vt, 7, ok);
-          const int vr = (tok0 + vt) & page_mask;
-          raw.vs[0] = raw.vs[1] = 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            raw.v[i] = *reinterpret_cast<const uint2*>(p + blk.v_code + (vr + i) * (D / 2) + vg * 8);
-            // a key that no row sees may be uninitialised memory: a zero scale
-            // keeps 0 * NaN out of the sum
-            const int key = tok0 + vt + i;
-            const uint32_t s = p[blk.v_scale + (vr + i) * (D / 16) + vg];
-            raw.vs[i >> 2] |= (ok && key >= t.lo && key < t.hi ? s : 0u) << (8 * (i & 3));
-          }
-        }
+      // The page of keys key .. key + more (0 where no row sees one of them).
+      auto page_of = [&](int key, int more) {
+        return key < t.hi && key + more >= t.lo ? pages[key >> page_shift] : 0;
       };
-      if (t.tiles > 0) fetch(0);
+      auto block_of = [&](int id, bool& ok) {
+        ok = id >= 0 && id < a.num_pages;
+        return a.cache + (static_cast<long>(ok ? id : 0) * a.kv_heads + t.kvh) * blk.bytes;
+      };
+      // Codes and scales of the next tile and page ids of the one after it are
+      // on the way while a tile is converted.
+      Words<kChans / 8> kraw;
+      uint32_t ks[kChans / 64], vs[2] = {0, 0};
+      uint2 vraw[8];
+      bool k_ok = true;
+      int kid = page_of(t.first * kKeys + kr, 0), vid = page_of(t.first * kKeys + vt, 7);
+      auto fetch_k = [&](int j) {
+        if (j >= t.tiles) return;
+        const int key = (t.first + j) * kKeys + kr;
+        const uint8_t* p = block_of(kid, k_ok);
+        const int row = key & page_mask;
+        kraw = load_words<kChans / 8>(p + row * (D / 2) + kpart * (kChans / 2));
+#pragma unroll
+        for (int i = 0; i < kChans / 64; ++i)
+          ks[i] = *reinterpret_cast<const uint32_t*>(p + blk.k_scale + row * (D / 16) +
+                                                     kpart * (kChans / 16) + 4 * i);
+        if (j + 1 < t.tiles) kid = page_of(key + kKeys, 0);
+      };
+      auto fetch_v = [&](int j) {
+        if (j >= t.tiles || !has_v) return;
+        const int key0 = (t.first + j) * kKeys + vt;
+        bool ok;
+        const uint8_t* p = block_of(vid, ok);
+        const int row = key0 & page_mask;
+        vs[0] = vs[1] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          vraw[i] = *reinterpret_cast<const uint2*>(p + blk.v_code + (row + i) * (D / 2) + vg * 8);
+          // a key that no row sees may be uninitialised memory: a zero scale
+          // keeps 0 * NaN out of the sum
+          const uint32_t s = p[blk.v_scale + (row + i) * (D / 16) + vg];
+          vs[i >> 2] |= (ok && key0 + i >= t.lo && key0 + i < t.hi ? s : 0u) << (8 * (i & 3));
+        }
+        if (j + 1 < t.tiles) vid = page_of(key0 + kKeys, 7);
+      };
+      fetch_k(0);
+      fetch_v(0);
       bool ok = true;
       for (int j = 0; j < t.tiles; ++j, ++kc) {
         const uint32_t st = kc & 1, parity = ((kc >> 1) & 1) ^ 1;
         if (!(ok = wait_warp(bars.k_empty[st], parity))) break;
-        if (raw.bad && lane == 0) atomicOr(status, MOE_DEV_BAD_PAGE);
-        if (lane == 0) *reinterpret_cast<volatile uint32_t*>(&s_bad[kc % kBadRing][fw]) = raw.bad;
+        const uint32_t bad = __ballot_sync(~0u, !k_ok);
+        if (lane == 0) {
+          if (bad) atomicOr(status, MOE_DEV_BAD_PAGE);
+          // (with 64 keys, warps 2 and 3 see the same rows again)
+          *reinterpret_cast<volatile uint32_t*>(&s_bad[kc % kBadRing][fw]) = bad;
+        }
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
+        for (int c = 0; c < kChans / 8; ++c) {
           uint32_t h[4];
-          e2m1_to_f16(raw.k.w[c], h);
-          const uint32_t two = e4m3x2_to_f16(raw.ks[c / 8] >> (16 * ((c / 4) & 1)));
+          e2m1_to_f16(kraw.w[c], h);
+          const uint32_t two = e4m3x2_to_f16(ks[c / 8] >> (16 * ((c / 4) & 1)));
           const uint32_t s = (c / 2) & 1 ? f16_high_twice(two) : f16_low_twice(two);
-          sts128(sm_k + st * S::kK + swizzled(ft, c, kKeys), hmul2(h[0], s), hmul2(h[1], s),
-                 hmul2(h[2], s), hmul2(h[3], s));
+          sts128(sm_k + st * H::kK + swizzled(kr, kpart * (kChans / 8) + c, kKeys), hmul2(h[0], s),
+                 hmul2(h[1], s), hmul2(h[2], s), hmul2(h[3], s));
         }
         ptx::fence_proxy_async();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(bars.k_full[st]));
+        fetch_k(j + 1);
         if (!(ok = wait_warp(bars.v_empty[st], parity))) break;
         if (has_v) {
           uint32_t s[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[i] = e4m3x2_to_f16(raw.vs[i >> 1] >> (16 * (i & 1)));
+          for (int i = 0; i < 4; ++i) s[i] = e4m3x2_to_f16(vs[i >> 1] >> (16 * (i & 1)));
 #pragma unroll
           for (int w = 0; w < 2; ++w) {  // eight channels
             uint32_t h[8][4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) e2m1_to_f16(w ? raw.v[i].y : raw.v[i].x, h[i]);
+            for (int i = 0; i < 8; ++i) e2m1_to_f16(w ? vraw[i].y : vraw[i].x, h[i]);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const int ch = vg * 16 + w * 8 + 2 * q;
@@ -537,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                   d[i] = hmul2(__byte_perm(h[2 * i][q], h[2 * i + 1][q], o ? 0x7632 : 0x5410), s[i]);
-                sts128(sm_v + st * S::kK + swizzled(ch + o, vt / 8, D), d[0], d[1], d[2], d[3]);
+                sts128(sm_v + st * H::kK + swizzled(ch + o, vt / 8, D), d[0], d[1], d[2], d[3]);
               }
             }
           }
@@ -545,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::fence_proxy_async();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(bars.v_full[st]));
-        if (j + 1 < t.tiles) fetch(j + 1);
+        fetch_v(j + 1);
       }
       if (!ok) break;
     }
@@ -556,20 +780,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------ the matrix thread
     uint32_t kc = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
     const uint32_t id_s = ptx::idesc_make(0, kHalf, kKeys), id_o = ptx::idesc_make(0, kHalf, D);
-    for (;;) {
-      const long u = next_unit();
-      if (u < 0) break;
-      const Unit t = unit_of(a, u, info, starts);
+    begin();
+    while (next()) {
       bool ok = true;
       if (lane == 0 && t.tiles > 0) {
         auto scores = [&](int x, uint32_t st) {
 #pragma unroll
           for (int pnl = 0; pnl < D / 64; ++pnl) {
-            const uint64_t da = ptx::sdesc_sw128(sm_q + x * S::kQ + pnl * kHalf * 128);
-            const uint64_t db = ptx::sdesc_sw128(sm_k + st * S::kK + pnl * kKeys * 128);
+            const uint64_t da = ptx::sdesc_sw128(sm_q + x * H::kQ + pnl * kHalf * 128);
+            const uint64_t db = ptx::sdesc_sw128(sm_k + st * H::kK + pnl * kKeys * 128);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              ptx::tc_mma<false>(tmem + kColsS + x * kHalf, da + 2 * kk, db + 2 * kk, id_s,
+              ptx::tc_mma<false>(tmem + kColsS + x * kKeys, da + 2 * kk, db + 2 * kk, id_s,
                                  pnl + kk > 0);
           }
           ptx::tc_commit(bar(bars.s_full[x]));
@@ -577,39 +799,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto sums = [&](int x, uint32_t st, bool more) {
 #pragma unroll
           for (int pnl = 0; pnl < kKeys / 64; ++pnl) {
-            const uint64_t db = ptx::sdesc_sw128(sm_v + st * S::kK + pnl * D * 128);
+            const uint64_t db = ptx::sdesc_sw128(sm_v + st * H::kK + pnl * D * 128);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_ts(tmem + kColsO + x * D, tmem + kColsS + x * kHalf + pnl * 32 + kk * 8,
+              mma_ts(tmem + kColsO + x * D, tmem + kColsS + x * kKeys + pnl * 32 + kk * 8,
                      db + 2 * kk, id_o, more || pnl + kk > 0);
           }
         };
-        for (int x = 0; ok && x < t.halves; ++x) {
+        const int halves = t.halves, tiles = t.tiles;
+        for (int x = 0; ok && x < halves; ++x) {
           ok = wait(bars.q_ready[x], q_phase[x]);
           q_phase[x] ^= 1;
         }
         ok = ok && wait(bars.k_full[kc & 1], (kc >> 1) & 1);
         if (ok) {
           ptx::tc_fence_after();
-          for (int x = 0; x < t.halves; ++x) scores(x, kc & 1);
+          for (int x = 0; x < halves; ++x) scores(x, kc & 1);
           ptx::tc_commit(bar(bars.k_empty[kc & 1]));
         }
-        for (int j = 0; ok && j < t.tiles; ++j, ++kc) {
-          const bool again = j + 1 < t.tiles;
+        for (int j = 0; ok && j < tiles; ++j, ++kc) {
+          const bool again = j + 1 < tiles;
           const uint32_t st = kc & 1, nst = (kc + 1) & 1;
           ok = wait(bars.v_full[st], (kc >> 1) & 1);
-          for (int x = 0; ok && x < t.halves; ++x) {
+          for (int x = 0; ok && x < halves; ++x) {
             if (!(ok = wait(bars.p_ready[x], p_phase[x]))) break;
             p_phase[x] ^= 1;
             ptx::tc_fence_after();
             sums(x, st, j > 0);
-            if (x == t.halves - 1) ptx::tc_commit(bar(bars.v_empty[st]));
+            if (x == halves - 1) ptx::tc_commit(bar(bars.v_empty[st]));
             if (again) {
               // S takes the place of the P that the products before it read:
               // matrix instructions of one thread run in the order of issue
               if (x == 0 && !(ok = wait(bars.k_full[nst], ((kc + 1) >> 1) & 1))) break;
               scores(x, nst);
-              if (x == t.halves - 1) ptx::tc_commit(bar(bars.k_empty[nst]));
+              if (x == halves - 1) ptx::tc_commit(bar(bars.k_empty[nst]));
             } else {
               ptx::tc_commit(bar(bars.o_done[x]));
             }
@@ -632,22 +855,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D>
 cudaError_t launch_dim(const AttnArgs& a, void* ws, const AttnLayout& L, cudaStream_t st) {
-  static std::atomic<unsigned long long> done{0};
-  cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(&attn_prompt_kernel<D>),
-                              Smem<D>::kBytes, done);
-  if (e != cudaSuccess) return e;
   char* w = static_cast<char*>(ws);
-  return launch_pdl(&attn_prompt_kernel<D>, dim3(a.sms), dim3(kThreads), Smem<D>::kBytes, st, a,
-                    reinterpret_cast<unsigned*>(w + L.status),
-                    reinterpret_cast<const SeqInfo*>(w + L.info),
-                    reinterpret_cast<const long*>(w + L.starts),
-                    reinterpret_cast<int*>(w + L.counters));
+  auto* status = reinterpret_cast<unsigned*>(w + L.status);
+  auto* counters = reinterpret_cast<int*>(w + L.counters);
+  auto* info = reinterpret_cast<SeqInfo*>(w + L.info);
+  auto* firsts = reinterpret_cast<int*>(w + L.firsts);
+  auto* row_tiles = reinterpret_cast<RowTile*>(w + L.row_tiles);
+  auto* starts = reinterpret_cast<long*>(w + L.starts);
+  const long group = a.heads / a.kv_heads;
+  const int max_row_tiles = static_cast<int>(a.T * group / Shape<D>::kTile + a.B);
+  cudaError_t e =
+      launch_pdl(&prompt_plan_kernel<D>, dim3(1), dim3(kPlanThreads), 0, st, a, max_row_tiles,
+                 status, counters, 2 * a.sms, info, firsts, row_tiles, starts);
+  if (e != cudaSuccess) return e;
+  static std::atomic<unsigned long long> done{0};
+  e = opt_in_smem(reinterpret_cast<const void*>(&attn_prompt_kernel<D>), Shape<D>::kBytes, done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(&attn_prompt_kernel<D>, dim3(a.sms), dim3(kThreads), Shape<D>::kBytes, st, a,
+                    status, counters, const_cast<const SeqInfo*>(info),
+                    const_cast<const int*>(firsts), const_cast<const RowTile*>(row_tiles),
+                    const_cast<const long*>(starts), reinterpret_cast<float2*>(w + L.stats),
+                    reinterpret_cast<float4*>(w + L.partial));
 }
 
 }  // namespace
 
 cudaError_t launch_prompt(const AttnArgs& a, void* ws, const AttnLayout& L, cudaStream_t st) {
-  return a.D == 64 ? launch_dim<64>(a, ws, L, st) : launch_dim<128>(a, ws, L, st);
+  return a.D == 64    ? launch_dim<64>(a, ws, L, st)
+         : a.D == 128 ? launch_dim<128>(a, ws, L, st)
+                      : launch_dim<256>(a, ws, L, st);
 }
 
 }  // namespace moe

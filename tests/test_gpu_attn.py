@@ -374,6 +374,12 @@ PROMPT = [  # heads, kv heads, D, page, lens, query tokens, window (bf16, >= 64 
     (8, 8, 64, 256, [1000], [600], 300),
     (3, 1, 128, 16, [33, 5], [60, 40], 0),               # queries before the first token
     (16, 16, 128, 64, [2050], [2050], 0),                # more units than SMs
+    (4, 1, 128, 64, [9000], [16], 0),                    # few rows, long context: pieces are joined
+    (8, 2, 64, 16, [5000, 700, 64], [70, 33, 16], 0),
+    (6, 2, 128, 32, [3000], [150], 1000),
+    (4, 2, 256, 16, [40, 333], [32, 33], 0),             # 256 channels: one half, tiles of 64 keys
+    (8, 1, 256, 64, [1200], [40], 300),
+    (2, 1, 256, 128, [70], [200], 0),
 ]
 
 
@@ -390,6 +396,22 @@ def test_attention_prompt(i):
     c.out.fill_(1.0)
     c.run()
     assert torch.equal(c.out, first[0]) and torch.equal(c.lse, first[1])
+
+
+def test_attention_prompt_overlapping_offsets_stay_inside_the_tables():
+    """Offsets that give many requests the same rows: flagged, and the requests
+    that fit the list are computed."""
+    B_ = 40
+    c = Case(130, "bf16", 4, 1, 128, 16, [64] * B_, [64] + [0] * (B_ - 1))
+    offs = [0, 64] * (B_ // 2) + [0]
+    c.d["offs"].copy_(torch.tensor(offs, dtype=torch.int32))
+    c.run()
+    rc, flags = B.moe_get_status(c.ws)
+    assert rc == 5 and flags & B.DEV_BAD_SEGMENT
+    c.d["offs"].copy_(torch.from_numpy(c.offs))
+    c.run()
+    assert B.moe_get_status(c.ws) == (0, 0)
+    c.check()
 
 
 def test_attention_prompt_peaked_scores_rescale():
