@@ -51,7 +51,10 @@ constexpr int kSoftRegs = 152, kMmaRegs = 80;
 constexpr int kBadRing = 4;  // tiles whose bad-page bits are kept: a fill warp is at most
                              // two tiles ahead of the slower half
 constexpr int kSetup = 4;    // list entries of a segment beside its tiles: its set-up and store
-constexpr int kMinTiles = 8;  // smallest range of a CTA
+constexpr int kMinTiles = 16;  // smallest range of a CTA
+// A cut this near to a segment's begin or end moves there: a piece's way
+// through the workspace and the join take longer than so many tiles.
+constexpr int kSnap = 8;
 constexpr int kPlanThreads = 1024;
 constexpr float kMostP = 16384.0f;              // 2^(kLift + kLag)
 constexpr uint32_t kColsS = 0, kColsO = 256;  // columns of S and of O
@@ -63,7 +66,12 @@ struct Shape {
   static constexpr int kKeys = D == 256 ? 64 : 128;  // keys per tile
   static constexpr int kQ = kHalf * D * 2;          // bytes of one half's queries
   static constexpr int kK = kKeys * D * 2;          // of one stage of keys, or of values
-  static constexpr int kBytes = kHalves * kQ + 4 * kK + 1024;
+  // Codes and scales on their way, per fill warp: 32 rows of up to 128 of a
+  // key's channels, and 64 tokens by 64 value channels.
+  static constexpr int kChans = D < 128 ? D : 128;
+  static constexpr int kRawKs = 32 * kChans / 2, kRawV = kRawKs + 32 * kChans / 16;
+  static constexpr int kRawVs = kRawV + 64 * 32, kRaw = kRawVs + 64 * 4;
+  static constexpr int kBytes = kHalves * kQ + 4 * kK + kFillWarps * kRaw + 1024;
 };
 
 struct Bars {
@@ -179,6 +187,22 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+// 4 or 8 bytes global -> shared.
+template <int N>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+
 // Byte offset of 16-byte chunk `chunk` of row `row` in a 128-byte-swizzled
 // operand whose panels (64 f16 wide) hold `rows` rows.
 __device__ __forceinline__ uint32_t swizzled(int row, int chunk, int rows) {
@@ -263,15 +287,16 @@ struct Piece {
   SeqInfo sq;
 };
 
-// Walks a CTA's range of the list. Every warp keeps one; a cut that falls into
-// a segment's first kSetup entries moves to its beginning.
+// Walks a CTA's range of the list, whose cuts move to a segment's ends where
+// those are near (kSnap < kMinTiles, so that no two cuts move to the same end).
+// Every warp keeps one.
 template <int D>
 struct Cursor {
   using H = Shape<D>;
-  long at, end, per;
+  long at, end, per, total;
   int r;
   __device__ __forceinline__ void begin(const long* starts, int n_tiles, int lane) {
-    const long total = starts[n_tiles];
+    total = starts[n_tiles];
     per = (total + gridDim.x - 1) / gridDim.x;
     if (per < kMinTiles) per = kMinTiles;
     at = blockIdx.x * per;
@@ -288,43 +313,53 @@ struct Cursor {
   }
   __device__ __forceinline__ bool next(const AttnArgs& a, const SeqInfo* info,
                                        const RowTile* row_tiles, const long* starts, Piece& p) {
-    if (at >= end) return false;
-    while (starts[r + 1] <= at) ++r;
-    const RowTile rt = row_tiles[r];
-    p.b = rt.b;
-    p.row0 = rt.row0;
-    p.sq = info[rt.b];
-    const int group = a.heads / a.kv_heads;
-    p.rows = p.sq.q_len * group;
-    const int last = min(p.rows, p.row0 + H::kTile) - 1;
-    p.halves = last >= p.row0 + kHalf ? 2 : 1;
-    const int before = p.sq.len - p.sq.q_len;
-    p.lo = a.window > 0 ? max(0, before + p.row0 / group - a.window + 1) : 0;
-    p.hi = before + last / group + 1;
-    const int tiles = p.hi <= 0 ? 0 : (p.hi + H::kKeys - 1) / H::kKeys - p.lo / H::kKeys;
-    const int len = kSetup + tiles, snap = kSetup + (tiles > 0);
-    p.kvh = static_cast<int>((at - starts[r]) / len);
-    const long seg = starts[r] + static_cast<long>(p.kvh) * len;
-    if (at - seg < snap) at = seg;
-    if (end - seg < snap) return false;  // a later CTA takes all of it
-    const int p0 = static_cast<int>(at - seg), p1 = static_cast<int>(min(seg + len, end) - seg);
-    const int t0 = max(0, p0 - kSetup);
-    p.first = p.lo / H::kKeys + t0;
-    p.tiles = p1 - kSetup - t0;
-    p.head = p0 == 0;
-    p.alone = p0 == 0 && p1 == len;
-    p.cta0 = static_cast<int>((seg + kSetup) / per);
-    p.cta1 = static_cast<int>((seg + len - 1) / per);
-    at = seg + p1;
-    return true;
+    for (;;) {
+      if (at >= end) return false;
+      while (starts[r + 1] <= at) ++r;
+      const RowTile rt = row_tiles[r];
+      p.b = rt.b;
+      p.row0 = rt.row0;
+      p.sq = info[rt.b];
+      const int group = a.heads / a.kv_heads;
+      p.rows = p.sq.q_len * group;
+      const int last = min(p.rows, p.row0 + H::kTile) - 1;
+      p.halves = last >= p.row0 + kHalf ? 2 : 1;
+      const int before = p.sq.len - p.sq.q_len;
+      p.lo = a.window > 0 ? max(0, before + p.row0 / group - a.window + 1) : 0;
+      p.hi = before + last / group + 1;
+      const int tiles = p.hi <= 0 ? 0 : (p.hi + H::kKeys - 1) / H::kKeys - p.lo / H::kKeys;
+      const int len = kSetup + tiles;
+      p.kvh = static_cast<int>((at - starts[r]) / len);
+      const long seg = starts[r] + static_cast<long>(p.kvh) * len;
+      int p0 = static_cast<int>(at - seg);
+      if (p0 <= kSnap) {
+        p0 = 0;
+      } else if (len - p0 <= kSnap) {  // the CTA before takes all of it
+        at = seg + len;
+        continue;
+      }
+      int p1 = static_cast<int>(min(static_cast<long>(len), end - seg));
+      if (p1 < len && p1 <= kSnap) return false;  // the next CTA takes all of it
+      if (len - p1 <= kSnap) p1 = len;
+      const int t0 = max(0, p0 - kSetup);
+      p.first = p.lo / H::kKeys + t0;
+      p.tiles = p1 - kSetup - t0;
+      p.head = p0 == 0;
+      p.alone = p0 == 0 && p1 == len;
+      p.cta0 = static_cast<int>((seg + kSnap) / per);
+      p.cta1 = max(p.cta0, static_cast<int>((seg + len - kSnap - 1) / per));
+      at = seg + p1;
+      return true;
+    }
   }
 };
 
-// One row of bf16 output from N sums and their factor.
-template <int N>
-__device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float* v, float f) {
+// 32 columns of a row, as bf16, to its place in a half's staging rows (laid out
+// like the half's queries, which no matrix instruction reads any more).
+__device__ __forceinline__ void stage_columns(uint32_t rows, int row, int c, const float* v,
+                                              float f) {
 #pragma unroll
-  for (int i = 0; i < N / 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     uint32_t h[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -332,7 +367,7 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float* v, fl
           __floats2bfloat162_rn(v[8 * i + 2 * q] * f, v[8 * i + 2 * q + 1] * f);
       h[q] = *reinterpret_cast<const uint32_t*>(&b2);
     }
-    reinterpret_cast<uint4*>(dst)[i] = make_uint4(h[0], h[1], h[2], h[3]);
+    sts128(rows + swizzled(row, 4 * c + i, kHalf), h[0], h[1], h[2], h[3]);
   }
 }
 
@@ -382,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_enter();
   const int group = a.heads / a.kv_heads;
   auto wait = [&](const uint64_t& b, uint32_t parity) {
-    return ptx::mbar_wait(bar(b), parity, &s_abort, status);
+    return ptx::mbar_wait_asleep(bar(b), parity, &s_abort, status);
   };
   // The same for a whole warp: all lanes go on or none (a timeout may reach
   // some lanes only, and tensor memory is read by whole warps).
@@ -401,6 +436,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row_l = (warp & 3) * 32 + lane;  // row of the half, lane of tensor memory
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
     const uint32_t ts = tmem + lanes + kColsS + x * kKeys, to = tmem + lanes + kColsO + x * D;
+    const uint32_t sm_rows = sm_q + x * H::kQ;
+    // rows are read and written by kRowLanes lanes of 16 bytes, several at once
+    constexpr int kRowLanes = D / 8, kRowsStep = 32 / kRowLanes, kSteps = kRowLanes;
     uint32_t s_phase = 0, o_phase = 0, join_phase = 0, tile_no = 0;
     begin();
     while (x < H::kHalves && next()) {
@@ -412,43 +450,72 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = r < t.rows;
       const int tok = r / group, head = t.kvh * group + (r - tok * group);
       const long at_row = static_cast<long>(t.sq.q0 + tok) * a.heads + head;
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + at_row * D;
+      // the warp's staged rows to the output
+      auto store_rows = [&] {
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < kSteps; ++i) {
+          const int rl = i * kRowsStep + lane / kRowLanes;
+          const long row = __shfl_sync(~0u, at_row, rl);
+          const bool there = __shfl_sync(~0u, static_cast<int>(live), rl);
+          const uint4 v =
+              lds128(sm_rows + swizzled((warp & 3) * 32 + rl, lane % kRowLanes, kHalf));
+          if (there)
+            reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D)[lane % kRowLanes] = v;
+        }
+        __syncwarp();
+      };
       if (t.tiles == 0) {  // no row of the segment sees a key
         if (live) {
-          for (int i = 0; i < D / 8; ++i)
-            reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at_row * D);
+          for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0, 0, 0, 0);
           if (a.lse) a.lse[at_row] = -INFINITY;
         }
         continue;
       }
-      float gain;
-      {  // this row's queries, scaled to f16
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q.p) +
-                                   (t.sq.q0 + (live ? tok : 0)) * a.q.token +
-                                   (live ? head : 0) * a.q.head;
-        float top = 0.0f;
-#pragma unroll 8
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 w = live ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0, 0, 0, 0);
-          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+      // The warp's rows of queries, whole rows by neighbouring lanes, scaled to
+      // f16; each lane keeps its own row's gain.
+      float gain = 0.0f;
+      {
+        const long src = (t.sq.q0 + (live ? tok : 0)) * a.q.token + (live ? head : 0) * a.q.head;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          uint4 w[kSteps / 2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[j] << 16)),
-                                   fabsf(__uint_as_float(v[j] & 0xffff0000u))));
-        }
-        float up, down;
-        row_power(top, up, down);
-        gain = down * a.scale_log2;
-#pragma unroll 8
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 w = live ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0, 0, 0, 0);
-          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-          uint32_t h[4];
+          for (int i = 0; i < kSteps / 2; ++i) {
+            const int rl = (half * (kSteps / 2) + i) * kRowsStep + lane / kRowLanes;
+            const long at = __shfl_sync(~0u, src, rl);
+            const bool there = __shfl_sync(~0u, static_cast<int>(live), rl);
+            w[i] = there ? *reinterpret_cast<const uint4*>(
+                               static_cast<const __nv_bfloat16*>(a.q.p) + at + lane % kRowLanes * 8)
+                         : make_uint4(0, 0, 0, 0);
+          }
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            h[j] = pack_f16(__uint_as_float(v[j] << 16) * up,
-                            __uint_as_float(v[j] & 0xffff0000u) * up);
-          sts128(sm_q + x * H::kQ + swizzled(row_l, i, kHalf), h[0], h[1], h[2], h[3]);
+          for (int i = 0; i < kSteps / 2; ++i) {
+            const int step = half * (kSteps / 2) + i;
+            const int rl = step * kRowsStep + lane / kRowLanes;
+            const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            float top = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[j] << 16)),
+                                     fabsf(__uint_as_float(v[j] & 0xffff0000u))));
+#pragma unroll
+            for (int d = kRowLanes / 2; d > 0; d /= 2)
+              top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+            float up, down;
+            row_power(top, up, down);
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              h[j] = pack_f16(__uint_as_float(v[j] << 16) * up,
+                              __uint_as_float(v[j] & 0xffff0000u) * up);
+            sts128(sm_rows + swizzled((warp & 3) * 32 + rl, lane % kRowLanes, kHalf), h[0], h[1],
+                   h[2], h[3]);
+            // lane rl keeps row rl's
+            const float mine = __shfl_sync(~0u, down, (lane % kRowsStep) * kRowLanes);
+            if (lane / kRowsStep == step) gain = mine * a.scale_log2;
+          }
         }
         ptx::fence_proxy_async();
         __syncwarp();
@@ -474,17 +541,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint4 bad = lds128(bad_at);
         const bool whole = tok0 >= all_first && tok0 + kKeys - 1 <= all_last &&
                            (bad.x | bad.y | bad.z | bad.w) == 0;
-        uint32_t v[2][32];
-        tmem_ld32(ts, v[0]);
 #pragma unroll 1
-        for (int c2 = 0; c2 < kKeys / 64; ++c2) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int c = 2 * c2 + e;
-            uint32_t(&s)[32] = v[e];
+        for (int c = 0; c < kKeys / 32; ++c) {
+            uint32_t s[32];
+            tmem_ld32(ts + 32 * c, s);
             tmem_landed(s);
-            // the next columns come while these are worked on
-            if (e == 0 || c2 + 1 < kKeys / 64) tmem_ld32(ts + 32 * (c + 1), v[e ^ 1]);
             if (!whole) {
               const uint32_t bits = lds32(bad_at + 4 * c);
 #pragma unroll
@@ -493,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (key < first || key > last || ((bits >> i) & 1u)) s[i] = 0xff800000u;
               }
             }
-            uint32_t pk[16], top = 0;
+            uint32_t pk[16], tops[4] = {0, 0, 0, 0};
             uint64_t add[2] = {0, 0};
             auto expo = [&] {
               const uint64_t off2 = pair_f32(-mbase, -mbase);
@@ -505,13 +566,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float p0 = ex2(x0), p1 = ex2(x1);
                 add[i & 1] = add_f32x2(add[i & 1], pair_f32(p0, p1));
                 pk[i] = pack_f16(p0, p1);
-                top = max_f16x2(top, pk[i]);
+                tops[i & 3] = max_f16x2(tops[i & 3], pk[i]);
               }
             };
             expo();
-            const float2 t2 = unpack_f16(top);
+            const float2 t2 = unpack_f16(
+                max_f16x2(max_f16x2(tops[0], tops[1]), max_f16x2(tops[2], tops[3])));
             if (__any_sync(~0u, fmaxf(t2.x, t2.y) > kMostP || m == -INFINITY)) {
-              if (e == 0 || c2 + 1 < kKeys / 64) tmem_landed(v[e ^ 1]);
               float mx = __uint_as_float(s[0]);
 #pragma unroll
               for (int i = 1; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(s[i]));
@@ -559,7 +620,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             l2[0] = add_f32x2(l2[0], add[0]);
             l2[1] = add_f32x2(l2[1], add[1]);
             tmem_st16(ts + 16 * c, pk);
-          }
         }
         tmem_wait_st();
         ptx::tc_fence_before();
@@ -582,8 +642,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t v[32];
           tmem_ld32(to + 32 * c, v);
           tmem_landed(v);
-          if (live) store_row<32>(dst + 32 * c, reinterpret_cast<const float*>(v), f);
+          stage_columns(sm_rows, row_l, c, reinterpret_cast<const float*>(v), f);
         }
+        store_rows();
         if (live && a.lse) a.lse[at_row] = log_sum(mbase, l);
         ptx::tc_fence_before();
         continue;
@@ -631,6 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = t.cta0; k <= t.cta1; ++k)
         top = fmaxf(top, __ldcg(&stats[slot_of(k) * kHalf + row_l]).x);
       auto weight = [&](float b2) { return b2 == -INFINITY ? 0.0f : ex2(b2 - top); };
+#pragma unroll 4
       for (int k = t.cta0; k <= t.cta1; ++k) {
         const float2 st = __ldcg(&stats[slot_of(k) * kHalf + row_l]);
         den += weight(st.x) * st.y;
@@ -640,35 +702,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < D / 32; ++c) {
         float sum[32] = {};
 #pragma unroll 1
-        for (int k = t.cta0; k <= t.cta1; ++k) {
-          const long slot = slot_of(k);
-          const float w = weight(__ldcg(&stats[slot * kHalf + row_l]).x);
+        for (int k = t.cta0; k <= t.cta1; k += 2) {  // two pieces' loads at a time
+          float4 v[2][8];
+          float w[2];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 v = __ldcg(&partial[(slot * (D / 4) + 8 * c + i) * kHalf + row_l]);
-            sum[4 * i] += w * v.x, sum[4 * i + 1] += w * v.y;
-            sum[4 * i + 2] += w * v.z, sum[4 * i + 3] += w * v.w;
+          for (int e = 0; e < 2; ++e) {
+            const long slot = slot_of(min(k + e, t.cta1));
+            w[e] = __ldcg(&stats[slot * kHalf + row_l]).x;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              v[e][i] = __ldcg(&partial[(slot * (D / 4) + 8 * c + i) * kHalf + row_l]);
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float g2 = k + e <= t.cta1 ? weight(w[e]) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              sum[4 * i] += g2 * v[e][i].x, sum[4 * i + 1] += g2 * v[e][i].y;
+              sum[4 * i + 2] += g2 * v[e][i].z, sum[4 * i + 3] += g2 * v[e][i].w;
+            }
           }
         }
-        if (live) store_row<32>(dst + 32 * c, sum, f);
+        stage_columns(sm_rows, row_l, c, sum, f);
       }
+      store_rows();
       if (live && a.lse) a.lse[at_row] = log_sum(top, den);
     }
   } else if (warp < kMmaWarp) {
     // ------------------------------------------------- codes to f16 operands
+    // A warp converts slices of its own, so that the codes it has under way in
+    // shared memory concern nobody else. The loops stay rolled: the three
+    // roles' code has to fit the instruction cache together (fully unrolled, the
+    // kernel spent most of its time fetching instructions).
     const int ft = threadIdx.x - kSoftWarps * 32, fw = warp - kSoftWarps;
-    // keys: a row, or a half of its 256 channels
-    constexpr int kParts = 128 / kKeys, kChans = D / kParts;
+    // keys: lane's row kr, all of its channels or half of 256
+    constexpr int kChans = H::kChans;
     const int kr = ft % kKeys, kpart = ft / kKeys;
-    // values: eight tokens from vt, 16 channels from 16 * vg. Eight neighbouring
-    // lanes have different tokens and the same channels: their 16-byte stores
-    // fall on the eight chunks of one 128-byte row.
-    constexpr int kGroups = kKeys / 8;
-    const int vt = (kGroups == 16 ? (lane & 7) + 8 * (fw & 1) : lane & 7) * 8;
-    const int vg = kGroups == 16 ? (lane >> 3) + 4 * (fw >> 1) : ft >> 3;
-    const bool has_v = vg < D / kKvGroup;
+    // values: 64 tokens from v0, 64 channels from 64 * vq; lane's eight tokens
+    // begin at vt, its 16 channels at 16 * vg. Eight neighbouring lanes have
+    // different tokens and the same channels: their 16-byte stores fall on the
+    // eight chunks of one 128-byte row.
+    const int v0 = kKeys == 128 ? 64 * (fw & 1) : 0, vq = kKeys == 128 ? fw >> 1 : fw;
+    const int vt = v0 + (lane & 7) * 8, vg = 4 * vq + (lane >> 3);
+    const bool has_v = vq < D / 64;
     const KvBlock blk = kv_block(a.page_size, D);
     const int page_mask = a.page_size - 1, page_shift = 31 - __clz(a.page_size);
+    const uint32_t raw = sm_v + 2 * H::kK + fw * H::kRaw;
     uint32_t kc = 0;
     begin();
     while (next()) {
@@ -681,45 +760,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = id >= 0 && id < a.num_pages;
         return a.cache + (static_cast<long>(ok ? id : 0) * a.kv_heads + t.kvh) * blk.bytes;
       };
-      // Codes and scales of the next tile and page ids of the one after it are
-      // on the way while a tile is converted.
-      Words<kChans / 8> kraw;
-      uint32_t ks[kChans / 64], vs[2] = {0, 0};
-      uint2 vraw[8];
-      bool k_ok = true;
+      // While a tile's keys or values are converted, its values or the next
+      // tile's keys are copied; page ids are read one tile ahead of that.
+      bool k_ok = true, v_ok = true;
       int kid = page_of(t.first * kKeys + kr, 0), vid = page_of(t.first * kKeys + vt, 7);
-      auto fetch_k = [&](int j) {
-        if (j >= t.tiles) return;
-        const int key = (t.first + j) * kKeys + kr;
-        const uint8_t* p = block_of(kid, k_ok);
-        const int row = key & page_mask;
-        kraw = load_words<kChans / 8>(p + row * (D / 2) + kpart * (kChans / 2));
-#pragma unroll
-        for (int i = 0; i < kChans / 64; ++i)
-          ks[i] = *reinterpret_cast<const uint32_t*>(p + blk.k_scale + row * (D / 16) +
-                                                     kpart * (kChans / 16) + 4 * i);
-        if (j + 1 < t.tiles) kid = page_of(key + kKeys, 0);
-      };
-      auto fetch_v = [&](int j) {
-        if (j >= t.tiles || !has_v) return;
-        const int key0 = (t.first + j) * kKeys + vt;
-        bool ok;
-        const uint8_t* p = block_of(vid, ok);
-        const int row = key0 & page_mask;
-        vs[0] = vs[1] = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          vraw[i] = *reinterpret_cast<const uint2*>(p + blk.v_code + (row + i) * (D / 2) + vg * 8);
-          // a key that no row sees may be uninitialised memory: a zero scale
-          // keeps 0 * NaN out of the sum
-          const uint32_t s = p[blk.v_scale + (row + i) * (D / 16) + vg];
-          vs[i >> 2] |= (ok && key0 + i >= t.lo && key0 + i < t.hi ? s : 0u) << (8 * (i & 3));
+      auto copy_k = [&](int j) {
+        if (j < t.tiles) {
+          const int key = (t.first + j) * kKeys + kr, row = key & page_mask;
+          const uint8_t* p = block_of(kid, k_ok);
+          const long codes = reinterpret_cast<long>(p + row * (D / 2) + kpart * (kChans / 2));
+          constexpr int kChunks = kChans / 32;  // 16-byte chunks of a row
+#pragma unroll 1
+          for (int i = 0; i < kChunks; ++i) {
+            const int n = 32 * i + lane, r = n / kChunks, c = n % kChunks;
+            const long src = __shfl_sync(~0u, codes, r);
+            // chunks of a row are swizzled by the row: lanes read one chunk of
+            // 32 rows at a time
+            const int place = kChunks == 4 ? c ^ ((r >> 1) & 3) : c ^ ((r >> 2) & 1);
+            ptx::cp_async16(raw + (r * kChunks + place) * 16,
+                            reinterpret_cast<const void*>(src + 16 * c));
+          }
+          cp_async_small<kChans / 16>(raw + H::kRawKs + lane * (kChans / 16),
+                                      p + blk.k_scale + row * (D / 16) + kpart * (kChans / 16));
+          if (j + 1 < t.tiles) kid = page_of(key + kKeys, 0);
         }
-        if (j + 1 < t.tiles) vid = page_of(key0 + kKeys, 7);
+        asm volatile("cp.async.commit_group;" ::: "memory");
       };
-      fetch_k(0);
-      fetch_v(0);
+      auto copy_v = [&](int j) {
+        if (j < t.tiles && has_v) {
+          const int key = (t.first + j) * kKeys + vt;
+          const uint8_t* p = block_of(vid, v_ok);
+          const long block = reinterpret_cast<long>(p);
+          const int row0 = key & page_mask;  // of the lane's eight tokens
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            // token 8 * g + e of the slice goes to row 8 * e + g: the lanes'
+            // g-th groups lie side by side
+            const int n = 32 * i + lane, tok = n >> 1, g = tok >> 3, e = tok & 7;
+            const long src = __shfl_sync(~0u, block, g);
+            const int row = __shfl_sync(~0u, row0, g) + e;
+            ptx::cp_async16(raw + H::kRawV + (8 * e + g) * 32 + (n & 1) * 16,
+                            reinterpret_cast<const void*>(src + blk.v_code + row * (D / 2) +
+                                                          vq * 32 + (n & 1) * 16));
+          }
+#pragma unroll 1
+          for (int i = 0; i < 2; ++i) {
+            const int tok = 32 * i + lane, g = tok >> 3, e = tok & 7;
+            const long src = __shfl_sync(~0u, block, g);
+            const int row = __shfl_sync(~0u, row0, g) + e;
+            cp_async_small<4>(raw + H::kRawVs + (8 * e + g) * 4,
+                              reinterpret_cast<const uint8_t*>(src + blk.v_scale + row * (D / 16) +
+                                                               vq * 4));
+          }
+          if (j + 1 < t.tiles) vid = page_of(key + kKeys, 7);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      copy_k(0);
+      copy_v(0);
       bool ok = true;
+#pragma unroll 1
       for (int j = 0; j < t.tiles; ++j, ++kc) {
         const uint32_t st = kc & 1, parity = ((kc >> 1) & 1) ^ 1;
         if (!(ok = wait_warp(bars.k_empty[st], parity))) break;
@@ -729,29 +829,57 @@ __global__ void __launch_bounds__(kThreads, 1)
           // (with 64 keys, warps 2 and 3 see the same rows again)
           *reinterpret_cast<volatile uint32_t*>(&s_bad[kc % kBadRing][fw]) = bad;
         }
+        asm volatile("cp.async.wait_group 1;" ::: "memory");  // the keys, not the values
+        __syncwarp();
+#pragma unroll 1
+        for (int i = 0; i < kChans / 32; ++i) {
+          constexpr int kChunks = kChans / 32;
+          const int place = kChunks == 4 ? i ^ ((lane >> 1) & 3) : i ^ ((lane >> 2) & 1);
+          const uint4 w = lds128(raw + (lane * kChunks + place) * 16);
+          const uint32_t two =
+              e4m3x2_to_f16(lds16(raw + H::kRawKs + lane * (kChans / 16) + 2 * i));
+          const uint32_t s2[2] = {f16_low_twice(two), f16_high_twice(two)};
+          const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int c = 0; c < kChans / 8; ++c) {
-          uint32_t h[4];
-          e2m1_to_f16(kraw.w[c], h);
-          const uint32_t two = e4m3x2_to_f16(ks[c / 8] >> (16 * ((c / 4) & 1)));
-          const uint32_t s = (c / 2) & 1 ? f16_high_twice(two) : f16_low_twice(two);
-          sts128(sm_k + st * H::kK + swizzled(kr, kpart * (kChans / 8) + c, kKeys), hmul2(h[0], s),
-                 hmul2(h[1], s), hmul2(h[2], s), hmul2(h[3], s));
+          for (int c = 0; c < 4; ++c) {
+            uint32_t h[4];
+            e2m1_to_f16(words[c], h);
+            const uint32_t s = s2[c / 2];
+            sts128(sm_k + st * H::kK + swizzled(kr, kpart * (kChans / 8) + 4 * i + c, kKeys),
+                   hmul2(h[0], s), hmul2(h[1], s), hmul2(h[2], s), hmul2(h[3], s));
+          }
         }
         ptx::fence_proxy_async();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(bars.k_full[st]));
-        fetch_k(j + 1);
+        copy_k(j + 1);
         if (!(ok = wait_warp(bars.v_empty[st], parity))) break;
+        asm volatile("cp.async.wait_group 1;" ::: "memory");  // the values, not the next keys
+        __syncwarp();
         if (has_v) {
+          const int key = (t.first + j) * kKeys + vt;
           uint32_t s[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[i] = e4m3x2_to_f16(vs[i >> 1] >> (16 * (i & 1)));
+          for (int i = 0; i < 4; ++i) {
+            uint32_t two = 0;
 #pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              // a key that no row sees may be uninitialised memory: a zero scale
+              // keeps 0 * NaN out of the sum
+              const int n = 2 * i + e;
+              const uint32_t b =
+                  lds8(raw + H::kRawVs + (8 * n + (lane & 7)) * 4 + (lane >> 3));
+              two |= (v_ok && key + n >= t.lo && key + n < t.hi ? b : 0u) << (8 * e);
+            }
+            s[i] = e4m3x2_to_f16(two);
+          }
+#pragma unroll 1
           for (int w = 0; w < 2; ++w) {  // eight channels
             uint32_t h[8][4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) e2m1_to_f16(w ? vraw[i].y : vraw[i].x, h[i]);
+            for (int i = 0; i < 8; ++i)
+              e2m1_to_f16(lds32(raw + H::kRawV + (8 * i + (lane & 7)) * 32 + (lane >> 3) * 8 + 4 * w),
+                          h[i]);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const int ch = vg * 16 + w * 8 + 2 * q;
@@ -769,10 +897,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::fence_proxy_async();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(bars.v_full[st]));
-        fetch_v(j + 1);
+        copy_v(j + 1);
       }
       if (!ok) break;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
   }

@@ -96,6 +96,39 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
   }
 }
 
+// The same try, which may suspend the thread for up to `hint` ns.
+__device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t hint) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(hint)
+      : "memory");
+  return ok != 0;
+}
+
+// mbar_wait whose first try sleeps for up to 20 us: a warp that waits for
+// another role of its CTA then spends no issue slots and no instruction fetches
+// on polling, which matters where the CTA's other warps need both.
+__device__ __forceinline__ bool mbar_wait_asleep(uint32_t bar, uint32_t parity,
+                                                 volatile int* abort, unsigned* status) {
+  constexpr uint32_t kSleepNs = 20000;
+  if (mbar_try_wait_for(bar, parity, kSleepNs)) return true;
+  const uint64_t t0 = globaltimer();
+  const uint64_t limit = g_wait_limit_ns;
+  for (;;) {
+    if (mbar_try_wait_for(bar, parity, kSleepNs)) return true;
+    if (*abort) return false;
+    if (globaltimer() - t0 > limit) {
+      *abort = 1;
+      if (status) atomicOr(status, MOE_DEV_TIMEOUT);
+      return false;
+    }
+  }
+}
+
 // Time-bounded wait that ignores the abort flag (used while unwinding).
 __device__ __forceinline__ bool mbar_wait_drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer();
