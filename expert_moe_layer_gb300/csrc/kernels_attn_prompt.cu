@@ -42,12 +42,12 @@ namespace {
 
 constexpr int kHalf = 128;  // rows of a half, lanes of tensor memory
 constexpr int kSoftWarps = 8, kFillWarps = 4;
+constexpr int kStageBytes = 32 * 32;  // a softmax warp's staging rows on the way out
 constexpr int kMmaWarp = kSoftWarps + kFillWarps;
 constexpr int kThreads = 512;  // whole groups of four warps (three idle ones)
-// Registers per thread: launched with 128 each (65,536 in all); the matrix
-// warp's group gives some of its share to the two softmax groups:
-// 128 * (2 * 152 + 128 + 80) = 65,536.
-constexpr int kSoftRegs = 152, kMmaRegs = 80;
+// Registers per thread: launched with 128 each (65,536 in all), shared out anew
+// by the groups of four warps: 128 * (2 * 184 + 80 + 64) = 65,536.
+constexpr int kSoftRegs = 184, kFillRegs = 80, kMmaRegs = 64;
 constexpr int kBadRing = 4;  // tiles whose bad-page bits are kept: a fill warp is at most
                              // two tiles ahead of the slower half
 constexpr int kSetup = 4;    // list entries of a segment beside its tiles: its set-up and store
@@ -71,7 +71,7 @@ struct Shape {
   static constexpr int kChans = D < 128 ? D : 128;
   static constexpr int kRawKs = 32 * kChans / 2, kRawV = kRawKs + 32 * kChans / 16;
   static constexpr int kRawVs = kRawV + 64 * 32, kRaw = kRawVs + 64 * 4;
-  static constexpr int kBytes = kHalves * kQ + 4 * kK + kFillWarps * kRaw + 1024;
+  static constexpr int kBytes = kHalves * kQ + 4 * kK + kFillWarps * kRaw + kSoftWarps * kStageBytes + 1024;
 };
 
 struct Bars {
@@ -113,14 +113,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
         "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
         "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15]), "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
@@ -187,6 +179,11 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint32_t lds16(uint32_t addr) {
   uint16_t v;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
@@ -354,23 +351,6 @@ struct Cursor {
   }
 };
 
-// 32 columns of a row, as bf16, to its place in a half's staging rows (laid out
-// like the half's queries, which no matrix instruction reads any more).
-__device__ __forceinline__ void stage_columns(uint32_t rows, int row, int c, const float* v,
-                                              float f) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t h[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const __nv_bfloat162 b2 =
-          __floats2bfloat162_rn(v[8 * i + 2 * q] * f, v[8 * i + 2 * q + 1] * f);
-      h[q] = *reinterpret_cast<const uint32_t*>(&b2);
-    }
-    sts128(rows + swizzled(row, 4 * c + i, kHalf), h[0], h[1], h[2], h[3]);
-  }
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_prompt_kernel(AttnArgs a, unsigned* status, int* counters, const SeqInfo* info,
@@ -385,7 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int s_last[2];
   __shared__ volatile int s_abort;
   const uint32_t base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sm_q = base, sm_k = base + H::kHalves * H::kQ, sm_v = sm_k + 2 * H::kK;
+  const uint32_t sm_q = base, sm_k = base + H::kHalves * H::kQ, sm_v = sm_k + 2 * H::kK,
+                 sm_raw = sm_v + 2 * H::kK, sm_stage = sm_raw + kFillWarps * H::kRaw;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto bar = [&](const uint64_t& b) { return ptx::smem_u32(&b); };
 
@@ -432,95 +413,120 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ---------------------------------------------------------------- softmax
-    const int x = warp >> 2;
-    const int row_l = (warp & 3) * 32 + lane;  // row of the half, lane of tensor memory
-    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
-    const uint32_t ts = tmem + lanes + kColsS + x * kKeys, to = tmem + lanes + kColsO + x * D;
+    const int x = warp >> 2, wl = warp & 3;
+    const int row_l = wl * 32 + lane;  // row of the half, lane of tensor memory
+    const uint32_t ts = tmem + (wl << 21) + kColsS + x * kKeys;
+    const uint32_t to = tmem + (wl << 21) + kColsO + x * D;
     const uint32_t sm_rows = sm_q + x * H::kQ;
-    // rows are read and written by kRowLanes lanes of 16 bytes, several at once
-    constexpr int kRowLanes = D / 8, kRowsStep = 32 / kRowLanes, kSteps = kRowLanes;
+    const uint32_t stage = sm_stage + warp * kStageBytes;
     uint32_t s_phase = 0, o_phase = 0, join_phase = 0, tile_no = 0;
-    begin();
-    while (x < H::kHalves && next()) {
-      if (x >= t.halves) {
-        tile_no += t.tiles;
-        continue;
-      }
-      const int r = t.row0 + x * kHalf + row_l;
-      const bool live = r < t.rows;
-      const int tok = r / group, head = t.kvh * group + (r - tok * group);
-      const long at_row = static_cast<long>(t.sq.q0 + tok) * a.heads + head;
-      // the warp's staged rows to the output
-      auto store_rows = [&] {
-        __syncwarp();
-#pragma unroll 4
-        for (int i = 0; i < kSteps; ++i) {
-          const int rl = i * kRowsStep + lane / kRowLanes;
-          const long row = __shfl_sync(~0u, at_row, rl);
-          const bool there = __shfl_sync(~0u, static_cast<int>(live), rl);
-          const uint4 v =
-              lds128(sm_rows + swizzled((warp & 3) * 32 + rl, lane % kRowLanes, kHalf));
-          if (there)
-            reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D)[lane % kRowLanes] = v;
+    // This thread's row of the current piece.
+    int r, tok, head;
+    bool live;
+    float gain = 0.0f;
+    auto place = [&] {
+      r = t.row0 + x * kHalf + row_l;
+      live = r < t.rows;
+      tok = r / group;
+      head = t.kvh * group + (r - tok * group);
+    };
+    // The next piece with keys for this half; what has none is zeroed.
+    auto advance = [&] {
+      while (next()) {
+        if (x >= t.halves) {
+          tile_no += t.tiles;
+          continue;
         }
-        __syncwarp();
-      };
-      if (t.tiles == 0) {  // no row of the segment sees a key
+        place();
+        if (t.tiles > 0) return true;
         if (live) {
+          const long at_row = static_cast<long>(t.sq.q0 + tok) * a.heads + head;
           uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at_row * D);
           for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0, 0, 0, 0);
           if (a.lse) a.lse[at_row] = -INFINITY;
         }
-        continue;
       }
-      // The warp's rows of queries, whole rows by neighbouring lanes, scaled to
-      // f16; each lane keeps its own row's gain.
-      float gain = 0.0f;
-      {
-        const long src = (t.sq.q0 + (live ? tok : 0)) * a.q.token + (live ? head : 0) * a.q.head;
+      return false;
+    };
+    // The warp's rows of queries, whole rows by neighbouring lanes, scaled to
+    // f16; each lane keeps its own row's gain.
+    auto load_queries = [&] {
+      constexpr int kRowLanes = D / 8, kRowsStep = 32 / kRowLanes, kBatch = 8;
+      const long src = (t.sq.q0 + (live ? tok : 0)) * a.q.token + (live ? head : 0) * a.q.head;
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          uint4 w[kSteps / 2];
+      for (int first = 0; first < kRowLanes; first += kBatch) {
+        uint4 w[kBatch];
 #pragma unroll
-          for (int i = 0; i < kSteps / 2; ++i) {
-            const int rl = (half * (kSteps / 2) + i) * kRowsStep + lane / kRowLanes;
-            const long at = __shfl_sync(~0u, src, rl);
-            const bool there = __shfl_sync(~0u, static_cast<int>(live), rl);
-            w[i] = there ? *reinterpret_cast<const uint4*>(
-                               static_cast<const __nv_bfloat16*>(a.q.p) + at + lane % kRowLanes * 8)
-                         : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int i = 0; i < kSteps / 2; ++i) {
-            const int step = half * (kSteps / 2) + i;
-            const int rl = step * kRowsStep + lane / kRowLanes;
-            const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-            float top = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[j] << 16)),
-                                     fabsf(__uint_as_float(v[j] & 0xffff0000u))));
-#pragma unroll
-            for (int d = kRowLanes / 2; d > 0; d /= 2)
-              top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-            float up, down;
-            row_power(top, up, down);
-            uint32_t h[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              h[j] = pack_f16(__uint_as_float(v[j] << 16) * up,
-                              __uint_as_float(v[j] & 0xffff0000u) * up);
-            sts128(sm_rows + swizzled((warp & 3) * 32 + rl, lane % kRowLanes, kHalf), h[0], h[1],
-                   h[2], h[3]);
-            // lane rl keeps row rl's
-            const float mine = __shfl_sync(~0u, down, (lane % kRowsStep) * kRowLanes);
-            if (lane / kRowsStep == step) gain = mine * a.scale_log2;
-          }
+        for (int i = 0; i < kBatch; ++i) {
+          const int rl = (first + i) * kRowsStep + lane / kRowLanes;
+          const long at = __shfl_sync(~0u, src, rl);
+          const bool there = __shfl_sync(~0u, static_cast<int>(live), rl);
+          w[i] = there ? *reinterpret_cast<const uint4*>(
+                             static_cast<const __nv_bfloat16*>(a.q.p) + at + lane % kRowLanes * 8)
+                       : make_uint4(0, 0, 0, 0);
         }
-        ptx::fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(bars.q_ready[x]));
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int rl = (first + i) * kRowsStep + lane / kRowLanes;
+          const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          float top = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[j] << 16)),
+                                   fabsf(__uint_as_float(v[j] & 0xffff0000u))));
+#pragma unroll
+          for (int d = kRowLanes / 2; d > 0; d /= 2)
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+          float up, down;
+          row_power(top, up, down);
+          uint32_t h[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            h[j] = pack_f16(__uint_as_float(v[j] << 16) * up,
+                            __uint_as_float(v[j] & 0xffff0000u) * up);
+          sts128(sm_rows + swizzled(wl * 32 + rl, lane % kRowLanes, kHalf), h[0], h[1], h[2], h[3]);
+          const float mine = __shfl_sync(~0u, down, (lane % kRowsStep) * kRowLanes);
+          if (lane / kRowsStep == first + i) gain = mine * a.scale_log2;
+        }
       }
+      ptx::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(bars.q_ready[x]));
+    };
+    // 32 columns of the warp's rows as bf16 to their places in `out`, through
+    // the warp's staging rows of 32 bytes: whole sectors by lane pairs.
+    auto store_columns = [&](int c, const float* v, float f, long at_row, bool there) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const __nv_bfloat162 b2 =
+              __floats2bfloat162_rn(v[16 * q + 2 * i] * f, v[16 * q + 2 * i + 1] * f);
+          h[i] = *reinterpret_cast<const uint32_t*>(&b2);
+        }
+        const int flip = (lane >> 2) & 1;  // spreads eight rows over the banks
+        __syncwarp();
+        sts128(stage + lane * 32 + 16 * flip, h[0], h[1], h[2], h[3]);
+        sts128(stage + lane * 32 + 16 * (flip ^ 1), h[4], h[5], h[6], h[7]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int rl = 16 * i + (lane >> 1);
+          const long row = __shfl_sync(~0u, at_row, rl);
+          const bool store = __shfl_sync(~0u, static_cast<int>(there), rl);
+          const uint4 w = lds128(stage + rl * 32 + 16 * ((lane & 1) ^ ((rl >> 2) & 1)));
+          if (store)
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D + 32 * c +
+                                      16 * q + 8 * (lane & 1)) = w;
+        }
+      }
+    };
+
+    begin();
+    bool more = x < H::kHalves && advance();
+    if (more) load_queries();
+    while (more) {
       const int p = t.sq.len - t.sq.q_len + tok;
       const int last = live ? p : 0x7fffffff;
       const int first = live && a.window > 0 ? p - a.window + 1 : 0;
@@ -528,106 +534,118 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r_lo = t.row0 + x * kHalf, r_hi = min(t.rows, r_lo + kHalf) - 1;
       const int all_last = t.sq.len - t.sq.q_len + r_lo / group;
       const int all_first = a.window > 0 ? t.sq.len - t.sq.q_len + r_hi / group - a.window + 1 : 0;
+      const bool frees = x == t.halves - 1 && threadIdx.x % 128 == 0;
       float m = -INFINITY, mbase = -kLift;  // m: a whole number
       uint64_t l2[2] = {0, 0};              // partial sums of P
       const uint64_t gain2 = pair_f32(gain, gain);
       bool ok = true;
+#pragma unroll 1
       for (int j = 0; j < t.tiles; ++j, ++tile_no) {
         if (!(ok = wait_warp(bars.s_full[x], s_phase))) break;
         s_phase ^= 1;
         ptx::tc_fence_after();
+        // This half's scores are the tile's last ones: the keys are free, and the
+        // values of the tile before, whose products were issued earlier. (A
+        // commit for each would hold up the matrix thread.)
+        if (frees) {
+          ptx::mbar_arrive(bar(bars.k_empty[tile_no & 1]));
+          if (j > 0) ptx::mbar_arrive(bar(bars.v_empty[(tile_no - 1) & 1]));
+        }
         const int tok0 = (t.first + j) * kKeys;
         const uint32_t bad_at = ptx::smem_u32(s_bad[tile_no % kBadRing]);
-        const uint4 bad = lds128(bad_at);
-        const bool whole = tok0 >= all_first && tok0 + kKeys - 1 <= all_last &&
-                           (bad.x | bad.y | bad.z | bad.w) == 0;
+        const bool inside = tok0 >= all_first && tok0 + kKeys - 1 <= all_last;
 #pragma unroll 1
-        for (int c = 0; c < kKeys / 32; ++c) {
-            uint32_t s[32];
-            tmem_ld32(ts + 32 * c, s);
-            tmem_landed(s);
-            if (!whole) {
-              const uint32_t bits = lds32(bad_at + 4 * c);
+        for (int c = 0; c < kKeys / 64; ++c) {
+          uint32_t s[64];
+          tmem_ld32(ts + 64 * c, *reinterpret_cast<uint32_t(*)[32]>(s));
+          tmem_ld32(ts + 64 * c + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+          const uint2 bad = lds64(bad_at + 8 * c);
+          tmem_landed(*reinterpret_cast<uint32_t(*)[32]>(s));
+          tmem_landed(*reinterpret_cast<uint32_t(*)[32]>(s + 32));
+          if (!inside || (bad.x | bad.y) != 0) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) {
+              const int key = tok0 + 64 * c + i;
+              if (key < first || key > last || (((i < 32 ? bad.x : bad.y) >> (i & 31)) & 1u))
+                s[i] = 0xff800000u;
+            }
+          }
+          uint32_t pk[32];
+          uint64_t add[2];
+#pragma unroll 1
+          for (bool again = false;; again = true) {
+            const uint64_t off2 = pair_f32(-mbase, -mbase);
+            uint32_t tops[4] = {0, 0, 0, 0};
+            add[0] = add[1] = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float x0, x1;
+              unpair_f32(fma_f32x2(pair_b32(s[2 * i], s[2 * i + 1]), gain2, off2), x0, x1);
+              const float p0 = ex2(x0), p1 = ex2(x1);
+              add[i & 1] = add_f32x2(add[i & 1], pair_f32(p0, p1));
+              pk[i] = pack_f16(p0, p1);
+              tops[i & 3] = max_f16x2(tops[i & 3], pk[i]);
+            }
+            const float2 top = unpack_f16(
+                max_f16x2(max_f16x2(tops[0], tops[1]), max_f16x2(tops[2], tops[3])));
+            if (again || !__any_sync(~0u, fmaxf(top.x, top.y) > kMostP || m == -INFINITY)) break;
+            // A row has outgrown its maximum (or has none yet): move it up by
+            // whole powers of two and scale down what has been summed.
+            float mx = __uint_as_float(s[0]);
+#pragma unroll
+            for (int i = 1; i < 64; ++i) mx = fmaxf(mx, __uint_as_float(s[i]));
+            const float nm = fmaxf(m, ceilf(mx * gain));
+            const float nb = nm == -INFINITY ? -kLift : nm - kLift;
+            const float f = m == -INFINITY ? 0.0f : ex2(mbase - nb);
+            m = nm;
+            mbase = nb;
+            l2[0] = fma_f32x2(l2[0], pair_f32(f, f), 0);
+            l2[1] = fma_f32x2(l2[1], pair_f32(f, f), 0);
+            if (c > 0) {  // P of this tile's first columns
+              uint32_t w[32];
+              tmem_wait_st();
+              tmem_ld32(ts, w);
+              tmem_landed(w);
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
-                const int key = tok0 + 32 * c + i;
-                if (key < first || key > last || ((bits >> i) & 1u)) s[i] = 0xff800000u;
+                const float2 g2 = unpack_f16(w[i]);
+                w[i] = pack_f16(g2.x * f, g2.y * f);
               }
+              tmem_st32(ts, w);
             }
-            uint32_t pk[16], tops[4] = {0, 0, 0, 0};
-            uint64_t add[2] = {0, 0};
-            auto expo = [&] {
-              const uint64_t off2 = pair_f32(-mbase, -mbase);
-              add[0] = add[1] = 0;
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float x0, x1;
-                unpair_f32(fma_f32x2(pair_b32(s[2 * i], s[2 * i + 1]), gain2, off2), x0, x1);
-                const float p0 = ex2(x0), p1 = ex2(x1);
-                add[i & 1] = add_f32x2(add[i & 1], pair_f32(p0, p1));
-                pk[i] = pack_f16(p0, p1);
-                tops[i & 3] = max_f16x2(tops[i & 3], pk[i]);
-              }
-            };
-            expo();
-            const float2 t2 = unpack_f16(
-                max_f16x2(max_f16x2(tops[0], tops[1]), max_f16x2(tops[2], tops[3])));
-            if (__any_sync(~0u, fmaxf(t2.x, t2.y) > kMostP || m == -INFINITY)) {
-              float mx = __uint_as_float(s[0]);
-#pragma unroll
-              for (int i = 1; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(s[i]));
-              const float nm = fmaxf(m, ceilf(mx * gain));
-              const float nb = nm == -INFINITY ? -kLift : nm - kLift;
-              const float f = m == -INFINITY ? 0.0f : ex2(mbase - nb);
-              m = nm;
-              mbase = nb;
-              l2[0] = fma_f32x2(l2[0], pair_f32(f, f), 0);
-              l2[1] = fma_f32x2(l2[1], pair_f32(f, f), 0);
-              tmem_wait_st();
+            if (j > 0) {  // the products of the tiles before have landed (s_full)
 #pragma unroll 1
-              for (int q = 0; q < c; q += 2) {  // P of this tile's earlier columns
+              for (int q = 0; q < D / 32; ++q) {
                 uint32_t w[32];
-                tmem_ld32(ts + 16 * q, w);
+                tmem_ld32(to + 32 * q, w);
                 tmem_landed(w);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  if (q + 1 == c && i >= 16) break;
-                  const float2 g2 = unpack_f16(w[i]);
-                  w[i] = pack_f16(g2.x * f, g2.y * f);
-                }
-                if (q + 1 < c) {
-                  tmem_st32(ts + 16 * q, w);
-                } else {
-                  uint32_t w16[16];
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) w16[i] = w[i];
-                  tmem_st16(ts + 16 * q, w16);
-                }
+                for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
+                tmem_st32(to + 32 * q, w);
               }
-              if (j > 0) {  // the products of the tiles before have all landed (s_full)
-#pragma unroll 1
-                for (int q = 0; q < D / 32; ++q) {
-                  uint32_t w[32];
-                  tmem_ld32(to + 32 * q, w);
-                  tmem_landed(w);
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
-                  tmem_st32(to + 32 * q, w);
-                }
-              }
-              expo();
             }
-            l2[0] = add_f32x2(l2[0], add[0]);
-            l2[1] = add_f32x2(l2[1], add[1]);
-            tmem_st16(ts + 16 * c, pk);
+          }
+          l2[0] = add_f32x2(l2[0], add[0]);
+          l2[1] = add_f32x2(l2[1], add[1]);
+          tmem_st32(ts + 32 * c, pk);
         }
         tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(bars.p_ready[x]));
       }
-      if (!ok || !wait_warp(bars.o_done[x], o_phase)) break;
+      if (!ok) break;
+      // The next piece's queries go in first (every score of this one is done),
+      // so that its first product does not wait for this one's rows.
+      const long at_row = static_cast<long>(t.sq.q0 + tok) * a.heads + head;
+      const bool there = live, alone = t.alone;
+      const int cta0 = t.cta0, cta1 = t.cta1;
+      const uint32_t last_tile = tile_no - 1;
+      more = advance();
+      if (more) load_queries();
+      if (!wait_warp(bars.o_done[x], o_phase)) break;
       o_phase ^= 1;
+      if (frees) ptx::mbar_arrive(bar(bars.v_empty[last_tile & 1]));
       ptx::tc_fence_after();
       float l;
       {
@@ -635,26 +653,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         unpair_f32(add_f32x2(l2[0], l2[1]), l0, l1);
         l = l0 + l1;
       }
-      if (t.alone) {
+      if (alone) {
         const float f = out_factor(l, a.v_scale);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t v[32];
           tmem_ld32(to + 32 * c, v);
           tmem_landed(v);
-          stage_columns(sm_rows, row_l, c, reinterpret_cast<const float*>(v), f);
+          store_columns(c, reinterpret_cast<const float*>(v), f, at_row, there);
         }
-        store_rows();
-        if (live && a.lse) a.lse[at_row] = log_sum(mbase, l);
+        if (there && a.lse) a.lse[at_row] = log_sum(mbase, l);
         ptx::tc_fence_before();
         continue;
       }
       // A piece: sums [D / 4][row] and statistics [row] to the workspace, lanes
       // at neighbouring rows. The CTA a segment begins in keeps its piece in
       // slot 1, later ones in slot 0.
-      auto slot_of = [&](int cta) {
-        return (2l * cta + (cta == t.cta0)) * H::kHalves + x;
-      };
+      auto slot_of = [&](int cta) { return (2l * cta + (cta == cta0)) * H::kHalves + x; };
       {
         const long slot = slot_of(blockIdx.x);
 #pragma unroll 1
@@ -674,12 +689,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       __threadfence();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(bars.written[x]));
-      if ((warp & 3) == 0) {
+      if (wl == 0) {
         if (!wait_warp(bars.written[x], join_phase)) break;
         if (lane == 0) {
           __threadfence();
           *reinterpret_cast<volatile int*>(&s_last[x]) =
-              ptx::add_acq_rel(counters + 2 * t.cta0 + x, 1) == t.cta1 - t.cta0;
+              ptx::add_acq_rel(counters + 2 * cta0 + x, 1) == cta1 - cta0;
           ptx::mbar_arrive(bar(bars.joined[x]));
         }
       }
@@ -689,11 +704,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       __threadfence();
       float top = -INFINITY, den = 0.0f;
 #pragma unroll 4
-      for (int k = t.cta0; k <= t.cta1; ++k)
+      for (int k = cta0; k <= cta1; ++k)
         top = fmaxf(top, __ldcg(&stats[slot_of(k) * kHalf + row_l]).x);
       auto weight = [&](float b2) { return b2 == -INFINITY ? 0.0f : ex2(b2 - top); };
 #pragma unroll 4
-      for (int k = t.cta0; k <= t.cta1; ++k) {
+      for (int k = cta0; k <= cta1; ++k) {
         const float2 st = __ldcg(&stats[slot_of(k) * kHalf + row_l]);
         den += weight(st.x) * st.y;
       }
@@ -702,12 +717,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < D / 32; ++c) {
         float sum[32] = {};
 #pragma unroll 1
-        for (int k = t.cta0; k <= t.cta1; k += 2) {  // two pieces' loads at a time
+        for (int k = cta0; k <= cta1; k += 2) {  // two pieces' loads at a time
           float4 v[2][8];
           float w[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const long slot = slot_of(min(k + e, t.cta1));
+            const long slot = slot_of(min(k + e, cta1));
             w[e] = __ldcg(&stats[slot * kHalf + row_l]).x;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -715,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float g2 = k + e <= t.cta1 ? weight(w[e]) : 0.0f;
+            const float g2 = k + e <= cta1 ? weight(w[e]) : 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               sum[4 * i] += g2 * v[e][i].x, sum[4 * i + 1] += g2 * v[e][i].y;
@@ -723,12 +738,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        stage_columns(sm_rows, row_l, c, sum, f);
+        store_columns(c, sum, f, at_row, there);
       }
-      store_rows();
-      if (live && a.lse) a.lse[at_row] = log_sum(top, den);
+      if (there && a.lse) a.lse[at_row] = log_sum(top, den);
     }
   } else if (warp < kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFillRegs));
     // ------------------------------------------------- codes to f16 operands
     // A warp converts slices of its own, so that the codes it has under way in
     // shared memory concern nobody else. The loops stay rolled: the three
@@ -747,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool has_v = vq < D / 64;
     const KvBlock blk = kv_block(a.page_size, D);
     const int page_mask = a.page_size - 1, page_shift = 31 - __clz(a.page_size);
-    const uint32_t raw = sm_v + 2 * H::kK + fw * H::kRaw;
+    const uint32_t raw = sm_raw + fw * H::kRaw;
     uint32_t kc = 0;
     begin();
     while (next()) {
@@ -944,27 +959,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) {
           ptx::tc_fence_after();
           for (int x = 0; x < halves; ++x) scores(x, kc & 1);
-          ptx::tc_commit(bar(bars.k_empty[kc & 1]));
         }
         for (int j = 0; ok && j < tiles; ++j, ++kc) {
           const bool again = j + 1 < tiles;
           const uint32_t st = kc & 1, nst = (kc + 1) & 1;
           ok = wait(bars.v_full[st], (kc >> 1) & 1);
+          // the next keys are there long before the scores have been worked on
+          if (again) ok = ok && wait(bars.k_full[nst], ((kc + 1) >> 1) & 1);
           for (int x = 0; ok && x < halves; ++x) {
             if (!(ok = wait(bars.p_ready[x], p_phase[x]))) break;
             p_phase[x] ^= 1;
             ptx::tc_fence_after();
             sums(x, st, j > 0);
-            if (x == halves - 1) ptx::tc_commit(bar(bars.v_empty[st]));
-            if (again) {
-              // S takes the place of the P that the products before it read:
-              // matrix instructions of one thread run in the order of issue
-              if (x == 0 && !(ok = wait(bars.k_full[nst], ((kc + 1) >> 1) & 1))) break;
-              scores(x, nst);
-              if (x == halves - 1) ptx::tc_commit(bar(bars.k_empty[nst]));
-            } else {
-              ptx::tc_commit(bar(bars.o_done[x]));
-            }
+            // S takes the place of the P that the products before it read:
+            // matrix instructions of one thread run in the order of issue
+            if (again) scores(x, nst);
+            else ptx::tc_commit(bar(bars.o_done[x]));
           }
         }
       }
