@@ -130,6 +130,17 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
+// True in one lane of a warp that runs converged.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // Two fp32 values in a 64-bit register, and the instructions on both at once.
 __device__ __forceinline__ uint64_t pair_b32(uint32_t lo, uint32_t hi) {
   uint64_t r;
@@ -394,11 +405,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(~0u, s_tmem, 0);  // (known to be uniform)
   pdl_enter();
   const int group = a.heads / a.kv_heads;
+  const uint64_t limit = ptx::wait_limit();
   auto wait = [&](const uint64_t& b, uint32_t parity) {
-    return ptx::mbar_wait_asleep(bar(b), parity, &s_abort, status);
+    return ptx::mbar_wait_asleep(bar(b), parity, limit, &s_abort, status);
   };
   // The same for a whole warp: all lanes go on or none (a timeout may reach
   // some lanes only, and tensor memory is read by whole warps).
@@ -921,70 +933,70 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
   }
   if (warp == kMmaWarp) {
-    // ------------------------------------------------------ the matrix thread
-    uint32_t kc = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+    // -------------------------------------------------------- the matrix warp
+    // The whole warp walks the loop and one elected lane issues: only in code
+    // that all lanes run can the operands stay in uniform registers (otherwise
+    // issuing takes 60 to 100 cycles per instruction, more than executing).
+    uint32_t kc = 0, q_phase = 0, p_phase = 0;
     const uint32_t id_s = ptx::idesc_make(0, kHalf, kKeys), id_o = ptx::idesc_make(0, kHalf, D);
+    auto scores = [&](int x, uint32_t st) {
+      const uint64_t da = ptx::sdesc_sw128(sm_q + x * H::kQ);
+      const uint64_t db = ptx::sdesc_sw128(sm_k + st * H::kK);
+      const uint32_t d = tmem + kColsS + x * kKeys;
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)  // 16-byte units: panels, 32 bytes within one
+          ptx::tc_mma<false>(d, da + (kk / 4) * (kHalf * 8) + (kk % 4) * 2,
+                             db + (kk / 4) * (kKeys * 8) + (kk % 4) * 2, id_s, kk > 0);
+        ptx::tc_commit(bar(bars.s_full[x]));
+      }
+      __syncwarp();
+    };
     begin();
     while (next()) {
+      const int halves = __shfl_sync(~0u, t.halves, 0), tiles = __shfl_sync(~0u, t.tiles, 0);
+      if (tiles == 0) continue;
       bool ok = true;
-      if (lane == 0 && t.tiles > 0) {
-        auto scores = [&](int x, uint32_t st) {
-#pragma unroll
-          for (int pnl = 0; pnl < D / 64; ++pnl) {
-            const uint64_t da = ptx::sdesc_sw128(sm_q + x * H::kQ + pnl * kHalf * 128);
-            const uint64_t db = ptx::sdesc_sw128(sm_k + st * H::kK + pnl * kKeys * 128);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              ptx::tc_mma<false>(tmem + kColsS + x * kKeys, da + 2 * kk, db + 2 * kk, id_s,
-                                 pnl + kk > 0);
-          }
-          ptx::tc_commit(bar(bars.s_full[x]));
-        };
-        auto sums = [&](int x, uint32_t st, bool more) {
-#pragma unroll
-          for (int pnl = 0; pnl < kKeys / 64; ++pnl) {
-            const uint64_t db = ptx::sdesc_sw128(sm_v + st * H::kK + pnl * D * 128);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_ts(tmem + kColsO + x * D, tmem + kColsS + x * kKeys + pnl * 32 + kk * 8,
-                     db + 2 * kk, id_o, more || pnl + kk > 0);
-          }
-        };
-        const int halves = t.halves, tiles = t.tiles;
-        for (int x = 0; ok && x < halves; ++x) {
-          ok = wait(bars.q_ready[x], q_phase[x]);
-          q_phase[x] ^= 1;
-        }
-        ok = ok && wait(bars.k_full[kc & 1], (kc >> 1) & 1);
-        if (ok) {
+#pragma unroll 1
+      for (int x = 0; ok && x < halves; ++x) ok = wait_warp(bars.q_ready[x], (q_phase >> x) & 1);
+      q_phase ^= (1u << halves) - 1u;
+      ok = ok && wait_warp(bars.k_full[kc & 1], (kc >> 1) & 1);
+      if (!ok) break;
+      ptx::tc_fence_after();
+#pragma unroll 1
+      for (int x = 0; x < halves; ++x) scores(x, kc & 1);
+#pragma unroll 1
+      for (int j = 0; ok && j < tiles; ++j, ++kc) {
+        const bool again = j + 1 < tiles;
+        const uint32_t st = kc & 1, nst = (kc + 1) & 1;
+        if (!(ok = wait_warp(bars.v_full[st], (kc >> 1) & 1))) break;
+        // the next keys are there long before the scores have been worked on
+        if (again && !(ok = wait_warp(bars.k_full[nst], ((kc + 1) >> 1) & 1))) break;
+#pragma unroll 1
+        for (int x = 0; x < halves; ++x) {
+          if (!(ok = wait_warp(bars.p_ready[x], (p_phase >> x) & 1))) break;
           ptx::tc_fence_after();
-          for (int x = 0; x < halves; ++x) scores(x, kc & 1);
-        }
-        for (int j = 0; ok && j < tiles; ++j, ++kc) {
-          const bool again = j + 1 < tiles;
-          const uint32_t st = kc & 1, nst = (kc + 1) & 1;
-          ok = wait(bars.v_full[st], (kc >> 1) & 1);
-          // the next keys are there long before the scores have been worked on
-          if (again) ok = ok && wait(bars.k_full[nst], ((kc + 1) >> 1) & 1);
-          for (int x = 0; ok && x < halves; ++x) {
-            if (!(ok = wait(bars.p_ready[x], p_phase[x]))) break;
-            p_phase[x] ^= 1;
-            ptx::tc_fence_after();
-            sums(x, st, j > 0);
-            // S takes the place of the P that the products before it read:
-            // matrix instructions of one thread run in the order of issue
-            if (again) scores(x, nst);
-            else ptx::tc_commit(bar(bars.o_done[x]));
+          const uint64_t db = ptx::sdesc_sw128(sm_v + st * H::kK);
+          const uint32_t d = tmem + kColsO + x * D, p = tmem + kColsS + x * kKeys;
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              mma_ts(d, p + kk * 8, db + (kk / 4) * (D * 8) + (kk % 4) * 2, id_o, j + kk > 0);
+            if (!again) ptx::tc_commit(bar(bars.o_done[x]));
           }
+          __syncwarp();
+          // S takes the place of the P that the products before it read: matrix
+          // instructions of one thread run in the order of issue
+          if (again) scores(x, nst);
         }
+        p_phase ^= (1u << halves) - 1u;
       }
-      if (!__shfl_sync(~0u, static_cast<int>(ok), 0)) break;
+      if (!ok) break;
     }
     // whatever was issued has to land before the tensor memory is given back
-    if (lane == 0) {
-      ptx::tc_commit(bar(bars.drain));
-      ptx::mbar_wait_drain(bar(bars.drain), 0);
-    }
+    if (elect_one()) ptx::tc_commit(bar(bars.drain));
+    __syncwarp();
+    ptx::mbar_wait_drain(bar(bars.drain), 0);
   }
   ptx::tc_fence_before();
   __syncthreads();

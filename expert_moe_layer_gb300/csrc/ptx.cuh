@@ -96,6 +96,19 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
   }
 }
 
+// The same without any suspension of the thread.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // The same try, which may suspend the thread for up to `hint` ns.
 __device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t hint) {
   uint32_t ok;
@@ -109,17 +122,22 @@ __device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity,
   return ok != 0;
 }
 
-// mbar_wait whose first try sleeps for up to 20 us: a warp that waits for
-// another role of its CTA then spends no issue slots and no instruction fetches
-// on polling, which matters where the CTA's other warps need both.
-__device__ __forceinline__ bool mbar_wait_asleep(uint32_t bar, uint32_t parity,
+// mbar_wait whose tries sleep for up to 20 us: a warp that waits for another
+// role of its CTA then spends no issue slots and no instruction fetches on
+// polling, which matters where the CTA's other warps need both. The caller has
+// read the limit once (wait_limit); limits below the sleep are polled for.
+__device__ __forceinline__ uint64_t wait_limit() {
+  return *const_cast<volatile unsigned long long*>(&g_wait_limit_ns);
+}
+__device__ __forceinline__ bool mbar_wait_asleep(uint32_t bar, uint32_t parity, uint64_t limit,
                                                  volatile int* abort, unsigned* status) {
   constexpr uint32_t kSleepNs = 20000;
-  if (mbar_try_wait_for(bar, parity, kSleepNs)) return true;
+  if (limit >= kSleepNs && mbar_try_wait_for(bar, parity, kSleepNs)) return true;
   const uint64_t t0 = globaltimer();
-  const uint64_t limit = g_wait_limit_ns;
   for (;;) {
-    if (mbar_try_wait_for(bar, parity, kSleepNs)) return true;
+    if (limit >= kSleepNs ? mbar_try_wait_for(bar, parity, kSleepNs)
+                          : mbar_test_wait(bar, parity))
+      return true;
     if (*abort) return false;
     if (globaltimer() - t0 > limit) {
       *abort = 1;
