@@ -779,67 +779,67 @@ __global__ void __launch_bounds__(kThreads, 1)
     begin();
     while (next()) {
       const int32_t* pages = a.page_table + static_cast<long>(t.b) * a.max_pages;
-      // The page of keys key .. key + more (0 where no row sees one of them).
-      auto page_of = [&](int key, int more) {
-        return key < t.hi && key + more >= t.lo ? pages[key >> page_shift] : 0;
+      // The page of eight keys from `key` (0 where no row sees one of them).
+      auto page_of = [&](int key) {
+        return key < t.hi && key + 7 >= t.lo ? pages[key >> page_shift] : 0;
       };
-      auto block_of = [&](int id, bool& ok) {
+      auto checked = [&](int id, bool& ok) {
         ok = id >= 0 && id < a.num_pages;
-        return a.cache + (static_cast<long>(ok ? id : 0) * a.kv_heads + t.kvh) * blk.bytes;
+        return ok ? id : 0;
+      };
+      auto block_of = [&](int id) {
+        return a.cache + (static_cast<long>(id) * a.kv_heads + t.kvh) * blk.bytes;
       };
       // While a tile's keys or values are converted, its values or the next
-      // tile's keys are copied; page ids are read one tile ahead of that.
+      // tile's keys are copied; page ids are read one tile ahead of that. Eight
+      // neighbouring tokens lie on one page.
       bool k_ok = true, v_ok = true;
-      int kid = page_of(t.first * kKeys + kr, 0), vid = page_of(t.first * kKeys + vt, 7);
+      int kid = page_of(t.first * kKeys + (kr & ~7)), vid = page_of(t.first * kKeys + vt);
       auto copy_k = [&](int j) {
         if (j < t.tiles) {
-          const int key = (t.first + j) * kKeys + kr, row = key & page_mask;
-          const uint8_t* p = block_of(kid, k_ok);
-          const long codes = reinterpret_cast<long>(p + row * (D / 2) + kpart * (kChans / 2));
-          constexpr int kChunks = kChans / 32;  // 16-byte chunks of a row
-#pragma unroll 1
+          const int key = (t.first + j) * kKeys + kr, key0 = key - lane;
+          const int id = checked(kid, k_ok);
+          constexpr int kChunks = kChans / 32, kRows = 32 / kChunks;  // 16-byte chunks of a row,
+          const int r0 = lane / kChunks, c = lane % kChunks;          // rows copied at a time
+          // chunks of a row are swizzled by the row: lanes read one chunk of 32
+          // rows at a time
+          const int place = kChunks == 4 ? c ^ ((r0 >> 1) & 3) : c ^ ((r0 >> 2) & 1);
+#pragma unroll
           for (int i = 0; i < kChunks; ++i) {
-            const int n = 32 * i + lane, r = n / kChunks, c = n % kChunks;
-            const long src = __shfl_sync(~0u, codes, r);
-            // chunks of a row are swizzled by the row: lanes read one chunk of
-            // 32 rows at a time
-            const int place = kChunks == 4 ? c ^ ((r >> 1) & 3) : c ^ ((r >> 2) & 1);
+            const int r = kRows * i + r0;
+            const uint8_t* p = block_of(__shfl_sync(~0u, id, r & ~7));
             ptx::cp_async16(raw + (r * kChunks + place) * 16,
-                            reinterpret_cast<const void*>(src + 16 * c));
+                            p + ((key0 + r) & page_mask) * (D / 2) + kpart * (kChans / 2) + 16 * c);
           }
           cp_async_small<kChans / 16>(raw + H::kRawKs + lane * (kChans / 16),
-                                      p + blk.k_scale + row * (D / 16) + kpart * (kChans / 16));
-          if (j + 1 < t.tiles) kid = page_of(key + kKeys, 0);
+                                      block_of(id) + blk.k_scale + (key & page_mask) * (D / 16) +
+                                          kpart * (kChans / 16));
+          if (j + 1 < t.tiles) kid = page_of((key & ~7) + kKeys);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
       auto copy_v = [&](int j) {
         if (j < t.tiles && has_v) {
-          const int key = (t.first + j) * kKeys + vt;
-          const uint8_t* p = block_of(vid, v_ok);
-          const long block = reinterpret_cast<long>(p);
-          const int row0 = key & page_mask;  // of the lane's eight tokens
-#pragma unroll 1
+          const int key = (t.first + j) * kKeys + vt, key0 = (t.first + j) * kKeys + v0;
+          const int id = checked(vid, v_ok);
+          // token 8 * g + e of the slice goes to row 8 * e + g: the lanes' g-th
+          // groups lie side by side
+#pragma unroll
           for (int i = 0; i < 4; ++i) {
-            // token 8 * g + e of the slice goes to row 8 * e + g: the lanes'
-            // g-th groups lie side by side
-            const int n = 32 * i + lane, tok = n >> 1, g = tok >> 3, e = tok & 7;
-            const long src = __shfl_sync(~0u, block, g);
-            const int row = __shfl_sync(~0u, row0, g) + e;
-            ptx::cp_async16(raw + H::kRawV + (8 * e + g) * 32 + (n & 1) * 16,
-                            reinterpret_cast<const void*>(src + blk.v_code + row * (D / 2) +
-                                                          vq * 32 + (n & 1) * 16));
+            const int tok = 16 * i + (lane >> 1), g = tok >> 3, e = tok & 7;
+            const uint8_t* p = block_of(__shfl_sync(~0u, id, g));
+            ptx::cp_async16(raw + H::kRawV + (8 * e + g) * 32 + (lane & 1) * 16,
+                            p + blk.v_code + ((key0 + tok) & page_mask) * (D / 2) + vq * 32 +
+                                (lane & 1) * 16);
           }
-#pragma unroll 1
+#pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int tok = 32 * i + lane, g = tok >> 3, e = tok & 7;
-            const long src = __shfl_sync(~0u, block, g);
-            const int row = __shfl_sync(~0u, row0, g) + e;
+            const uint8_t* p = block_of(__shfl_sync(~0u, id, g));
             cp_async_small<4>(raw + H::kRawVs + (8 * e + g) * 4,
-                              reinterpret_cast<const uint8_t*>(src + blk.v_scale + row * (D / 16) +
-                                                               vq * 4));
+                              p + blk.v_scale + ((key0 + tok) & page_mask) * (D / 16) + vq * 4);
           }
-          if (j + 1 < t.tiles) vid = page_of(key + kKeys, 7);
+          if (j + 1 < t.tiles) vid = page_of(key + kKeys);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
@@ -858,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         asm volatile("cp.async.wait_group 1;" ::: "memory");  // the keys, not the values
         __syncwarp();
-#pragma unroll 1
+#pragma unroll 2
         for (int i = 0; i < kChans / 32; ++i) {
           constexpr int kChunks = kChans / 32;
           const int place = kChunks == 4 ? i ^ ((lane >> 1) & 3) : i ^ ((lane >> 2) & 1);
@@ -970,8 +970,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool again = j + 1 < tiles;
         const uint32_t st = kc & 1, nst = (kc + 1) & 1;
         if (!(ok = wait_warp(bars.v_full[st], (kc >> 1) & 1))) break;
-        // the next keys are there long before the scores have been worked on
-        if (again && !(ok = wait_warp(bars.k_full[nst], ((kc + 1) >> 1) & 1))) break;
 #pragma unroll 1
         for (int x = 0; x < halves; ++x) {
           if (!(ok = wait_warp(bars.p_ready[x], (p_phase >> x) & 1))) break;
@@ -987,7 +985,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           // S takes the place of the P that the products before it read: matrix
           // instructions of one thread run in the order of issue
-          if (again) scores(x, nst);
+          if (again) {
+            if (x == 0 && !(ok = wait_warp(bars.k_full[nst], ((kc + 1) >> 1) & 1))) break;
+            scores(x, nst);
+          }
         }
         p_phase ^= (1u << halves) - 1u;
       }

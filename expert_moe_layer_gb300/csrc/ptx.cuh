@@ -132,6 +132,7 @@ __device__ __forceinline__ uint64_t wait_limit() {
 __device__ __forceinline__ bool mbar_wait_asleep(uint32_t bar, uint32_t parity, uint64_t limit,
                                                  volatile int* abort, unsigned* status) {
   constexpr uint32_t kSleepNs = 20000;
+  if (mbar_test_wait(bar, parity)) return true;
   if (limit >= kSleepNs && mbar_try_wait_for(bar, parity, kSleepNs)) return true;
   const uint64_t t0 = globaltimer();
   for (;;) {
