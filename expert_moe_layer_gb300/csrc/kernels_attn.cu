@@ -35,7 +35,7 @@ namespace {
 constexpr int kTile = 16;   // cached tokens per tile
 constexpr int kWarps = 4;   // per CTA; each takes every fourth tile of a segment
 constexpr int kThreads = kWarps * 32;
-constexpr int kMinTiles = 2 * kWarps;  // smallest range of a CTA
+constexpr int kMinTiles = kWarps;  // smallest range of a CTA
 // A segment's set-up (its queries, the join of the warps, its rows' stores)
 // takes a CTA as long as this many tiles; the list counts them.
 constexpr int kSetup = 14;

@@ -130,6 +130,11 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
+// The lowest n bits, of none to all.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
+}
+
 // True in one lane of a warp that runs converged.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -463,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The warp's rows of queries, whole rows by neighbouring lanes, scaled to
     // f16; each lane keeps its own row's gain.
     auto load_queries = [&] {
-      constexpr int kRowLanes = D / 8, kRowsStep = 32 / kRowLanes, kBatch = 8;
+      constexpr int kRowLanes = D / 8, kRowsStep = 32 / kRowLanes, kBatch = 4;
       const long src = (t.sq.q0 + (live ? tok : 0)) * a.q.token + (live ? head : 0) * a.q.head;
 #pragma unroll 1
       for (int first = 0; first < kRowLanes; first += kBatch) {
@@ -540,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (more) load_queries();
     while (more) {
       const int p = t.sq.len - t.sq.q_len + tok;
-      const int last = live ? p : 0x7fffffff;
+      const int last = live ? p : 0x7ffffff0;  // (one more is added below)
       const int first = live && a.window > 0 ? p - a.window + 1 : 0;
       // keys that every row of the half sees
       const int r_lo = t.row0 + x * kHalf, r_hi = min(t.rows, r_lo + kHalf) - 1;
@@ -575,12 +580,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_landed(*reinterpret_cast<uint32_t(*)[32]>(s));
           tmem_landed(*reinterpret_cast<uint32_t(*)[32]>(s + 32));
           if (!inside || (bad.x | bad.y) != 0) {
+            // keys from `first` to `last`, but those on bad pages, as bits
+            const int key0 = tok0 + 64 * c;
+            const uint32_t seen[2] = {low_bits(last + 1 - key0) & ~low_bits(first - key0) & ~bad.x,
+                                      low_bits(last - 31 - key0) & ~low_bits(first - 32 - key0) &
+                                          ~bad.y};
 #pragma unroll
-            for (int i = 0; i < 64; ++i) {
-              const int key = tok0 + 64 * c + i;
-              if (key < first || key > last || (((i < 32 ? bad.x : bad.y) >> (i & 31)) & 1u))
-                s[i] = 0xff800000u;
-            }
+            for (int i = 0; i < 64; ++i)
+              if (!(seen[i / 32] & (1u << (i % 32)))) s[i] = 0xff800000u;
           }
           uint32_t pk[32];
           uint64_t add[2];
