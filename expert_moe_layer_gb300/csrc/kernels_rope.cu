@@ -252,6 +252,89 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int cq, int 
   }
 }
 
+// Any even R, 16-byte aligned rows: a thread makes one 16-byte chunk of the
+// output. The other elements of a half-layout chunk's pairs start anywhere and
+// are read one by one (they are other lanes' chunks, so L1 has them). A row
+// rotated in place is read by all of its lanes before any of them writes, which
+// one warp has to do: the launch sees to it.
+template <typename T, bool kInterleaved, int kHeads>
+__global__ void __launch_bounds__(kThreads) rope_wide_kernel(RopeArgs a, int cq, int ck,
+                                                             unsigned total) {
+  constexpr int V = 16 / sizeof(T);
+  constexpr int kSharers = kKvGroup / V;
+  pdl_enter();
+  const unsigned idx = blockIdx.x * kThreads + threadIdx.x;
+  if (idx >= total) return;
+  const unsigned units = a.D / V;
+  const int c0 = static_cast<int>(idx % units) * V;
+  const Chunk c = chunk_of(a, idx / units, kHeads, cq, ck);
+  const int pairs = c.kind == 2 ? 0 : a.R / 2;
+  const Rows rows = c.kind == 0 ? a.q : c.kind == 1 ? a.k : a.v;
+  const T* src = static_cast<const T*>(rows.p) + c.t * rows.token + c.h0 * rows.head;
+  uint4 raw[kHeads];
+  T other[kInterleaved ? 1 : kHeads][V];
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    if (c.h0 + i < c.h1) {
+      const T* p = src + i * rows.head;
+      raw[i] = *reinterpret_cast<const uint4*>(p + c0);
+      if constexpr (!kInterleaved) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const int ch = c0 + j;
+          if (ch < 2 * pairs) other[i][j] = p[ch < pairs ? ch + pairs : ch - pairs];
+        }
+      }
+    }
+  }
+  long slot = 0;
+  if (c.kind && (slot = slot_of(a, c.t)) < 0) return;
+  bool ok = true;
+  const float* row = table_row(a, c.t, ok);
+  if (!ok) return;
+  float cs[V], sn[V];  // of each channel: own * cos + other * (+- sin)
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int ch = c0 + j;
+    if (ch < 2 * pairs) {
+      const int pair = kInterleaved ? ch / 2 : ch < pairs ? ch : ch - pairs;
+      const bool first = kInterleaved ? j % 2 == 0 : ch < pairs;
+      cs[j] = row[pair];
+      const float v = row[pairs + pair];
+      sn[j] = first != (a.inverse != 0) ? -v : v;
+    }
+  }
+  Place at = {nullptr, 0};
+  if (c.kind) at = place_of(a, slot);
+  const int lane = threadIdx.x & 31;
+  const unsigned lanes = ((1u << kSharers) - 1u) << (lane & ~(kSharers - 1));
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    const int h = c.h0 + i;
+    if (h >= c.h1) break;
+    float x[V], y[V];
+    unpack_chunk(raw[i], x);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      y[j] = x[j];
+      if (c0 + j < 2 * pairs) {
+        float o;
+        if constexpr (kInterleaved) o = x[j ^ 1];
+        else o = to_f(other[i][j]);
+        y[j] = __fadd_rn(__fmul_rn(x[j], cs[j]), __fmul_rn(o, sn[j]));
+      }
+    }
+    if (c.kind == 0) {
+      store_chunk(static_cast<T*>(a.q_out) + (static_cast<long>(c.t) * a.q_heads + h) * a.D + c0, y);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) y[j] = to_f(from_f<T>(y[j]));
+      store_codes<V>(a, c.kind == 2, at, h, c0, y, lanes);
+    }
+  }
+}
+
 // Any D, R and strides, one element at a time. A query's pairs are shared out
 // over the head's threads (each pair read and written by one thread); keys and
 // values go group by group, a key's other channels read where they are.
@@ -393,12 +476,18 @@ bool rows_aligned(const Rows& r, int eb) {
 template <typename T>
 cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t st) {
   const int eb = sizeof(T);
-  const bool fast = a.D % 32 == 0 && a.R % 32 == 0 &&
-                    (a.q_heads == 0 || (rows_aligned(a.q, eb) &&
-                                        reinterpret_cast<uintptr_t>(a.q_out) % 16 == 0)) &&
-                    (a.kv_heads == 0 || (rows_aligned(a.k, eb) && rows_aligned(a.v, eb))) &&
+  const bool rows16 = a.D % kKvGroup == 0 &&
+                      (a.q_heads == 0 || (rows_aligned(a.q, eb) &&
+                                          reinterpret_cast<uintptr_t>(a.q_out) % 16 == 0)) &&
+                      (a.kv_heads == 0 || (rows_aligned(a.k, eb) && rows_aligned(a.v, eb)));
+  const bool fast = rows16 && a.D % 32 == 0 && a.R % 32 == 0 &&
                     reinterpret_cast<uintptr_t>(a.table) % 16 == 0;
-  const long units = fast ? a.D / (32 / eb) : (a.D + 15) / 16;
+  // (8192 tokens, 40 heads of 128 in bf16: 34.5 us fast; wide 58.8 us for 66 of the
+  // channels in halves and 39.3 us for 98 interleaved; one element at a time
+  // 124 and 131 us)
+  const int lanes = a.D / (16 / eb);
+  const bool wide = rows16 && !fast && (a.q.p != a.q_out || 32 % lanes == 0);
+  const long units = fast ? lanes / 2 : wide ? lanes : (a.D + 15) / 16;
   // heads per thread: 4 once that still gives every SM its 2048 threads
   const long all = units * a.T * (a.q_heads + 2l * a.kv_heads);
   const int hb = all / 4 >= 152l * 2048 ? 4 : 1;
@@ -408,6 +497,12 @@ cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t st) {
   if (total > 0xffffff00l) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>((total + kThreads - 1) / kThreads)), block(kThreads);
   const unsigned n = static_cast<unsigned>(total);
+  if (wide) {
+    auto* kern = a.interleaved
+                     ? (hb == 1 ? &rope_wide_kernel<T, true, 1> : &rope_wide_kernel<T, true, 4>)
+                     : (hb == 1 ? &rope_wide_kernel<T, false, 1> : &rope_wide_kernel<T, false, 4>);
+    return launch_pdl(kern, grid, block, 0, st, a, cq, ck, n);
+  }
   if (!fast) return launch_pdl(&rope_any_kernel<T>, grid, block, 0, st, a, hb, cq, ck, n);
   auto* kern = a.interleaved ? (hb == 1 ? &rope_kernel<T, true, 1> : &rope_kernel<T, true, 4>)
                              : (hb == 1 ? &rope_kernel<T, false, 1> : &rope_kernel<T, false, 4>);

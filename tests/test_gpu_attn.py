@@ -71,6 +71,9 @@ ROPE = [  # dtype, T, heads, D, R, layout, slack heads
     ("bf16", 2, 2, 128, 0, "half", 1), ("f32", 6, 1, 512, 2, "half", 0),
     ("bf16", 1100, 16, 128, 96, "half", 4), ("bf16", 2, 3, 18, 10, "half", 0),
     ("bf16", 900, 24, 128, 128, "interleaved", 2),
+    ("bf16", 1000, 20, 128, 66, "half", 1), ("bf16", 1000, 20, 128, 98, "interleaved", 1),
+    ("f32", 700, 16, 256, 200, "half", 1), ("f32", 40, 5, 256, 34, "half", 0),
+    ("bf16", 37, 5, 64, 2, "half", 2), ("bf16", 9, 3, 48, 46, "half", 0), ("f32", 3, 2, 64, 62, "half", 1),
 ]
 
 
@@ -126,6 +129,8 @@ APPEND = [  # dtype, T, heads, kv heads, D, R, layout, page, k_scale
     ("f32", 11, 2, 2, 64, 30, "interleaved", 128, 0.7), ("bf16", 8, 2, 1, 128, 0, "half", 16, 1.0),
     ("bf16", 700, 32, 8, 128, 128, "half", 64, 1.0),
     ("bf16", 600, 40, 8, 128, 64, "interleaved", 256, 1.0),
+    ("bf16", 700, 24, 8, 128, 98, "half", 64, 1.0), ("bf16", 500, 24, 8, 64, 46, "interleaved", 16, 1.0),
+    ("f32", 90, 6, 2, 256, 250, "half", 32, 1.0),
 ]
 
 
