@@ -1,6 +1,6 @@
 // Attention over the 4-bit paged cache: the split kernel.
 //
-// A work unit is a tile of 16 cached tokens of one (request, row tile, kv
+// A work unit is a tile of 32 cached tokens of one (request, row tile, kv
 // head) segment; a row is one (query token, query head of the group) pair and
 // a row tile has 4, 8 or 16 of them. All segments' tiles form one list, which is
 // cut into equal ranges, one per CTA, so that requests of any lengths fill the
@@ -32,14 +32,15 @@
 namespace moe {
 namespace {
 
-constexpr int kTile = 16;   // cached tokens per tile
+constexpr int kSub = 16;    // cached tokens per matrix instruction, never across pages
+constexpr int kTile = 32;   // cached tokens per tile: what a warp takes at a time
 constexpr int kWarps = 4;   // per CTA; each takes every fourth tile of a segment
 constexpr int kThreads = kWarps * 32;
 constexpr int kMinTiles = kWarps;  // smallest range of a CTA
 // A segment's set-up (its queries, the join of the warps, its rows' stores)
 // takes a CTA as long as this many tiles; the list counts them.
-constexpr int kSetup = 14;
-constexpr int kStages = 4;  // tiles a warp has in shared memory or on the way
+constexpr int kSetup = 7;
+constexpr int kStages = 2;  // tiles a warp has in shared memory or on the way
 constexpr int kMaxCtasPerSm = 4;
 constexpr int kPlanThreads = 1024;
 constexpr int kInlineSeqs = 256;  // up to so many requests are planned by every CTA
@@ -119,28 +120,32 @@ __device__ __forceinline__ uint32_t load_scales(const uint8_t* p) {
 }
 
 template <int D>
-struct TileRegs {
-  Words<D / 32> k[2];  // key rows g, g + 8 of the tile: D/4 channels
+struct KeyRegs {
+  Words<D / 32> k[2];  // key rows g, g + 8 of a sub-tile: D/4 channels
+  uint32_t s[2];
+};
+template <int D>
+struct ValueRegs {
   Words<D / 64> v[4];  // value rows 2c, 2c+1, 2c+8, 2c+9: D/8 channels
-  uint32_t ks[2], vs[4];
+  uint32_t s[4];
 };
 
-// A tile in shared memory: the rows of key codes, value codes, key scales and
+// A sub-tile in shared memory: the rows of key codes, value codes, key scales and
 // value scales. Value rows are swizzled (bits 5 and 6 of the offset), so that
 // the four even or odd rows that a quarter of the lanes reads lie in different
 // banks.
 template <int D>
 struct TileBytes {
   static constexpr int kRow = D / 2, kScales = D / kKvGroup;
-  static constexpr int kCodes = kTile * kRow, kAllScales = kTile * kScales;
+  static constexpr int kCodes = kSub * kRow, kAllScales = kSub * kScales;
   static constexpr int kV = kCodes, kKs = 2 * kCodes, kVs = kKs + kAllScales;
-  static constexpr int kBytes = kVs + kAllScales;
+  static constexpr int kBytes = kVs + kAllScales, kTileBytes = kTile / kSub * kBytes;
   __device__ static constexpr uint32_t value(int row, int byte) {
     return static_cast<uint32_t>((row * kRow + byte) ^ (((row >> 1) & 3) << 5));
   }
 };
 
-// Copies a tile (rows row0 .. row0 + 15 of a block) into a stage.
+// Copies a sub-tile (rows row0 .. row0 + 15 of a block) into its place.
 template <int D>
 __device__ __forceinline__ void copy_tile(uint32_t stage, const uint8_t* block, int page_size,
                                           int row0, int lane) {
@@ -161,28 +166,32 @@ __device__ __forceinline__ void copy_tile(uint32_t stage, const uint8_t* block, 
   }
 }
 
-// The codes and scales of a staged tile for lane (g, c) = (lane / 4, lane % 4).
+// The codes and scales of a staged sub-tile for lane (g, c) = (lane / 4, lane % 4).
 template <int D>
-__device__ __forceinline__ void load_tile(TileRegs<D>& t, const uint8_t* stage, int g, int c) {
+__device__ __forceinline__ void load_keys(KeyRegs<D>& t, const uint8_t* stage, int g, int c) {
   using B = TileBytes<D>;
-  constexpr int kVs = D >= 128 ? D / 128 : 1;  // scales a lane's value channels fall under
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = g + 8 * i;
     t.k[i] = load_words<D / 32>(stage + r * B::kRow + c * (D / 8));
-    t.ks[i] = load_scales<D / 64>(stage + B::kKs + r * B::kScales + c * (D / 64));
+    t.s[i] = load_scales<D / 64>(stage + B::kKs + r * B::kScales + c * (D / 64));
   }
+}
+template <int D>
+__device__ __forceinline__ void load_values(ValueRegs<D>& t, const uint8_t* stage, int g, int c) {
+  using B = TileBytes<D>;
+  constexpr int kVs = D >= 128 ? D / 128 : 1;  // scales a lane's value channels fall under
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = 2 * c + (i & 1) + 8 * (i >> 1);
     t.v[i] = load_words<D / 64>(stage + B::kV + B::value(r, g * (D / 16)));
-    t.vs[i] = load_scales<kVs>(stage + B::kVs + r * B::kScales + g * D / 8 / kKvGroup);
+    t.s[i] = load_scales<kVs>(stage + B::kVs + r * B::kScales + g * D / 8 / kKvGroup);
   }
 }
 
 template <int D, int kRows>
 __host__ __device__ constexpr int split_smem() {
-  constexpr int stages = kWarps * kStages * TileBytes<D>::kBytes, sums = kWarps * kRows * D * 4;
+  constexpr int stages = kWarps * kStages * TileBytes<D>::kTileBytes, sums = kWarps * kRows * D * 4;
   constexpr int join = kAttnMaxSms * (kRows == 16 ? 2 : kMaxCtasPerSm) * kRows * 8;
   constexpr int most = stages > sums ? stages : sums;
   return (most > join ? most : join) + kWarps * kRows * 8;
@@ -206,7 +215,7 @@ __host__ __device__ constexpr int ctas_per_sm() {
 template <typename T, int D, int kRows, int kTerms, bool kInline>
 __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
     attn_split_kernel(AttnArgs a, unsigned* status, int* counters, const SeqInfo* info_in,
-                      const long* starts_in, float* stats, float* partial, int tiles_per_page_log2) {
+                      const long* starts_in, float* stats, float* partial, int page_shift) {
   constexpr bool kBoth = kRows == 4;             // columns 4-7 repeat rows 0-3
   constexpr int NT = kBoth ? 1 : kRows / 8;      // column tiles of the scores
   constexpr int NP = kBoth ? 1 : 2 * NT;         // column tiles of the sums
@@ -361,31 +370,44 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
     const int tB = min(t1, tile_last < 0 ? 0 : tile_last / kTile + 1 - first_tile);
     const int32_t* pages = a.page_table + static_cast<long>(b) * a.max_pages;
     // The CTA's warps take the tiles of the range in turn. Each keeps a ring of
-    // kStages tiles: the copies run kStages - 1 tiles ahead, the page id one
-    // more.
-    uint8_t* ring = reinterpret_cast<uint8_t*>(smem) + warp * kStages * TileBytes<D>::kBytes;
+    // kStages tiles: the copies run kStages - 1 tiles ahead, the page ids one
+    // more. The two sub-tiles may lie on two pages.
+    constexpr int kSubs = kTile / kSub;
+    uint8_t* ring = reinterpret_cast<uint8_t*>(smem) + warp * kStages * TileBytes<D>::kTileBytes;
     const uint32_t ring_addr = ptx::smem_u32(ring);
-    auto page_of = [&](int t) {
-      return t < tB ? pages[(t + first_tile) >> tiles_per_page_log2] : 0;
-    };
-    uint32_t ok_bits = 0;  // by stage: the page id was good
-    auto copy = [&](int t, int stage, int id) {
+    auto pages_of = [&](int t) {  // (0 for a sub-tile that no row sees)
+      int2 ids = make_int2(0, 0);
       if (t < tB) {
-        const bool ok = id >= 0 && id < a.num_pages;
-        if (!ok && lane == 0) atomicOr(status, MOE_DEV_BAD_PAGE);
-        ok_bits = (ok_bits & ~(1u << stage)) | (static_cast<uint32_t>(ok) << stage);
-        const int tile = t + first_tile;
-        copy_tile<D>(ring_addr + stage * TileBytes<D>::kBytes,
-                     a.cache + (static_cast<long>(ok ? id : 0) * a.kv_heads + kvh) * blk.bytes,
-                     a.page_size, (tile & ((1 << tiles_per_page_log2) - 1)) * kTile, lane);
+        const int tok = (t + first_tile) * kTile;
+        if (tok + kSub > tile_first) ids.x = pages[tok >> page_shift];
+        if (tok + kSub <= tile_last)
+          ids.y = page_shift == 4 ? pages[(tok + kSub) >> 4] : pages[tok >> page_shift];
+      }
+      return ids;
+    };
+    uint32_t ok_bits = 0;  // by stage and sub-tile: the page id was good
+    auto copy = [&](int t, int stage, int2 ids) {
+      if (t < tB) {
+        const int row = ((t + first_tile) * kTile) & ((1 << page_shift) - 1);
+#pragma unroll
+        for (int sub = 0; sub < kSubs; ++sub) {
+          const int id = sub ? ids.y : ids.x;
+          const bool ok = id >= 0 && id < a.num_pages;
+          if (!ok && lane == 0) atomicOr(status, MOE_DEV_BAD_PAGE);
+          const uint32_t bit = 1u << (stage * kSubs + sub);
+          ok_bits = ok ? ok_bits | bit : ok_bits & ~bit;
+          copy_tile<D>(ring_addr + stage * TileBytes<D>::kTileBytes + sub * TileBytes<D>::kBytes,
+                       a.cache + (static_cast<long>(ok ? id : 0) * a.kv_heads + kvh) * blk.bytes,
+                       a.page_size, page_shift == 4 ? 0 : row + sub * kSub, lane);
+        }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     int t = tA + warp;
     {
-      int ids[kStages - 1];
+      int2 ids[kStages - 1];
 #pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) ids[i] = page_of(t + i * kWarps);
+      for (int i = 0; i < kStages - 1; ++i) ids[i] = pages_of(t + i * kWarps);
       if (!entered) {
         // status and counters are clear from here on; everything else that is
         // read was written before the kernel that clears them
@@ -396,60 +418,79 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
 #pragma unroll
       for (int i = 0; i < kStages - 1; ++i) copy(t + i * kWarps, i, ids[i]);
     }
-    int next_id = page_of(t + (kStages - 1) * kWarps);
+    int2 next_ids = pages_of(t + (kStages - 1) * kWarps);
     for (int stage = 0; t < tB; t += kWarps, stage = stage + 1 == kStages ? 0 : stage + 1) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-      __syncwarp();  // every lane's copies of this tile, every lane's reads of the last one
-      copy(t + (kStages - 1) * kWarps, stage == 0 ? kStages - 1 : stage - 1, next_id);
-      next_id = page_of(t + kStages * kWarps);
-      const bool ok = (ok_bits >> stage) & 1u;
-      TileRegs<D> cur;
-      load_tile<D>(cur, ring + stage * TileBytes<D>::kBytes, g, c);
+      __syncwarp();  // every lane has read the stage that is copied to next
+      copy(t + (kStages - 1) * kWarps, stage == 0 ? kStages - 1 : stage - 1, next_ids);
+      next_ids = pages_of(t + kStages * kWarps);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      __syncwarp();  // every lane's copies of this tile have landed
+      const uint32_t oks = (ok_bits >> (stage * kSubs)) & ((1u << kSubs) - 1u);
+      const uint8_t* here = ring + stage * TileBytes<D>::kTileBytes;
       const int tok0 = (t + first_tile) * kTile;
-      const bool whole = ok && tok0 >= all_first && tok0 + kTile - 1 <= all_last;
+      const bool whole =
+          oks == (1u << kSubs) - 1u && tok0 >= all_first && tok0 + kTile - 1 <= all_last;
 
-      float s[NT][4];
+      float s[kSubs][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int sub = 0; sub < kSubs; ++sub) {
+        KeyRegs<D> cur;
+        load_keys<D>(cur, here + sub * TileBytes<D>::kBytes, g, c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[nt][j] = 0.0f;
-      uint32_t ks2[2][(D + 127) / 128];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+          for (int j = 0; j < 4; ++j) s[sub][nt][j] = 0.0f;
+        uint32_t ks2[2][(D + 127) / 128];
 #pragma unroll
-        for (int j = 0; j < (D + 127) / 128; ++j) ks2[i][j] = e4m3x2_to_f16(cur.ks[i] >> (16 * j));
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int w = 0; w < D / 32; ++w) {  // 8 channels of each row: two k steps
-        uint32_t k0[4], k1[4];
-        e2m1_to_f16(cur.k[0].w[w], k0);
-        e2m1_to_f16(cur.k[1].w[w], k1);
-        const int sc = w / 2;  // the scale these channels fall under
-        const uint32_t s0 = sc & 1 ? f16_high_twice(ks2[0][sc / 2]) : f16_low_twice(ks2[0][sc / 2]);
-        const uint32_t s1 = sc & 1 ? f16_high_twice(ks2[1][sc / 2]) : f16_low_twice(ks2[1][sc / 2]);
+          for (int j = 0; j < (D + 127) / 128; ++j) ks2[i][j] = e4m3x2_to_f16(cur.s[i] >> (16 * j));
 #pragma unroll
-        for (int hstep = 0; hstep < 2; ++hstep) {
-          const uint32_t af[4] = {hmul2(k0[2 * hstep], s0), hmul2(k1[2 * hstep], s1),
-                                  hmul2(k0[2 * hstep + 1], s0), hmul2(k1[2 * hstep + 1], s1)};
+        for (int w = 0; w < D / 32; ++w) {  // 8 channels of each row: two k steps
+          uint32_t k0[4], k1[4];
+          e2m1_to_f16(cur.k[0].w[w], k0);
+          e2m1_to_f16(cur.k[1].w[w], k1);
+          const int sc = w / 2;  // the scale these channels fall under
+          const uint32_t s0 =
+              sc & 1 ? f16_high_twice(ks2[0][sc / 2]) : f16_low_twice(ks2[0][sc / 2]);
+          const uint32_t s1 =
+              sc & 1 ? f16_high_twice(ks2[1][sc / 2]) : f16_low_twice(ks2[1][sc / 2]);
+#pragma unroll
+          for (int hstep = 0; hstep < 2; ++hstep) {
+            const uint32_t af[4] = {hmul2(k0[2 * hstep], s0), hmul2(k1[2 * hstep], s1),
+                                    hmul2(k0[2 * hstep + 1], s0), hmul2(k1[2 * hstep + 1], s1)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int term = 0; term < kTerms; ++term)
+                mma(s[sub][nt], af, qf[term][nt][4 * w + 2 * hstep],
+                    qf[term][nt][4 * w + 2 * hstep + 1]);
+          }
+        }
+      }
+      if (!whole) {
+#pragma unroll
+        for (int sub = 0; sub < kSubs; ++sub)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int term = 0; term < kTerms; ++term)
-              mma(s[nt], af, qf[term][nt][4 * w + 2 * hstep], qf[term][nt][4 * w + 2 * hstep + 1]);
-        }
+            for (int j = 0; j < 4; ++j) {
+              const int tok = tok0 + sub * kSub + g + 8 * (j >> 1);
+              if (!((oks >> sub) & 1u) || tok < first[nt][j & 1] || tok > last[nt][j & 1])
+                s[sub][nt][j] = -INFINITY;
+            }
       }
-      // scores in powers of two; [j] column 2c + (j & 1), token g + 8 (j >> 1)
+      // [j]: column 2c + (j & 1), token g + 8 (j >> 1)
       bool grow = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float x = s[nt][j] * gain[nt][j & 1];
-          if (!whole) {
-            const int tok = tok0 + g + 8 * (j >> 1);
-            if (!ok || tok < first[nt][j & 1] || tok > last[nt][j & 1]) x = -INFINITY;
-          }
-          s[nt][j] = x;
-          grow |= x > m[nt][j & 1] + kLag;
+        for (int j = 0; j < 2; ++j) {
+          float x = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
+#pragma unroll
+          for (int sub = 1; sub < kSubs; ++sub)
+            x = fmaxf(x, fmaxf(s[sub][nt][j], s[sub][nt][j + 2]));
+          grow |= x * gain[nt][j] > m[nt][j] + kLag;
         }
       if (__any_sync(~0u, grow)) {
 #pragma unroll
@@ -457,7 +498,11 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
           float f[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float x = fmaxf(fmaxf(s[nt][j], s[nt][j + 2]), m[nt][j]);
+            float x = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
+#pragma unroll
+            for (int sub = 1; sub < kSubs; ++sub)
+              x = fmaxf(x, fmaxf(s[sub][nt][j], s[sub][nt][j + 2]));
+            x = fmaxf(x * gain[nt][j], m[nt][j]);
             x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
             x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
             x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
@@ -476,80 +521,87 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
               for (int j = 0; j < 4; ++j) o[i][np][j] *= f[j & 1];
         }
       }
-      uint32_t pf[kTerms][NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float p[4];
+      for (int sub = 0; sub < kSubs; ++sub) {
+        // P in powers of two over the base, transposed to the B operand
+        uint32_t pf[kTerms][NT][2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          p[j] = ex2(s[nt][j] - base[nt][j & 1]);
-          l[nt][j & 1] += p[j];
-        }
+        for (int nt = 0; nt < NT; ++nt) {
+          float p[4];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t w = pack_f16(p[2 * half], p[2 * half + 1]);
-          pf[0][nt][half] = transpose8x8(w);
-          if constexpr (kTerms == 2) {
-            const float2 f = unpack_f16(w);
-            pf[1][nt][half] = transpose8x8(pack_f16(p[2 * half] - f.x, p[2 * half + 1] - f.y));
-          }
-        }
-      }
-      // V^T as the A operand. A token that no row sees may be uninitialised
-      // memory: its scale is zeroed, so that 0 * NaN cannot enter the sum.
-      uint32_t vs[4][kVs];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (!whole) {
-          const int tok = tok0 + 2 * c + (i & 1) + 8 * (i >> 1);
-          if (!ok || tok < tile_first || tok > tile_last) cur.vs[i] = 0;
-        }
-#pragma unroll
-        for (int j = 0; j < kVs; ++j)
-          vs[i][j] = e4m3x2_to_f16(((cur.vs[i] >> (8 * j)) & 0xffu) * 0x101u);
-      }
-      // P at the columns of one parity: of the even channels, then of the odd
-      uint32_t pb[kTerms][2][NP][2];  // [term][half of the tokens][column tile][token 2c, 2c + 1]
-#pragma unroll
-      for (int term = 0; term < kTerms; ++term)
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-          for (int np = 0; np < NP; ++np) {
-            const uint32_t w = pf[term][kBoth ? 0 : np / 2][half];
-            const bool odd = kBoth ? g >= 4 : np & 1;
-            pb[term][half][np][0] = __byte_perm(w, 0, odd ? 0x1044 : 0x4410);
-            pb[term][half][np][1] = __byte_perm(w, 0, odd ? 0x3244 : 0x4432);
+          for (int j = 0; j < 4; ++j) {
+            p[j] = ex2(fmaf(s[sub][nt][j], gain[nt][j & 1], -base[nt][j & 1]));
+            l[nt][j & 1] += p[j];
           }
 #pragma unroll
-      for (int w = 0; w < D / 64; ++w) {  // 8 channels: two m tiles
-        uint32_t h[4][4];
-        const int sc = D == 256 ? w / 2 : 0;
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t w = pack_f16(p[2 * half], p[2 * half + 1]);
+            pf[0][nt][half] = transpose8x8(w);
+            if constexpr (kTerms == 2) {
+              const float2 f = unpack_f16(w);
+              pf[1][nt][half] = transpose8x8(pack_f16(p[2 * half] - f.x, p[2 * half + 1] - f.y));
+            }
+          }
+        }
+        // V^T as the A operand. A token that no row sees may be uninitialised
+        // memory: its scale is zeroed, so that 0 * NaN cannot enter the sum.
+        ValueRegs<D> cur;
+        load_values<D>(cur, here + sub * TileBytes<D>::kBytes, g, c);
+        uint32_t vs[4][kVs];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          e2m1_to_f16(cur.v[i].w[w], h[i]);
+          if (!whole) {
+            const int tok = tok0 + sub * kSub + 2 * c + (i & 1) + 8 * (i >> 1);
+            if (!((oks >> sub) & 1u) || tok < tile_first || tok > tile_last) cur.s[i] = 0;
+          }
 #pragma unroll
-          for (int q = 0; q < 4; ++q) h[i][q] = hmul2(h[i][q], vs[i][sc]);
+          for (int j = 0; j < kVs; ++j)
+            vs[i][j] = e4m3x2_to_f16(((cur.s[i] >> (8 * j)) & 0xffu) * 0x101u);
         }
+        // P at the columns of one parity: of the even channels, then of the odd
+        uint32_t pb[kTerms][2][NP][2];  // [term][half of the tokens][column tile][token 2c, 2c + 1]
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint32_t af[2][4] = {{h[0][2 * q], h[0][2 * q + 1], h[1][2 * q], h[1][2 * q + 1]},
-                                     {h[2][2 * q], h[2][2 * q + 1], h[3][2 * q], h[3][2 * q + 1]}};
+        for (int term = 0; term < kTerms; ++term)
 #pragma unroll
-          for (int np = 0; np < NP; ++np) {
-            float(&acc)[4] = o[2 * w + q][np];
-            if constexpr (kTerms == 1) {
-              mma(acc, af[0], pb[0][0][np][0], pb[0][0][np][1]);
-              mma(acc, af[1], pb[0][1][np][0], pb[0][1][np][1]);
-            } else {
-              float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          for (int half = 0; half < 2; ++half)
 #pragma unroll
-              for (int term = kTerms - 1; term >= 0; --term) {
-                mma(d, af[0], pb[term][0][np][0], pb[term][0][np][1]);
-                mma(d, af[1], pb[term][1][np][0], pb[term][1][np][1]);
+            for (int np = 0; np < NP; ++np) {
+              const uint32_t w = pf[term][kBoth ? 0 : np / 2][half];
+              const bool odd = kBoth ? g >= 4 : np & 1;
+              pb[term][half][np][0] = __byte_perm(w, 0, odd ? 0x1044 : 0x4410);
+              pb[term][half][np][1] = __byte_perm(w, 0, odd ? 0x3244 : 0x4432);
+            }
+#pragma unroll
+        for (int w = 0; w < D / 64; ++w) {  // 8 channels: two m tiles
+          uint32_t h[4][4];
+          const int sc = D == 256 ? w / 2 : 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            e2m1_to_f16(cur.v[i].w[w], h[i]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) h[i][q] = hmul2(h[i][q], vs[i][sc]);
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t af[2][4] = {
+                {h[0][2 * q], h[0][2 * q + 1], h[1][2 * q], h[1][2 * q + 1]},
+                {h[2][2 * q], h[2][2 * q + 1], h[3][2 * q], h[3][2 * q + 1]}};
+#pragma unroll
+            for (int np = 0; np < NP; ++np) {
+              float(&acc)[4] = o[2 * w + q][np];
+              if constexpr (kTerms == 1) {
+                mma(acc, af[0], pb[0][0][np][0], pb[0][0][np][1]);
+                mma(acc, af[1], pb[0][1][np][0], pb[0][1][np][1]);
+              } else {
+                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int term = kTerms - 1; term >= 0; --term) {
+                  mma(d, af[0], pb[term][0][np][0], pb[term][0][np][1]);
+                  mma(d, af[1], pb[term][1][np][0], pb[term][1][np][1]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[j] += d[j];
               }
-#pragma unroll
-              for (int j = 0; j < 4; ++j) acc[j] += d[j];
             }
           }
         }
@@ -708,7 +760,7 @@ cudaError_t launch_split_as(const AttnArgs& a, void* ws, const AttnLayout& L, cu
   e = opt_in_smem(reinterpret_cast<const void*>(kern), smem, done);
   if (e != cudaSuccess) return e;
   int log2 = 0;
-  while ((kTile << log2) < a.page_size) ++log2;
+  while ((1 << log2) < a.page_size) ++log2;
   return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, a, status, counters,
                     const_cast<const SeqInfo*>(info), const_cast<const long*>(starts),
                     reinterpret_cast<float*>(w + L.stats), reinterpret_cast<float*>(w + L.partial),
