@@ -36,12 +36,13 @@ constexpr int kSub = 16;    // cached tokens per matrix instruction, never acros
 constexpr int kTile = 32;   // cached tokens per tile: what a warp takes at a time
 constexpr int kWarps = 4;   // per CTA; each takes every fourth tile of a segment
 constexpr int kThreads = kWarps * 32;
-constexpr int kMinTiles = kWarps;  // smallest range of a CTA
+constexpr int kMinTiles = 2;  // smallest range of a CTA
 // A segment's set-up (its queries, the join of the warps, its rows' stores)
 // takes a CTA as long as this many tiles; the list counts them.
-constexpr int kSetup = 7;
+constexpr int kSetup = 9;
 constexpr int kStages = 2;  // tiles a warp has in shared memory or on the way
 constexpr int kMaxCtasPerSm = 4;
+constexpr int kJoin = 16;  // pieces whose sums the joining CTA loads together
 constexpr int kPlanThreads = 1024;
 constexpr int kInlineSeqs = 256;  // up to so many requests are planned by every CTA
 
@@ -198,7 +199,8 @@ __host__ __device__ constexpr int split_smem() {
 }
 template <int D, int kRows, int kTerms>
 __host__ __device__ constexpr int ctas_per_sm() {
-  return D == 256 || kRows == 16 || kTerms == 2 ? 2 : kMaxCtasPerSm;
+  if (D == 256) return 2;
+  return kRows == 16 || (kTerms == 2 && D == 128) ? 2 : kTerms == 2 ? 3 : kMaxCtasPerSm;
 }
 
 // kRows is 4, 8 or 16. The matrix instruction pairs neighbouring k indices in
@@ -718,12 +720,20 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
           if (row0 + r >= rows) continue;
           float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           const float* src = partial + (2l * cta0 * kRows + r) * D + ch;
-#pragma unroll 16
-          for (int k = 0; k < n; ++k) {
-            const long slot = 2l * k + (k == 0);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + slot * kRows * D));
-            const float f = w[r * n + k];
-            sum.x += f * v.x, sum.y += f * v.y, sum.z += f * v.z, sum.w += f * v.w;
+          for (int k0 = 0; k0 < n; k0 += kJoin) {  // kJoin pieces on the way at a time
+            float4 v[kJoin];
+#pragma unroll
+            for (int j = 0; j < kJoin; ++j) {
+              const int k = k0 + j;
+              v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (k < n)
+                v[j] = __ldcg(reinterpret_cast<const float4*>(src + (2l * k + (k == 0)) * kRows * D));
+            }
+#pragma unroll
+            for (int j = 0; j < kJoin; ++j) {
+              const float f = k0 + j < n ? w[r * n + k0 + j] : 0.0f;
+              sum.x += f * v[j].x, sum.y += f * v[j].y, sum.z += f * v[j].z, sum.w += f * v[j].w;
+            }
           }
           const int tok = (row0 + r) / group, h = kvh * group + (row0 + r) - tok * group;
           const long at_row = static_cast<long>(sq.q0 + tok) * a.heads + h;
