@@ -302,71 +302,6 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
       all_first = a.window > 0 ? max(0, pos1 - a.window + 1) : 0;
     }
 
-    // q^T as the B operand: column g (+ 8 nt), channels c*D/4 ..
-    uint32_t qf[kTerms][NT][D / 8];
-    float q_gain[NT];  // 2^-x of the row g (+ 8 nt) this lane loads
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = row0 + nt * 8 + (kBoth ? g & 3 : g);
-      float x[D / 4];
-      if (r < rows) {
-        const int tok = r / group, h = kvh * group + (r - tok * group);
-        const T* src = static_cast<const T*>(a.q.p) + (sq.q0 + tok) * a.q.token + h * a.q.head +
-                       c * (D / 4);
-        if constexpr (sizeof(T) == 2) {
-          const Words<D / 8> w = load_words<D / 8>(reinterpret_cast<const uint8_t*>(src));
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            x[2 * i] = __uint_as_float(w.w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w.w[i] & 0xffff0000u);
-          }
-        } else {
-          const Words<D / 4> w = load_words<D / 4>(reinterpret_cast<const uint8_t*>(src));
-#pragma unroll
-          for (int i = 0; i < D / 4; ++i) x[i] = __uint_as_float(w.w[i]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < D / 4; ++i) x[i] = 0.0f;
-      }
-      float top = 0.0f;
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
-      top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-      float up;
-      row_power(top, up, q_gain[nt]);
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const float lo = x[2 * i] * up, hi = x[2 * i + 1] * up;
-        qf[0][nt][i] = pack_f16(lo, hi);
-        if constexpr (kTerms == 2) {
-          const float2 f = unpack_f16(qf[0][nt][i]);
-          qf[1][nt][i] = pack_f16(lo - f.x, hi - f.y);
-        }
-      }
-    }
-    // the gains of this lane's score columns, with the softmax scale
-    float gain[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        gain[nt][j] = __shfl_sync(~0u, q_gain[nt], (2 * c + j) * 4) * a.scale_log2;
-
-    float o[D / 32][NP][4];
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-      for (int np = 0; np < NP; ++np)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][np][j] = 0.0f;
-    float m[NT][2], base[NT][2], l[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) m[nt][j] = -INFINITY, base[nt][j] = -kLift, l[nt][j] = 0.0f;
-
     // tiles of this row tile that hold a visible token
     const int tA = max(t0, tile_first / kTile - first_tile);
     const int tB = min(t1, tile_last < 0 ? 0 : tile_last / kTile + 1 - first_tile);
@@ -406,21 +341,90 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     int t = tA + warp;
-    {
-      int2 ids[kStages - 1];
+    int2 ids[kStages - 1];
 #pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) ids[i] = pages_of(t + i * kWarps);
-      if (!entered) {
-        // status and counters are clear from here on; everything else that is
-        // read was written before the kernel that clears them
-        pdl_enter();
-        if (blockIdx.x == 0 && flags) atomicOr(status, flags);
-        entered = true;
+    for (int i = 0; i < kStages - 1; ++i) ids[i] = pages_of(t + i * kWarps);
+    // The queries' rows (padding rows are zero) are on the way while the first
+    // tiles are asked for.
+    constexpr int kQWords = D / 4 * static_cast<int>(sizeof(T)) / 4;
+    Words<kQWords> raw[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = row0 + nt * 8 + (kBoth ? g & 3 : g);
+      if (r < rows) {
+        const int tok = r / group, h = kvh * group + (r - tok * group);
+        raw[nt] = load_words<kQWords>(reinterpret_cast<const uint8_t*>(
+            static_cast<const T*>(a.q.p) + (sq.q0 + tok) * a.q.token + h * a.q.head + c * (D / 4)));
+      } else {
+#pragma unroll
+        for (int i = 0; i < kQWords; ++i) raw[nt].w[i] = 0;
       }
-#pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) copy(t + i * kWarps, i, ids[i]);
     }
+    if (!entered) {
+      // status and counters are clear from here on; everything else that is
+      // read was written before the kernel that clears them
+      pdl_enter();
+      if (blockIdx.x == 0 && flags) atomicOr(status, flags);
+      entered = true;
+    }
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) copy(t + i * kWarps, i, ids[i]);
     int2 next_ids = pages_of(t + (kStages - 1) * kWarps);
+
+    // q^T as the B operand: column g (+ 8 nt), channels c*D/4 ..
+    uint32_t qf[kTerms][NT][D / 8];
+    float q_gain[NT];  // 2^-x of the row g (+ 8 nt) this lane loads
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float x[D / 4];
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          x[2 * i] = __uint_as_float(raw[nt].w[i] << 16);
+          x[2 * i + 1] = __uint_as_float(raw[nt].w[i] & 0xffff0000u);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) x[i] = __uint_as_float(raw[nt].w[i]);
+      }
+      float top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+      float up;
+      row_power(top, up, q_gain[nt]);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const float lo = x[2 * i] * up, hi = x[2 * i + 1] * up;
+        qf[0][nt][i] = pack_f16(lo, hi);
+        if constexpr (kTerms == 2) {
+          const float2 f = unpack_f16(qf[0][nt][i]);
+          qf[1][nt][i] = pack_f16(lo - f.x, hi - f.y);
+        }
+      }
+    }
+    // the gains of this lane's score columns, with the softmax scale
+    float gain[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        gain[nt][j] = __shfl_sync(~0u, q_gain[nt], (2 * c + j) * 4) * a.scale_log2;
+
+    float o[D / 32][NP][4];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int np = 0; np < NP; ++np)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][np][j] = 0.0f;
+    float m[NT][2], base[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) m[nt][j] = -INFINITY, base[nt][j] = -kLift, l[nt][j] = 0.0f;
+
     for (int stage = 0; t < tB; t += kWarps, stage = stage + 1 == kStages ? 0 : stage + 1) {
       __syncwarp();  // every lane has read the stage that is copied to next
       copy(t + (kStages - 1) * kWarps, stage == 0 ? kStages - 1 : stage - 1, next_ids);
