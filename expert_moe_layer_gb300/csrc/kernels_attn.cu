@@ -229,12 +229,16 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
   __shared__ int s_last;
   const SeqInfo* info = info_in;
   const long* starts = starts_in;
+  // The kernel before this one only clears status and counters, which are not
+  // touched before the first segment's join: everything else that is read was
+  // written before that kernel began, and the wait for it comes that late.
   bool entered = !kInline;
   unsigned flags = 0;
   if constexpr (kInline) {
     __shared__ SeqInfo s_info[kInlineSeqs];
     __shared__ long s_starts[kInlineSeqs + 1];
     flags = sum_work<kThreads>(a, kRows, s_info, s_starts);
+    if (blockIdx.x != 0) flags = 0;  // one CTA reports the requests
     __syncthreads();
     info = s_info;
     starts = s_starts;
@@ -261,23 +265,29 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
     }
     b = lo;
   }
+  // the segment of the first tile; later segments follow by counting
+  long seg_start = -1;
+  int row_tile = 0, kvh = 0;
   while (at < end) {
-    while (starts[b + 1] <= at) ++b;
     const SeqInfo sq = info[b];
     const int first_tile = sq.first_key / kTile;
     const int rows = sq.q_len * group;
     const int per_seg = kSetup + max(0, (sq.len + kTile - 1) / kTile - first_tile);
-    const long seg = (at - starts[b]) / per_seg;
-    const long seg_start = starts[b] + seg * per_seg, seg_end = seg_start + per_seg;
+    if (seg_start < 0) {
+      const long seg = (at - starts[b]) / per_seg;
+      seg_start = starts[b] + seg * per_seg;
+      row_tile = static_cast<int>(seg / a.kv_heads);
+      kvh = static_cast<int>(seg - static_cast<long>(row_tile) * a.kv_heads);
+    }
+    const long seg_end = seg_start + per_seg;
     if (at - seg_start < kSetup) at = seg_start;
     if (end - seg_start < kSetup) break;  // a later CTA takes all of it
     // this CTA's part [p0, p1) of the segment's list, and of its tiles
     const int p0 = static_cast<int>(at - seg_start);
     const int p1 = static_cast<int>(min(seg_end, end) - seg_start);
     const int t0 = max(0, p0 - kSetup), t1 = p1 - kSetup;
-    const int row_tile = static_cast<int>(seg / a.kv_heads);
-    const int kvh = static_cast<int>(seg - static_cast<long>(row_tile) * a.kv_heads);
     const int row0 = row_tile * kRows;
+    auto token_of = [&](int r) { return sq.q_len == 1 ? 0 : r / group; };
 
     // this lane's score columns are rows nt*8 + 2c and + 1: their token limits
     int last[NT][2], first[NT][2];
@@ -288,13 +298,13 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
       for (int j = 0; j < 2; ++j) {
         const int r = row0 + nt * 8 + (kBoth ? (2 * c + j) & 3 : 2 * c + j);
         // padding rows (zero queries whose columns are never written) see all
-        const int p = sq.len - sq.q_len + r / group;
+        const int p = sq.len - sq.q_len + token_of(r);
         last[nt][j] = r < rows ? p : 0x7fffffff;
         first[nt][j] = r < rows && a.window > 0 ? max(0, p - a.window + 1) : 0;
       }
     {
       const int r_end = min(rows, row0 + kRows) - 1;
-      const int pos0 = sq.len - sq.q_len + row0 / group, pos1 = sq.len - sq.q_len + r_end / group;
+      const int pos0 = sq.len - sq.q_len + token_of(row0), pos1 = sq.len - sq.q_len + token_of(r_end);
       tile_last = pos1;
       tile_first = a.window > 0 ? max(0, pos0 - a.window + 1) : 0;
       // tokens that every row of the tile sees
@@ -330,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
         for (int sub = 0; sub < kSubs; ++sub) {
           const int id = sub ? ids.y : ids.x;
           const bool ok = id >= 0 && id < a.num_pages;
-          if (!ok && lane == 0) atomicOr(status, MOE_DEV_BAD_PAGE);
+          if (!ok) flags |= MOE_DEV_BAD_PAGE;
           const uint32_t bit = 1u << (stage * kSubs + sub);
           ok_bits = ok ? ok_bits | bit : ok_bits & ~bit;
           copy_tile<D>(ring_addr + stage * TileBytes<D>::kTileBytes + sub * TileBytes<D>::kBytes,
@@ -352,20 +362,13 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
     for (int nt = 0; nt < NT; ++nt) {
       const int r = row0 + nt * 8 + (kBoth ? g & 3 : g);
       if (r < rows) {
-        const int tok = r / group, h = kvh * group + (r - tok * group);
+        const int tok = token_of(r), h = kvh * group + (r - tok * group);
         raw[nt] = load_words<kQWords>(reinterpret_cast<const uint8_t*>(
             static_cast<const T*>(a.q.p) + (sq.q0 + tok) * a.q.token + h * a.q.head + c * (D / 4)));
       } else {
 #pragma unroll
         for (int i = 0; i < kQWords; ++i) raw[nt].w[i] = 0;
       }
-    }
-    if (!entered) {
-      // status and counters are clear from here on; everything else that is
-      // read was written before the kernel that clears them
-      pdl_enter();
-      if (blockIdx.x == 0 && flags) atomicOr(status, flags);
-      entered = true;
     }
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) copy(t + i * kWarps, i, ids[i]);
@@ -617,6 +620,8 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
     // join the warps: sums [row][channel] and statistics (base, l) in shared
     // memory, in the place of the stages
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!entered) pdl_enter();
+    entered = true;
     __syncthreads();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -665,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
       }
       if (alone) {
         if (row0 + r < rows) {
-          const int tok = (row0 + r) / group, h = kvh * group + (row0 + r) - tok * group;
+          const int tok = token_of(row0 + r), h = kvh * group + (row0 + r) - tok * group;
           const long at_row = static_cast<long>(sq.q0 + tok) * a.heads + h;
           const float f = out_factor(den, a.v_scale);
           store4(static_cast<T*>(a.out) + at_row * D + ch,
@@ -739,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
               sum.x += f * v[j].x, sum.y += f * v[j].y, sum.z += f * v[j].z, sum.w += f * v[j].w;
             }
           }
-          const int tok = (row0 + r) / group, h = kvh * group + (row0 + r) - tok * group;
+          const int tok = token_of(row0 + r), h = kvh * group + (row0 + r) - tok * group;
           const long at_row = static_cast<long>(sq.q0 + tok) * a.heads + h;
           const float f = out_factor(s_stat[2 * r + 1], a.v_scale);
           store4(static_cast<T*>(a.out) + at_row * D + ch,
@@ -750,11 +755,17 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
     }
     __syncthreads();
     at = seg_start + p1;
+    if (p1 == per_seg) {
+      seg_start = at;
+      if (++kvh == a.kv_heads) kvh = 0, ++row_tile;
+      if (at < end && at == starts[b + 1]) {
+        while (starts[b + 1] <= at) ++b;
+        row_tile = kvh = 0;
+      }
+    }
   }
-  if (!entered) {
-    pdl_enter();
-    if (blockIdx.x == 0 && flags) atomicOr(status, flags);
-  }
+  if (!entered) pdl_enter();
+  if (flags) atomicOr(status, flags);
 }
 
 template <typename T, int D, int kRows, int kTerms, bool kInline>
