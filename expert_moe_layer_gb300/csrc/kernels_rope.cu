@@ -8,7 +8,7 @@
 // per lane and chunk, 4097 x 16 heads of 256 in fp32 took 34.4 us instead of
 // 27.4). The rows are loaded before the position and the table row, which have
 // to be fetched one after the other (23.0 us then: 6.0 TB/s, 89 % of a copy's
-// rate; bf16, 8192 x 40 heads of 128 half rotated: 34.5 us, 4.9 TB/s). The
+// rate; bf16, 8192 x 40 heads of 128 half rotated: 29.8 us, 5.7 TB/s). The
 // cosines and sines serve several heads; a row rotated in place is read and
 // written by one thread only.
 #include <cuda_bf16.h>
@@ -22,6 +22,10 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+// CTAs per SM of the kernels of one and of four heads per thread. Three of the
+// latter spill 10 registers and are still faster (29.8 us, the case below) than
+// two without (34.0) or four (34.3); the former need the registers of five.
+constexpr int ctas_per_sm(int heads) { return heads == 1 ? 5 : 3; }
 
 template <typename T>
 __device__ __forceinline__ float to_f(T v);
@@ -167,8 +171,8 @@ __device__ __forceinline__ long slot_of(const RopeArgs& a, int t) {
 
 // D and R multiples of 32, 16-byte aligned rows.
 template <typename T, bool kInterleaved, int kHeads>
-__global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int cq, int ck,
-                                                        unsigned total) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(kHeads))
+    rope_kernel(RopeArgs a, int cq, int ck, unsigned total) {
   constexpr int V = 16 / sizeof(T);     // elements of a chunk
   constexpr int kSharers = kKvGroup / V;  // lanes that share a scale
   pdl_enter();
@@ -482,15 +486,19 @@ cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t st) {
                       (a.kv_heads == 0 || (rows_aligned(a.k, eb) && rows_aligned(a.v, eb)));
   const bool fast = rows16 && a.D % 32 == 0 && a.R % 32 == 0 &&
                     reinterpret_cast<uintptr_t>(a.table) % 16 == 0;
-  // (8192 tokens, 40 heads of 128 in bf16: 34.5 us fast; wide 58.8 us for 66 of the
+  // (8192 tokens, 40 heads of 128 in bf16: 29.8 us fast; wide 58.8 us for 66 of the
   // channels in halves and 39.3 us for 98 interleaved; one element at a time
   // 124 and 131 us)
   const int lanes = a.D / (16 / eb);
   const bool wide = rows16 && !fast && (a.q.p != a.q_out || 32 % lanes == 0);
   const long units = fast ? lanes / 2 : wide ? lanes : (a.D + 15) / 16;
-  // heads per thread: 4 once that still gives every SM its 2048 threads
+  // Heads per thread, one or four: a table row serves all of them. Queries alone
+  // (32 heads of 128 in bf16): 256 tokens 2.2 us with one and 2.6 with four, 512
+  // tokens 2.8 and 2.7, 4096 tokens 18.3 and 14.4. Keys and values are quantised
+  // one head after the other (8 of each beside them): 64 tokens 4.9 and 7.1 us,
+  // 1024 tokens 10.0 and 11.1, 2048 tokens 17.7 and 15.5.
   const long all = units * a.T * (a.q_heads + 2l * a.kv_heads);
-  const int hb = all / 4 >= 152l * 2048 ? 4 : 1;
+  const int hb = all / 4 >= 152l * (a.kv_heads ? 1024 : 192) ? 4 : 1;
   const int cq = (a.q_heads + hb - 1) / hb, ck = (a.kv_heads + hb - 1) / hb;
   const long total = units * a.T * (cq + 2l * ck);
   if (total == 0) return cudaSuccess;
