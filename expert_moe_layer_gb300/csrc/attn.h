@@ -84,7 +84,8 @@ struct SeqInfo {
 };
 
 // Rows of a row tile of the prompt kernel (query tokens times heads of a
-// group), and the rows per request it is used from.
+// group), and the rows per request it is used from (uses_prompt_kernel has the
+// times of both sides).
 constexpr int prompt_tile(int head_dim) { return head_dim == 256 ? 128 : 256; }
 constexpr int kPromptRows = 64;
 cudaError_t launch_prompt(const AttnArgs& a, void* ws, const AttnLayout& L, cudaStream_t st);
