@@ -667,6 +667,15 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
       }
     __syncthreads();
     const bool alone = p0 == 0 && p1 == per_seg;
+    // four channels of a row: the sum of its P V, its base and its sum of P
+    auto finish = [&](int r, int ch, float4 sum, float top, float den) {
+      const int tok = token_of(row0 + r), h = kvh * group + (row0 + r) - tok * group;
+      const long at_row = static_cast<long>(sq.q0 + tok) * a.heads + h;
+      const float f = out_factor(den, a.v_scale);
+      store4(static_cast<T*>(a.out) + at_row * D + ch,
+             make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f));
+      if (a.lse && ch == 0) a.lse[at_row] = log_sum(top, den);
+    };
     // pieces of a segment: the CTA it begins in keeps its piece in slot 1 (its
     // range ends inside the segment), later ones in slot 0
     const long my_slot = 2l * blockIdx.x + (p0 == 0 ? 1 : 0);
@@ -686,14 +695,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
         sum.x += f * v.x, sum.y += f * v.y, sum.z += f * v.z, sum.w += f * v.w;
       }
       if (alone) {
-        if (row0 + r < rows) {
-          const int tok = token_of(row0 + r), h = kvh * group + (row0 + r) - tok * group;
-          const long at_row = static_cast<long>(sq.q0 + tok) * a.heads + h;
-          const float f = out_factor(den, a.v_scale);
-          store4(static_cast<T*>(a.out) + at_row * D + ch,
-                 make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f));
-          if (a.lse && ch == 0) a.lse[at_row] = log_sum(top, den);
-        }
+        if (row0 + r < rows) finish(r, ch, sum, top, den);
       } else {
         *reinterpret_cast<float4*>(partial + (my_slot * kRows + r) * D + ch) = sum;
         if (ch == 0) {
@@ -712,61 +714,88 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
       __syncthreads();
       if (s_last) {
         __threadfence();
-        // every piece's statistics into shared memory, then its weight
         const int n = cta1 - cta0 + 1;
-        float* w = smem;                 // [kRows][n] bases, then weights
-        float* dens = smem + kRows * n;  // [kRows][n]
-        for (int i = threadIdx.x; i < kRows * n; i += kThreads) {
-          const int r = i / n, k = i - r * n;
-          const long slot = (2l * (cta0 + k) + (k == 0)) * kRows + r;
-          const float2 st = __ldcg(reinterpret_cast<const float2*>(stats + slot * 2));
-          w[i] = st.x;
-          dens[i] = st.y;
-        }
-        __syncthreads();
-        for (int r = warp; r < kRows; r += kWarps) {
-          float top = -INFINITY, den = 0.0f;
-          for (int k = lane; k < n; k += 32) top = fmaxf(top, w[r * n + k]);
-#pragma unroll
-          for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-          for (int k = lane; k < n; k += 32) {
-            const float b2 = w[r * n + k];
-            const float f = b2 == -INFINITY ? 0.0f : ex2(b2 - top);
-            w[r * n + k] = f;
-            den += f * dens[r * n + k];
-          }
-#pragma unroll
-          for (int d = 16; d > 0; d /= 2) den += __shfl_xor_sync(~0u, den, d);
-          __syncwarp();
-          if (lane == 0) s_stat[2 * r] = top, s_stat[2 * r + 1] = den;
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
-          const int r = i / (D / 4), ch = (i % (D / 4)) * 4;
-          if (row0 + r >= rows) continue;
-          float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          const float* src = partial + (2l * cta0 * kRows + r) * D + ch;
-          for (int k0 = 0; k0 < n; k0 += kJoin) {  // kJoin pieces on the way at a time
+        const float* first_sum = partial + 2l * cta0 * kRows * D;
+        const float* first_stat = stats + 4l * cta0 * kRows;
+        auto slot_of = [](int k) { return (2l * k + (k == 0)) * kRows; };
+        if (n <= kJoin) {  // statistics and sums are fetched together
+          for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
+            const int r = i / (D / 4), ch = (i % (D / 4)) * 4;
+            if (row0 + r >= rows) continue;
+            float2 st[kJoin];
             float4 v[kJoin];
 #pragma unroll
-            for (int j = 0; j < kJoin; ++j) {
-              const int k = k0 + j;
-              v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              if (k < n)
-                v[j] = __ldcg(reinterpret_cast<const float4*>(src + (2l * k + (k == 0)) * kRows * D));
+            for (int k = 0; k < kJoin; ++k) {
+              st[k] = make_float2(-INFINITY, 0.0f);
+              v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (k < n) {
+                st[k] = __ldcg(reinterpret_cast<const float2*>(first_stat + (slot_of(k) + r) * 2));
+                v[k] = __ldcg(reinterpret_cast<const float4*>(first_sum + (slot_of(k) + r) * D + ch));
+              }
+            }
+            float top = -INFINITY, den = 0.0f;
+            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < kJoin; ++k) top = fmaxf(top, st[k].x);
+#pragma unroll
+            for (int k = 0; k < kJoin; ++k) {
+              const float f = st[k].x == -INFINITY ? 0.0f : ex2(st[k].x - top);
+              den += f * st[k].y;
+              sum.x += f * v[k].x, sum.y += f * v[k].y, sum.z += f * v[k].z, sum.w += f * v[k].w;
+            }
+            finish(r, ch, sum, top, den);
+          }
+        } else {
+          // every piece's statistics into shared memory, then its weight
+          float* w = smem;                 // [kRows][n] bases, then weights
+          float* dens = smem + kRows * n;  // [kRows][n]
+          for (int i = threadIdx.x; i < kRows * n; i += kThreads) {
+            const int r = i / n, k = i - r * n;
+            const float2 st =
+                __ldcg(reinterpret_cast<const float2*>(first_stat + (slot_of(k) + r) * 2));
+            w[i] = st.x;
+            dens[i] = st.y;
+          }
+          __syncthreads();
+          for (int r = warp; r < kRows; r += kWarps) {
+            float top = -INFINITY, den = 0.0f;
+            for (int k = lane; k < n; k += 32) top = fmaxf(top, w[r * n + k]);
+#pragma unroll
+            for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+            for (int k = lane; k < n; k += 32) {
+              const float b2 = w[r * n + k];
+              const float f = b2 == -INFINITY ? 0.0f : ex2(b2 - top);
+              w[r * n + k] = f;
+              den += f * dens[r * n + k];
             }
 #pragma unroll
-            for (int j = 0; j < kJoin; ++j) {
-              const float f = k0 + j < n ? w[r * n + k0 + j] : 0.0f;
-              sum.x += f * v[j].x, sum.y += f * v[j].y, sum.z += f * v[j].z, sum.w += f * v[j].w;
-            }
+            for (int d = 16; d > 0; d /= 2) den += __shfl_xor_sync(~0u, den, d);
+            __syncwarp();
+            if (lane == 0) s_stat[2 * r] = top, s_stat[2 * r + 1] = den;
           }
-          const int tok = token_of(row0 + r), h = kvh * group + (row0 + r) - tok * group;
-          const long at_row = static_cast<long>(sq.q0 + tok) * a.heads + h;
-          const float f = out_factor(s_stat[2 * r + 1], a.v_scale);
-          store4(static_cast<T*>(a.out) + at_row * D + ch,
-                 make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f));
-          if (a.lse && ch == 0) a.lse[at_row] = log_sum(s_stat[2 * r], s_stat[2 * r + 1]);
+          __syncthreads();
+          for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
+            const int r = i / (D / 4), ch = (i % (D / 4)) * 4;
+            if (row0 + r >= rows) continue;
+            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int k0 = 0; k0 < n; k0 += kJoin) {  // kJoin pieces on the way at a time
+              float4 v[kJoin];
+#pragma unroll
+              for (int j = 0; j < kJoin; ++j) {
+                const int k = k0 + j;
+                v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (k < n)
+                  v[j] = __ldcg(
+                      reinterpret_cast<const float4*>(first_sum + (slot_of(k) + r) * D + ch));
+              }
+#pragma unroll
+              for (int j = 0; j < kJoin; ++j) {
+                const float f = k0 + j < n ? w[r * n + k0 + j] : 0.0f;
+                sum.x += f * v[j].x, sum.y += f * v[j].y, sum.z += f * v[j].z, sum.w += f * v[j].w;
+              }
+            }
+            finish(r, ch, sum, s_stat[2 * r], s_stat[2 * r + 1]);
+          }
         }
       }
     }
