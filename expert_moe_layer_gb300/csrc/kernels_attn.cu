@@ -19,8 +19,8 @@
 // that enough bytes are on the way without registers and without barriers.
 //
 // Measured (bf16, 32 query and 8 kv heads of 128): 8 requests of 131071 tokens
-// 227 us, 5.3 TB/s of codes (79 % of a copy's rate); 64 requests of 1 to 16384
-// tokens 39 us; one request of 1000 tokens (16 and 2 heads) 10 us, a chain of
+// 226 us, 5.3 TB/s of codes (79 % of a copy's rate); 64 requests of 1 to 16384
+// tokens 38 us; one request of 1000 tokens (16 and 2 heads) 8.5 us, a chain of
 // dependent loads. Instruction issue is the bound: 331 warp instructions per 16
 // tokens, 65 % of the issue slots while an SM is busy, the half-rate pipe that
 // converts codes at 56 %. One vote and one set of copies per 32 tokens instead
@@ -44,17 +44,18 @@ constexpr int kSub = 16;    // cached tokens per matrix instruction, never acros
 constexpr int kTile = 32;   // cached tokens per tile: what a warp takes at a time
 constexpr int kWarps = 4;   // per CTA; each takes every fourth tile of a segment
 constexpr int kThreads = kWarps * 32;
-// Smallest range of a CTA: one request of 1000 tokens takes 10.6 us with two
-// tiles, 12.2 with one and 12.7 with four; long lists do not notice.
-constexpr int kMinTiles = 2;
+// Smallest range of a CTA: a tile for each warp. One request of 1000 tokens takes
+// 9.9 us with two tiles, 8.5 with four and 8.8 with eight, one of 4096 tokens
+// 13.2, 10.7 and 10.3, one of 300 tokens 7.4, 7.2 and 7.9; long lists do not notice.
+constexpr int kMinTiles = kWarps;
 // A segment's set-up (its queries, the join of the warps, its rows' stores)
 // takes a CTA as long as this many tiles; the list counts them. (64 requests
 // of 1 to 16384 tokens: 47.4 us with 5, 43.7 with 7, 41.2 with 9.)
 constexpr int kSetup = 9;
 constexpr int kStages = 2;  // tiles a warp has in shared memory or on the way
 constexpr int kMaxCtasPerSm = 4;
-constexpr int kJoin = 16;  // pieces whose sums the joining CTA loads together (one by
-                           // one: 68 us instead of 61 with ten pieces of 16 rows)
+constexpr int kJoin = 16;  // pieces whose sums the joining CTA loads together (ten pieces
+                           // of 16 rows: 57 us; one by one, after their statistics, 68)
 constexpr int kPlanThreads = 1024;
 // Up to so many requests are planned by every CTA itself, more by the kernel
 // before: 17.3 against 20.4 us (21 requests), 40.9 and 42.7 (64), 35.7 and 37.2
