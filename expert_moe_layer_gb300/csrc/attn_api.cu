@@ -309,7 +309,11 @@ int moe_kv_attention(const moe_attn_config* cfg, int num_seqs, int T, int max_q_
   if (a.sms > kAttnMaxSms) a.sms = kAttnMaxSms;
   a.B = num_seqs, a.T = T, a.max_q = max_q_len;
   a.heads = cfg->num_heads, a.kv_heads = cfg->num_kv_heads;
-  a.D = cfg->head_dim, a.page_size = cfg->page_size, a.window = cfg->window;
+  a.D = cfg->head_dim, a.page_size = cfg->page_size;
+  // A request has at most a table row's tokens, so that a window of as many is no
+  // limit. Positions lie between -2^18 and 2^28 and so do the windows left: a
+  // position less a window stays within 32 bits in the kernels.
+  a.window = cfg->window < int64_t{max_pages} * cfg->page_size ? cfg->window : 0;
   const float scale =
       cfg->softmax_scale > 0.0f ? cfg->softmax_scale
                                 : 1.0f / std::sqrt(static_cast<float>(cfg->head_dim));
