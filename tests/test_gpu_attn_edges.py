@@ -39,3 +39,62 @@ def test_windows_as_wide_as_any_number(i, window):
     c.window = c.cfg.window = 0                         # no request has as many tokens
     c.run()
     assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+
+
+# --------------------------------------------------------- scores of fp32 layers
+def _one_key(D, heads, q):
+    """fp32 queries [heads, D] of one kv head over a single cached key whose
+    channels are all 6: the denominator is 1 and lse is the score itself."""
+    cfg = B.make_attn_config(heads, 1, D, 16, "f32")
+    k = torch.full((1, 1, D), 6.0, device="cuda")
+    cache = torch.zeros(1, 1, 16 * D * 9 // 8, dtype=torch.uint8, device="cuda")
+    B.moe_kv_append(cfg, 1, None, k, k, None, torch.zeros(1, dtype=torch.int64, device="cuda"), None,
+                    None, cache)
+    out, lse = torch.empty(1, heads, D, device="cuda"), torch.empty(1, heads, device="cuda")
+    ws = torch.empty(B.kv_attention_workspace_size(cfg, 1, 1, 1), dtype=torch.uint8, device="cuda")
+    B.moe_kv_attention(cfg, 1, 1, 1, q[None].cuda(), None, torch.ones(1, dtype=torch.int32, device="cuda"),
+                       torch.zeros(1, 1, dtype=torch.int32, device="cuda"), cache, out, lse, ws)
+    assert B.moe_get_status(ws) == (0, 0)
+    # the weight is p over itself: p as two f16, the exponential and the sums (test_gpu_attn's terms)
+    assert ((out.double() - 6).abs() <= 6 * (2.0 ** -24 + 2.0 ** -21 + 32 * 2.0 ** -23 + 2.0 ** -21)).all()
+    score = 6.0 * q.double().sum(1) * D ** -0.5
+    reach = 6.0 * q.double().abs().sum(1) * D ** -0.5
+    return lse[0].double().cpu(), score, reach
+
+
+def _score_bound(D, score, reach):
+    """Of the score, relative to the sum of |q k|, in units of 2^-23: the queries
+    are held in 22 bits (2); 32 channels at a time go through the matrix unit, the
+    high terms in two steps that lose up to 2 each, the low terms 2^-11 of that
+    (4.5); D/32 - 1 fp32 additions (half of that). Of lse: the gain, the maximum,
+    the base, the logarithm's sum and the factor to natural units round once each
+    (2.5, with the factor's own error 3), and the exponential and the logarithm add
+    2^-21."""
+    return 2.0 ** -23 * ((6.5 + (D / 32 - 1) / 2) * reach + 3 * score.abs()) + 2.0 ** -21
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("heads", [1, 4, 8])
+def test_f32_scores_do_not_lose_their_small_parts(D, heads):
+    """One channel carries the score; one channel of every other 16 adds a little
+    whose high and low halves both end just below a bit of the running sum."""
+    q = torch.zeros(heads, D, dtype=torch.float64)
+    ulp = 2.0 ** -13                          # of 6 * 172 in fp32
+    for h in range(heads):
+        small = (1025 + 2 * h) * 2.0 ** -15   # f16; 6 * small is half an ulp over whole ones
+        q[h, 4:D // 4:4] = small + 0.74 / 6 * ulp
+    q[:, 0] = 172.0
+    q = (q * 2.0 ** 3).float()                # scores of several hundred
+    got, score, reach = _one_key(D, heads, q)
+    assert ((got - score).abs() <= _score_bound(D, score, reach)).all(), \
+        ((got - score) / (2.0 ** -23 * reach)).tolist()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_f32_scores_of_large_queries(D):
+    gen = torch.Generator().manual_seed(D)
+    q = torch.randn(8, D, generator=gen).abs() * 100
+    q[4:] *= torch.randn(4, D, generator=gen).sign()
+    got, score, reach = _one_key(D, 8, q)
+    assert ((got - score).abs() <= _score_bound(D, score, reach)).all(), \
+        ((got - score) / (2.0 ** -23 * reach)).tolist()
