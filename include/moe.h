@@ -586,7 +586,7 @@ MOE_API int moe_rope(const moe_attn_config* cfg, int T, int num_heads, const voi
  *   slots [T] int64: where each token goes; -1 = nowhere (a padding token: its
  *   queries are still rotated). Two tokens must not share a slot.
  * A slot outside [-1, num_pages * page_size) sets MOE_DEV_BAD_SLOT and a bad
- * position MOE_DEV_BAD_POSITION; the token is then skipped. */
+ * position MOE_DEV_BAD_POSITION; the token is then skipped, its queries too. */
 MOE_API int moe_kv_append(const moe_attn_config* cfg, int T, const void* q,
                           int64_t q_token_stride, int64_t q_head_stride, const void* k,
                           int64_t k_token_stride, int64_t k_head_stride, const void* v,

@@ -98,3 +98,63 @@ def test_f32_scores_of_large_queries(D):
     got, score, reach = _one_key(D, 8, q)
     assert ((got - score).abs() <= _score_bound(D, score, reach)).all(), \
         ((got - score) / (2.0 ** -23 * reach)).tolist()
+
+
+# -------------------------------------------------------------------- append
+APPENDS = [  # dtype, T, heads, kv heads, D, R, elements before the rows: each rotation kernel, few and many tokens
+    ("bf16", 9, 4, 2, 128, 64, 0), ("bf16", 700, 24, 8, 128, 128, 0),
+    ("bf16", 9, 4, 2, 128, 66, 0), ("bf16", 700, 24, 8, 128, 34, 0),
+    ("bf16", 9, 4, 2, 64, 64, 1), ("f32", 11, 3, 1, 256, 256, 0), ("f32", 11, 3, 1, 64, 30, 0),
+]
+
+
+def _append_inputs(dtype, T, heads, kv, D, R, skew, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    cfg = B.make_attn_config(heads, kv, D, 16, dtype, R, "half", 50)
+    flat = torch.randn(skew + T * (heads + 2 * kv) * D, generator=gen, device="cuda").to(dt)
+    rows = flat[skew:].view(T, heads + 2 * kv, D)
+    table = torch.randn(50, R, generator=gen, device="cuda")
+    pos = torch.randint(0, 50, (T,), generator=gen, device="cuda", dtype=torch.int32)
+    pages = T // 16 + 2
+    slots = torch.randperm(pages * 16, generator=gen, device="cuda")[:T]
+    cache = torch.zeros(pages, kv, 16 * D * 9 // 8, dtype=torch.uint8, device="cuda")
+    return cfg, rows[:, :heads], rows[:, heads:heads + kv], rows[:, heads + kv:], pos, slots, table, cache
+
+
+@pytest.mark.parametrize("i", range(len(APPENDS)))
+def test_append_skips_the_queries_of_a_bad_slot(i):
+    """A slot of -1 takes a token's queries alone; one outside the cache nothing."""
+    cfg, q, k, v, pos, slots, table, cache = _append_inputs(*APPENDS[i], seed=i)
+    T = q.shape[0]
+    want = torch.empty(q.shape, dtype=q.dtype, device="cuda")
+    B.moe_rope(cfg, T, q, pos, table, want)
+    good = cache.clone()
+    B.moe_kv_append(cfg, T, None, k, v, pos, slots, table, None, good)
+    slots[1], slots[3], slots[T - 1], slots[5] = -2, cache.shape[0] * 16, 1 << 40, -1
+    out = torch.full_like(want, 5.0)
+    ws = torch.zeros(4, dtype=torch.uint8, device="cuda")
+    B.moe_kv_append(cfg, T, q, k, v, pos, slots, table, out, cache, ws)
+    assert B.moe_get_status(ws) == (5, B.DEV_BAD_SLOT)
+    bad = torch.zeros(T, dtype=torch.bool, device="cuda")
+    bad[[1, 3, T - 1]] = True
+    assert (out[bad] == 5).all()
+    assert torch.equal(out[~bad], want[~bad])
+    # the other tokens' keys and values, and nothing else
+    again = torch.zeros_like(cache)
+    keep = ~bad
+    keep[5] = False
+    n = int(keep.sum())
+    B.moe_kv_append(cfg, n, None, k[keep], v[keep], pos[keep], slots[keep], table, None, again)
+    assert torch.equal(cache, again) and not torch.equal(cache, good)
+
+
+@pytest.mark.parametrize("i", range(len(APPENDS)))
+def test_append_rotates_queries_in_place(i):
+    cfg, q, k, v, pos, slots, table, cache = _append_inputs(*APPENDS[i], seed=50 + i)
+    T = q.shape[0]
+    want = torch.empty(q.shape, dtype=q.dtype, device="cuda")
+    B.moe_kv_append(cfg, T, q, k, v, pos, slots, table, want, cache)
+    own, again = q.contiguous().clone(), torch.zeros_like(cache)
+    B.moe_kv_append(cfg, T, own, k, v, pos, slots, table, own, again)
+    assert torch.equal(own, want) and torch.equal(again, cache)
