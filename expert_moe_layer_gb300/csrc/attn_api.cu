@@ -120,9 +120,17 @@ int frequencies(int R, const moe_rope_scaling* s, double* f, double* gain) {
     auto pair = [&](double turns) {
       return R * std::log(s->original_positions / (turns * 2.0 * kPi)) / (2.0 * std::log(base));
     };
-    low = std::fmax(std::floor(pair(fast)), 0.0);
-    high = std::fmin(std::ceil(pair(slow)), R - 1.0);
-    if (low == high) high += 0.001;
+    low = std::floor(pair(fast));
+    high = std::ceil(pair(slow));
+    if (high < 0.0) {  // no pair turns as often as slow_turns: f / s for all
+      low = -1.0, high = 0.0;
+    } else if (low > R - 1.0) {  // every pair turns more often than fast_turns: f for all
+      high = low + 1.0;
+    } else {
+      low = std::fmax(low, 0.0);
+      high = std::fmin(high, R - 1.0);
+      if (low == high) high += 0.001;
+    }
   }
   for (int i = 0; i < R / 2; ++i) {
     const double own = std::pow(base, -2.0 * i / R);

@@ -527,7 +527,9 @@ typedef struct {
  *   YARN    (Peng et al., "YaRN", 2023) the same mix with a ramp over the pair
  *           index between the pairs d(fast_turns), rounded down, and
  *           d(slow_turns), rounded up, d(n) = R ln(original / (2pi n)) /
- *           (2 ln base); cosines and sines times attention_factor. */
+ *           (2 ln base), each cut to the R channels unless both lie on one side
+ *           of them (then f_i, or f_i / s, for all); cosines and sines times
+ *           attention_factor. */
 #define MOE_ROPE_SCALE_NONE 0
 #define MOE_ROPE_SCALE_LINEAR 1
 #define MOE_ROPE_SCALE_NTK 2

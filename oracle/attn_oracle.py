@@ -52,9 +52,16 @@ def frequencies(R, base, kind="none", factor=1.0, original=0.0, slow=0.0, fast=0
         keep = np.clip((turns - slow) / (fast - slow), 0, 1)
         f = f * keep + f / factor * (1 - keep)
     elif kind == "yarn":
-        lo = max(math.floor(R * math.log(original / (fast * 2 * math.pi)) / (2 * math.log(base))), 0)
-        hi = min(math.ceil(R * math.log(original / (slow * 2 * math.pi)) / (2 * math.log(base))), R - 1)
-        hi = hi + 0.001 if hi == lo else hi
+        lo, hi = (R * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
+                  for turns in (fast, slow))
+        lo, hi = math.floor(lo), math.ceil(hi)
+        if hi < 0:          # the whole ramp lies before the first pair
+            lo, hi = -1, 0
+        elif lo > R - 1:    # or behind the last
+            hi = lo + 1
+        else:
+            lo, hi = max(lo, 0), min(hi, R - 1)
+            hi = hi + 0.001 if hi == lo else hi
         ramp = np.clip((np.arange(R // 2) - lo) / (hi - lo), 0, 1)
         f = f * (1 - ramp) + f / factor * ramp
         gain = gain or 0.1 * math.log(factor) + 1.0

@@ -2,6 +2,8 @@
 
 Tolerances are those of Case.check unless a test derives its own.
 """
+import math
+
 import pytest
 import torch
 
@@ -158,3 +160,26 @@ def test_append_rotates_queries_in_place(i):
     own, again = q.contiguous().clone(), torch.zeros_like(cache)
     B.moe_kv_append(cfg, T, own, k, v, pos, slots, table, own, again)
     assert torch.equal(own, want) and torch.equal(again, cache)
+
+
+# --------------------------------------------------------------------- table
+@pytest.mark.parametrize("base,original,scaled", [(4.0, 131072.0, False), (1e4, 4.0, True),
+                                                  (1e4, 1e12, False), (1e6, 0.5, True)])
+@pytest.mark.parametrize("R", [64, 96, 128])
+def test_yarn_whose_ramp_lies_on_one_side_of_the_pairs(base, original, scaled, R):
+    """Every pair turns more than 32 times in the original context and keeps its
+    frequency, or less than once and is slowed down by the factor. Positions are
+    small, so that fp64 angles are exact to 2^-45: the table's bound is its series'
+    2^-29 and 2^-29 of the angle that is cut off, two roundings of the fractions,
+    one of the gain and of its product, all on values up to the gain."""
+    n, factor = 200, 8.0
+    f = base ** (-2.0 * torch.arange(R // 2, dtype=torch.float64) / R)
+    turns = original * f / (2 * math.pi)
+    assert (turns < 1).all() if scaled else (turns > 32).all()
+    a = torch.arange(n, dtype=torch.float64)[:, None] * (f / factor if scaled else f)
+    gain = 0.1 * math.log(factor) + 1
+    want = gain * torch.cat([a.cos(), a.sin()], 1)
+    cfg = B.make_attn_config(1, 1, 128, rotary_dim=R, rope_positions=n)
+    out = torch.empty(n, R, device="cuda")
+    B.moe_rope_table(cfg, n, None, B.make_rope_scaling(base, "yarn", factor, original), out)
+    assert ((out.double().cpu() - want).abs() <= 4 * 2.0 ** -24 * gain).all()
