@@ -558,7 +558,8 @@ MOE_API size_t moe_kv_page_bytes(const moe_attn_config* cfg);
  * for the R/2 pairs, then sin(p f_i), p = positions[r] (int32, any value), or
  * p = r when positions is NULL. Each angle is reduced exactly: the frequency is
  * held as a 64-bit fraction of a turn, so p f_i mod 1 turn is an integer product
- * that wraps. n may be up to 2^24. */
+ * that wraps. The frequency itself is fp64's (53 bits): an angle is off by 2^-32
+ * at a million positions, by up to 2^-21 at 2^31. n may be up to 2^24. */
 MOE_API int moe_rope_table(const moe_attn_config* cfg, int n, const int32_t* positions,
                            const moe_rope_scaling* scaling, float* table, void* ws,
                            size_t ws_bytes, void* stream);

@@ -2,6 +2,7 @@
 
 Tolerances are those of Case.check unless a test derives its own.
 """
+import decimal
 import math
 
 import pytest
@@ -183,3 +184,31 @@ def test_yarn_whose_ramp_lies_on_one_side_of_the_pairs(base, original, scaled, R
     out = torch.empty(n, R, device="cuda")
     B.moe_rope_table(cfg, n, None, B.make_rope_scaling(base, "yarn", factor, original), out)
     assert ((out.double().cpu() - want).abs() <= 4 * 2.0 ** -24 * gain).all()
+
+
+PI = decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+
+
+@pytest.mark.parametrize("R,base", [(64, 1e4), (128, 1e6), (96, 1e4), (34, 5e5)])
+def test_table_at_far_positions(R, base):
+    """Against angles reduced with 60 digits. The table's own bound is that of the
+    test above. A frequency is fp64's power (2^-52), its turns a division by a
+    rounded 2 pi (2^-53 and 2^-54) cut to 2^-64, and its exponent is rounded, which
+    ln(base) multiplies: the position multiplies all of them."""
+    pos = [0, 1, -1, 4095, 131071, 1 << 20, (1 << 20) - 1, 16777213, -16777213, 1 << 27, 2 ** 31 - 1, -2 ** 31]
+    cfg = B.make_attn_config(1, 1, 128, rotary_dim=R, rope_positions=len(pos))
+    out = torch.empty(len(pos), R, device="cuda")
+    B.moe_rope_table(cfg, len(pos), torch.tensor(pos, dtype=torch.int32, device="cuda"),
+                     B.make_rope_scaling(base), out)
+    got = out.double().cpu()
+    with decimal.localcontext() as ctx:
+        ctx.prec = 60
+        f = [decimal.Decimal(base) ** (decimal.Decimal(-2 * i) / R) for i in range(R // 2)]
+        for r, p in enumerate(pos):
+            for i in range(R // 2):
+                turns = p * f[i] / (2 * PI)
+                a = float((turns - turns.to_integral_value()) * 2 * PI)
+                exponent = 2 * i / R * math.log(base) * 2.0 ** -53
+                tol = 4 * 2.0 ** -24 + abs(p) * (float(f[i]) * (2.0 ** -51 + exponent) + 7 * 2.0 ** -64)
+                assert abs(got[r, i] - math.cos(a)) <= tol, (p, i)
+                assert abs(got[r, R // 2 + i] - math.sin(a)) <= tol, (p, i)
