@@ -34,6 +34,12 @@ class Cache:
         order = torch.randperm(pages, device="cuda", dtype=torch.int32)
         self.page_table = order.reshape(requests, per).contiguous()
         self.page_size = cfg.page_size
+        self.tokens = min(per * cfg.page_size, cfg.rope_positions)   # room of a request
+
+    def room(self, lens, new):
+        """Refuses, before anything is enqueued, what has no page or no position."""
+        if max(lens) + new > self.tokens:
+            raise ValueError(f"a request of {max(lens) + new} tokens; the cache holds {self.tokens}")
 
     def slots(self, request, position):
         """Slot of each (request, position) pair."""
@@ -91,6 +97,7 @@ class Decoder:
 def prompt(model, cache, xs):
     """The prompts xs [n_b, hidden] of all requests in one call."""
     lens = [x.shape[0] for x in xs]
+    cache.room(lens, 0)
     request = torch.repeat_interleave(torch.arange(len(xs)), torch.tensor(lens)).cuda()
     position = torch.cat([torch.arange(n) for n in lens]).cuda()
     offsets = torch.tensor([0] + lens).cumsum(0).int().cuda()
@@ -103,6 +110,8 @@ class DecodeGraph:
     """One token per request, captured once; the lengths live on the device."""
 
     def __init__(self, model, cache, lens):
+        cache.room(lens, 1)             # (the warm-up writes a token)
+        self.host_lens = list(lens)
         n, hidden = len(lens), model.layers[0]["o"].shape[0]
         self.x = torch.zeros(n, hidden, dtype=torch.bfloat16, device="cuda")
         self.lens = torch.tensor(lens, dtype=torch.int32, device="cuda")   # cached tokens so far
@@ -129,6 +138,8 @@ class DecodeGraph:
         return out
 
     def step(self, x):
+        self.cache.room(self.host_lens, 1)
+        self.host_lens = [n + 1 for n in self.host_lens]
         self.x.copy_(x)
         self.graph.replay()
         return self.out
