@@ -4,6 +4,7 @@ Tolerances are those of Case.check unless a test derives its own.
 """
 import decimal
 import math
+import random
 
 import pytest
 import torch
@@ -212,3 +213,71 @@ def test_table_at_far_positions(R, base):
                 tol = 4 * 2.0 ** -24 + abs(p) * (float(f[i]) * (2.0 ** -51 + exponent) + 7 * 2.0 ** -64)
                 assert abs(got[r, i] - math.cos(a)) <= tol, (p, i)
                 assert abs(got[r, R // 2 + i] - math.sin(a)) <= tol, (p, i)
+
+
+# ------------------------------------------------------------- large batches
+def _batch(seed, n, most, queries):
+    """n requests: lengths 0 to `most`, query counts of `queries`, empty ones among both."""
+    rng = random.Random(seed)
+    lens = [rng.choice([0, 1, 15, 16, 17, rng.randint(0, most), rng.randint(0, most)]) for _ in range(n)]
+    qs = [rng.choice(queries) for _ in range(n)]
+    lens[0], qs[0], qs[-1] = most, max(queries), 0
+    return lens, qs
+
+
+BATCHES = [  # dtype, heads, kv heads, D, page, requests, longest, query counts, window
+    # every CTA of the split kernel plans up to 256 requests itself, 128 at a time
+    ("bf16", 2, 1, 128, 16, 128, 90, [1], 0), ("bf16", 2, 1, 128, 16, 129, 90, [1, 0], 0),
+    ("bf16", 2, 2, 64, 32, 256, 70, [1, 2, 0], 0),
+    # more are planned by the kernel before it, 1024 at a time: each type, rows of 4, 8 and 16
+    ("bf16", 2, 1, 128, 16, 257, 90, [1, 0], 0), ("bf16", 6, 1, 128, 16, 300, 60, [1], 20),
+    ("bf16", 6, 1, 128, 64, 300, 60, [1, 2, 0], 0), ("bf16", 2, 2, 64, 16, 1025, 50, [1, 0], 0),
+    ("bf16", 7, 1, 64, 16, 260, 300, [1], 0), ("bf16", 12, 1, 64, 16, 260, 90, [1, 3], 0),
+    ("bf16", 2, 1, 256, 16, 270, 60, [1, 0], 0), ("bf16", 8, 1, 256, 16, 270, 60, [1, 0], 0),
+    ("bf16", 5, 1, 256, 16, 270, 60, [1, 3], 9),
+    ("f32", 2, 1, 128, 16, 2100, 40, [1, 0], 0), ("f32", 6, 1, 128, 16, 300, 60, [1, 2], 0),
+    ("f32", 2, 2, 64, 16, 300, 90, [1, 2, 0], 0), ("f32", 8, 1, 64, 16, 270, 60, [1], 30),
+    ("f32", 2, 1, 256, 16, 300, 60, [1, 0], 0), ("f32", 4, 1, 256, 32, 270, 60, [1, 2], 0),
+    # the prompt kernel: requests and row tiles beyond a round of its plan
+    ("bf16", 2, 1, 128, 16, 1025, 60, [1, 0, 2, 40], 0), ("bf16", 1, 1, 64, 16, 2100, 90, [1, 0, 64], 20),
+    ("bf16", 4, 2, 256, 16, 1030, 50, [1, 0, 33], 0),
+]
+
+
+@pytest.mark.parametrize("i", range(len(BATCHES)))
+def test_large_batches(i):
+    dtype, heads, kv, D, page, n, most, queries, window = BATCHES[i]
+    lens, qs = _batch(i, n, most, queries)
+    c = Case(300 + i, dtype, heads, kv, D, page, lens, qs, window).run()
+    assert B.moe_get_status(c.ws) == (0, 0)
+    c.check()
+    out, lse = c.out.clone(), c.lse.clone()
+    c.out.fill_(1.0)
+    c.run()
+    assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+
+
+def test_large_batch_of_long_and_short_requests():
+    """Segments cut over many CTAs between hundreds that fit into one."""
+    lens, qs = _batch(50, 400, 200, [1])
+    for b in (3, 200, 398):
+        lens[b] = 6000
+    c = Case(350, "bf16", 4, 2, 128, 64, lens, qs).run()
+    assert B.moe_get_status(c.ws) == (0, 0)
+    c.check()
+
+
+def test_prompt_of_more_row_tiles_than_a_round_of_the_plan():
+    """8300 query tokens of a group of 32: 1038 row tiles of one request."""
+    c = Case(351, "bf16", 32, 1, 64, 64, [8300, 40], [8300, 2]).run()
+    assert B.moe_get_status(c.ws) == (0, 0)
+    c.check(rows=[0, 1, 7, 8, 1000, 4095, 4096, 8190, 8191, 8192, 8199, 8200, 8299])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_f32_rows_of_four_and_eight(D):
+    for heads, lens, qs in ((1, [3000, 1], [4, 1]), (4, [3000, 20], [1, 1]), (8, [2000, 7], [1, 0]),
+                            (3, [100, 40], [5, 3])):
+        c = Case(360 + heads, "f32", heads, 1, D, 32, lens, qs).run()
+        assert B.moe_get_status(c.ws) == (0, 0)
+        c.check()
