@@ -107,6 +107,13 @@ __device__ __forceinline__ void row_power(float top, float& up, float& down) {
   down = __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
 }
 
+// What a row's scores are multiplied by: never 0, since a masked score is -inf
+// and has to stay it. (Scores are below 2^28 before it: under the smallest
+// normal number all of them are 0.)
+__device__ __forceinline__ float score_gain(float down, float scale_log2) {
+  return fmaxf(down * scale_log2, 0x1p-126f);
+}
+
 // 1 / denominator times `gain`; 0 for a query that saw no key (NaN stays NaN).
 __device__ __forceinline__ float out_factor(float den, float gain) {
   return den > 0.0f || den != den ? gain / den : 0.0f;

@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        gain[nt][j] = __shfl_sync(~0u, q_gain[nt], (2 * c + j) * 4) * a.scale_log2;
+        gain[nt][j] = score_gain(__shfl_sync(~0u, q_gain[nt], (2 * c + j) * 4), a.scale_log2);
 
     float o[D / 32][NP][4];
 #pragma unroll

@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             __uint_as_float(v[j] & 0xffff0000u) * up);
           sts128(sm_rows + swizzled(wl * 32 + rl, lane % kRowLanes, kHalf), h[0], h[1], h[2], h[3]);
           const float mine = __shfl_sync(~0u, down, (lane % kRowsStep) * kRowLanes);
-          if (lane / kRowsStep == first + i) gain = mine * a.scale_log2;
+          if (lane / kRowsStep == first + i) gain = score_gain(mine, a.scale_log2);
         }
       }
       ptx::fence_proxy_async();

@@ -215,6 +215,20 @@ def test_table_at_far_positions(R, base):
                 assert abs(got[r, R // 2 + i] - math.sin(a)) <= tol, (p, i)
 
 
+# ------------------------------------------------------------ far ends of scales
+@pytest.mark.parametrize("dtype,D,lens,qs", [("bf16", 128, [40, 3], [1, 1]), ("bf16", 128, [300, 90], [70, 64]),
+                                             ("bf16", 256, [100], [80]), ("f32", 64, [40, 70], [2, 1])])
+@pytest.mark.parametrize("ks,scale", [(1e-20, 0.0), (1.0, 1e-30), (1e-30, 1e-8)])
+def test_zero_queries_under_tiny_scales(dtype, D, lens, qs, ks, scale):
+    """A row of zeros scores 0 everywhere whatever the scales: the mean of the
+    values, and the logarithm of the keys' number; masked keys stay masked."""
+    c = Case(370, dtype, 2, 2, D, 16, lens, qs, ks=ks, scale=scale)
+    c.q[:, 0] = 0
+    c.run()
+    assert B.moe_get_status(c.ws) == (0, 0)
+    c.check()
+
+
 # ------------------------------------------------------------- large batches
 def _batch(seed, n, most, queries):
     """n requests: lengths 0 to `most`, query counts of `queries`, empty ones among both."""
