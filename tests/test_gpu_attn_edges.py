@@ -10,6 +10,7 @@ import pytest
 import torch
 
 from expert_moe_layer_gb300 import binding as B
+from oracle import attn_oracle as A
 from test_gpu_attn import Case
 
 pytestmark = pytest.mark.gpu
@@ -295,3 +296,81 @@ def test_f32_rows_of_four_and_eight(D):
         c = Case(360 + heads, "f32", heads, 1, D, 32, lens, qs).run()
         assert B.moe_get_status(c.ws) == (0, 0)
         c.check()
+
+
+# ---------------------------------------------------- layouts and strange rows
+MIXED = [  # dtype, heads, kv heads, D, page, lens, query tokens, window: rows of 4, 8, 16, and the prompt kernel
+    ("bf16", 2, 1, 128, 16, [50, 9], [2, 2], 0), ("bf16", 4, 1, 64, 32, [50, 9], [2, 1], 0),
+    ("bf16", 3, 1, 128, 64, [500, 70], [5, 4], 0), ("f32", 2, 1, 128, 16, [90, 9], [4, 3], 0),
+    ("bf16", 2, 1, 256, 16, [70], [6], 30), ("bf16", 4, 2, 128, 16, [700, 90], [200, 40], 0),
+    ("bf16", 4, 2, 64, 256, [700, 90], [200, 40], 50), ("bf16", 2, 2, 256, 32, [300, 90], [130, 70], 0),
+]
+
+
+@pytest.mark.parametrize("i", range(len(MIXED)))
+def test_rows_of_nan_and_infinity_concern_themselves_alone(i):
+    """Padding rows of a captured batch hold anything."""
+    dtype, heads, kv, D, page, lens, qs, window = MIXED[i]
+    c = Case(400 + i, dtype, heads, kv, D, page, lens, qs, window)
+    strange = [r for r in range(max(qs)) if r % 3 == 1]
+    for b in range(len(lens)):
+        for n, r in enumerate(r for r in strange if r < qs[b]):
+            c.q[c.offs[b] + r] = [float("nan"), float("inf"), -float("inf")][n % 3]
+    c.run()
+    assert B.moe_get_status(c.ws) == (0, 0)
+    c.check(rows=[r for r in range(max(qs)) if r % 3 != 1])
+    assert torch.isnan(c.out[c.offs[0] + 1]).all()      # a query of NaN says so
+
+
+@pytest.mark.parametrize("i", range(len(MIXED)))
+def test_queries_whose_heads_come_first(i):
+    """[heads, tokens, channels] in memory: the token stride is the smaller one."""
+    dtype, heads, kv, D, page, lens, qs, window = MIXED[i]
+    c = Case(420 + i, dtype, heads, kv, D, page, lens, qs, window).run()
+    out, lse = c.out.clone(), c.lse.clone()
+    c.q = c.q.transpose(0, 1).contiguous().transpose(0, 1)
+    c.out.fill_(1.0)
+    c.run()
+    assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+
+
+@pytest.mark.parametrize("i", range(len(MIXED)))
+def test_tokens_of_bad_pages_are_left_out(i):
+    """The first, a middle and the last page of a request, below and beyond the
+    cache; queries are compared with attention over the tokens that are left."""
+    dtype, heads, kv, D, page, lens, qs, window = MIXED[i]
+    c = Case(440 + i, dtype, heads, kv, D, page, lens, qs)
+    n, q = lens[0], qs[0]
+    used = -(-n // page)
+    bad = sorted({0, used // 2, used - 1}) if used > 3 else [0]
+    for p, v in zip(bad, (-1, c.cache.shape[0], 2 ** 31 - 1)):
+        c.d["table"][0, p] = v
+    c.run()
+    assert B.moe_get_status(c.ws) == (5, B.DEV_BAD_PAGE)
+    c.check(only=range(1, len(lens)))
+    keep = torch.tensor([t for t in range(n) if t // page not in bad])
+    qd, out, lse = c.q.double().cpu().numpy(), c.out.double().cpu().numpy(), c.lse.double().cpu().numpy()
+    for r in sorted({0, 1, q // 2, q - 1}):
+        k = keep[keep <= n - q + r].numpy()
+        if not len(k):
+            assert (out[r] == 0).all() and (lse[r] == -math.inf).all()
+            continue
+        ref, l, size, reach = A.attention(qd[r:r + 1], c.k[0][k], c.v[0][k], len(k), c.scale)
+        ds, sums = (D / 16 + 4) * 2.0 ** -23 * reach, (n / 16 + 32) * 2.0 ** -23
+        p = 2.0 ** -11 if dtype == "bf16" else 2.0 ** -21
+        tol = c.u * abs(ref) + size * (2 * ds[..., None] + p + sums + 2.0 ** -21)
+        assert (abs(out[r:r + 1] - ref) <= tol).all(), r
+        assert (abs(lse[r:r + 1] - l) <= ds + sums + 2.0 ** -20 + 2.0 ** -23 * abs(l)).all(), r
+
+
+@pytest.mark.parametrize("dtype,heads,D", [("bf16", 64, 64), ("bf16", 512, 128), ("bf16", 130, 256),
+                                           ("f32", 512, 64), ("bf16", 63, 128)])
+def test_single_tokens_of_very_wide_groups(dtype, heads, D):
+    """One kv head under up to 512 query heads, one token each: without offsets."""
+    c = Case(460, dtype, heads, 1, D, 16, [100, 0, 1, 333], [1] * 4).run(offs=False)
+    assert B.moe_get_status(c.ws) == (0, 0)
+    c.check()
+    want = c.out.clone()
+    c.out.fill_(1.0)
+    B.moe_kv_attention(c.cfg, 4, 4, 1, c.q, c.d["offs"], c.d["lens"], c.d["table"], c.cache, c.out, None, c.ws)
+    assert torch.equal(c.out, want)
