@@ -309,7 +309,6 @@ struct Piece {
   int lo, hi;                      // keys [lo, hi) are seen by some row
   int first, tiles;                // its key tiles
   bool alone;                      // it is the whole segment
-  bool head;                       // the segment begins with it
   int cta0, cta1;                  // CTAs of the segment's pieces
   SeqInfo sq;
 };
@@ -371,7 +370,6 @@ struct Cursor {
       const int t0 = max(0, p0 - kSetup);
       p.first = p.lo / H::kKeys + t0;
       p.tiles = p1 - kSetup - t0;
-      p.head = p0 == 0;
       p.alone = p0 == 0 && p1 == len;
       p.cta0 = static_cast<int>((seg + kSnap) / per);
       p.cta1 = max(p.cta0, static_cast<int>((seg + len - kSnap - 1) / per));

@@ -22,6 +22,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kSms = 152;  // of this part: sizes of work are measured by it
 // CTAs per SM of the kernels of one and of four heads per thread. Three of the
 // latter spill 10 registers and are still faster (29.8 us, the case below) than
 // two without (34.0) or four (34.3); the former need the registers of five.
@@ -538,7 +539,7 @@ cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t st) {
   // one head after the other (8 of each beside them): 64 tokens 4.9 and 7.1 us,
   // 1024 tokens 10.0 and 11.1, 2048 tokens 17.7 and 15.5.
   const long all = units * a.T * (a.q_heads + 2l * a.kv_heads);
-  const int hb = all / 4 >= 152l * (a.kv_heads ? 1024 : 192) ? 4 : 1;
+  const int hb = all / 4 >= static_cast<long>(kSms) * (a.kv_heads ? 1024 : 192) ? 4 : 1;
   const int cq = (a.q_heads + hb - 1) / hb, ck = (a.kv_heads + hb - 1) / hb;
   const long total = units * a.T * (cq + 2l * ck);
   if (total == 0) return cudaSuccess;
@@ -568,7 +569,7 @@ cudaError_t launch_rope_table(const RopeTurns& turns, int pairs, float gain, int
   // enough rows per block to use each thread's frequency several times, few
   // enough to give every SM work
   const int lanes = kThreads / pairs;
-  int rows = n / (152 * 16);
+  int rows = n / (kSms * 16);
   rows = (rows < lanes ? lanes : rows + lanes - 1) / lanes * lanes;
   return launch_pdl(&rope_table_kernel, dim3((n + rows - 1) / rows), dim3(kThreads), 0, st, turns,
                     pairs, gain, n, positions, table, rows);

@@ -11,7 +11,10 @@
 // completed. The GEMM kernels use this: their tile tables (written at least
 // two kernels earlier) and their weight operands (never written by the
 // library) are read before the wait, so the first weight tiles stream in
-// while the preceding kernel finishes.
+// while the preceding kernel finishes. So does the split attention kernel with
+// everything that its call was handed (lengths, page ids, queries, the cache):
+// the kernel before it is the call's own, which only clears the status and the
+// counters, and what the caller enqueued ended before that one began.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -632,6 +632,9 @@ MOE_API int moe_kv_read(const moe_attn_config* cfg, int N, const int64_t* slots,
  * MOE_DEV_BAD_PAGE for a page id outside [0, num_pages) (its tokens are left
  * out), or a length below 0 or beyond the table's row (it is clamped).
  * num_seqs and max_pages may be up to 2^18 and 2^20.
+ * max_q_len chooses the kernel of the whole call: from 64 rows (max_q_len times
+ * the heads of a group, bf16) one that is made for many rows. Single tokens are
+ * right there but slow, so a batch of both is faster as two calls.
  * ws: moe_kv_attention_workspace_size(cfg, num_seqs, T, max_q_len) bytes
  * (0: invalid). */
 MOE_API size_t moe_kv_attention_workspace_size(const moe_attn_config* cfg, int num_seqs, int T,
@@ -661,7 +664,9 @@ MOE_API int moe_get_status(const void* ws, void* stream, uint32_t* flags);
  * top-k ids against E. A failed check skips the
  * access or clamps the value into range (the outputs are then unusable) and
  * is counted in a device record, which also keeps the site, index and bound
- * of the first failure. Same entry points and results otherwise; slower. */
+ * of the first failure. The attention calls have no such checks: what they
+ * read from a caller (positions, slots, page ids, offsets, lengths) is checked
+ * in libmoe.so already. Same entry points and results otherwise; slower. */
 typedef struct {
   uint32_t count; /* failed check evaluations since the last take (one bad
                      value may be checked, and counted, several times)      */
