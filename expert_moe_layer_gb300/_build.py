@@ -24,10 +24,11 @@ LIB_DEBUG = os.path.join(PKG, "libmoe_debug.so")
 
 SOURCES = ["moe_api.cu", "kernels_gemm.cu", "kernels_gemm_pair.cu", "kernels_mlp_fused.cu",
            "kernels_route.cu", "kernels_align.cu", "attn_api.cu", "kernels_rope.cu",
-           "kernels_attn.cu", "kernels_attn_prompt.cu"]
+           "kernels_attn.cu", "kernels_attn_prompt.cu", "serve_api.cu", "kernels_pool.cu",
+           "kernels_norm.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "launch.cuh", "align_block.cuh", "topk_warp.cuh", "act.cuh",
            "dbg.cuh", "attn.h", "kv4.cuh",
-           "attn_dev.cuh"]
+           "attn_dev.cuh", "serve.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # hidden visibility: only the MOE_API entry points of include/moe.h are
 # exported, so two builds in one process share no internal symbol

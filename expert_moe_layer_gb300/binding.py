@@ -26,6 +26,7 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
                 6: "MOE_ERR_TIMEOUT"}
 DEV_BAD_EXPERT_ID, DEV_CAP_OVERFLOW, DEV_TIMEOUT, DEV_BAD_SEGMENT = 0x1, 0x2, 0x4, 0x8
 DEV_BAD_POSITION, DEV_BAD_SLOT, DEV_BAD_PAGE = 0x10, 0x20, 0x40
+DEV_BAD_ROW, DEV_NO_PAGE = 0x80, 0x100
 
 
 class MoeError(RuntimeError):
@@ -63,6 +64,27 @@ class RopeScaling(ctypes.Structure):
     _fields_ = [("base", ctypes.c_double), ("kind", ctypes.c_int), ("factor", ctypes.c_double),
                 ("original_positions", ctypes.c_double), ("slow_turns", ctypes.c_double),
                 ("fast_turns", ctypes.c_double), ("attention_factor", ctypes.c_double)]
+
+
+class KvCaches(ctypes.Structure):
+    """Caches (one per layer) that the same page ids index (make_kv_caches)."""
+    _fields_ = [("num_caches", ctypes.c_int), ("num_pages", ctypes.c_int64),
+                ("caches", ctypes.POINTER(ctypes.c_void_p))]
+
+
+class KvPool(ctypes.Structure):
+    """A page table and its caches (make_kv_pool)."""
+    _fields_ = [("page_table", ctypes.c_void_p), ("held", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p), ("num_rows", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("caches", KvCaches)]
+
+
+class NormConfig(ctypes.Structure):
+    _fields_ = [("hidden_size", ctypes.c_int), ("act_dtype", ctypes.c_int),
+                ("residual_dtype", ctypes.c_int), ("kind", ctypes.c_int),
+                ("post_norm", ctypes.c_int), ("gate", ctypes.c_int),
+                ("residual_scale", ctypes.c_float), ("weight_offset", ctypes.c_float),
+                ("eps", ctypes.c_float)]
 
 
 class WorkspaceOffsets(ctypes.Structure):
@@ -123,6 +145,15 @@ def make_rope_scaling(base=10000.0, kind="none", factor=1.0, original_positions=
                        attention_factor)
 
 
+def make_norm_config(hidden_size, kind="rms", act_dtype="bf16", residual_dtype=None,
+                     post_norm=False, gate="linear", residual_scale=1.0, weight_offset=0.0,
+                     eps=1e-6) -> NormConfig:
+    dt = {"bf16": MOE_BF16, "f32": MOE_F32}
+    return NormConfig(hidden_size, dt[act_dtype], dt[residual_dtype or act_dtype],
+                      {"rms": 0, "layer": 1}[kind], int(bool(post_norm)),
+                      {"linear": 0, "sigmoid": 1}[gate], residual_scale, weight_offset, eps)
+
+
 _libs: dict[bool, ctypes.CDLL] = {}  # debug build? -> loaded library
 _use_debug = False
 _lock = threading.Lock()
@@ -130,6 +161,7 @@ _VP, _SZ, _I = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
 _I64 = ctypes.c_int64
 _CFG = ctypes.POINTER(MoeConfig)
 _ACFG = ctypes.POINTER(AttnConfig)
+_POOL, _CACHES = ctypes.POINTER(KvPool), ctypes.POINTER(KvCaches)
 _ROWS = [_VP, _I64, _I64]  # a strided [T, heads, D] tensor: pointer, token and head strides
 
 _SIGS = {
@@ -168,6 +200,15 @@ _SIGS = {
     "moe_kv_attention_workspace_size": (_SZ, [_ACFG, _I, _I, _I]),
     "moe_kv_attention": (_I, [_ACFG, _I, _I, _I] + _ROWS + [_VP] * 3 + [_I, _VP, _I64] +
                          [_VP, _VP, _VP, _SZ, _VP]),
+    "moe_kv_pool_workspace_size": (_SZ, [_ACFG, _POOL, _I]),
+    "moe_kv_fork": (_I, [_ACFG, _POOL, _I] + [_VP] * 4 + [_SZ, _VP]),
+    "moe_kv_reserve": (_I, [_ACFG, _POOL, _I] + [_VP] * 4 + [_SZ, _VP]),
+    "moe_kv_release": (_I, [_ACFG, _POOL, _I] + [_VP] * 3 + [_SZ, _VP]),
+    "moe_kv_compact": (_I, [_ACFG, _POOL, _VP, _VP, _SZ, _VP]),
+    "moe_kv_copy_pages": (_I, [_ACFG, _CACHES, _CACHES, _I, _VP, _VP, _VP, _SZ, _VP]),
+    "moe_validate_norm_config": (_I, [ctypes.POINTER(NormConfig)]),
+    "moe_norm": (_I, [ctypes.POINTER(NormConfig), _I, _VP, _I64, _VP, _I64, _VP, _VP, _VP, _I64,
+                      _I64] + [_VP] * 5 + [_SZ, _VP]),
     "moe_debug_build": (_I, []),
     "moe_debug_take": (_I, [ctypes.POINTER(DebugRecord)]),
     "moe_debug_selftest": (_I, [_VP]),
@@ -491,6 +532,131 @@ def moe_kv_attention(cfg, num_seqs, T, max_q_len, q, q_offsets, seq_lens, page_t
         *_cache(cache, cfg), _typed("out", out, cfg.act_dtype, (T, cfg.num_heads, cfg.head_dim)),
         _typed("lse", lse, "f32", (T, cfg.num_heads)), _p(ws), _nbytes(ws),
         _stream(stream)))
+
+
+# --------------------------------------------------------------- shared pages
+def make_kv_caches(cfg, caches) -> KvCaches:
+    """The caches (uint8 tensors [pages, kv heads, block bytes], one per layer)
+    that the same page ids index. Keeps the tensors alive."""
+    caches = list(caches)
+    if not caches:
+        raise ValueError("at least one cache")
+    found = [_cache(c, cfg) for c in caches]
+    if any(n != found[0][1] for _, n in found):
+        raise ValueError("the caches must have the same number of pages; got "
+                         f"{[n for _, n in found]}")
+    array = (ctypes.c_void_p * len(found))(*[p for p, _ in found])
+    out = KvCaches(len(found), found[0][1], array)
+    out.keep = (caches, array)
+    return out
+
+
+def make_kv_pool(cfg, page_table, held, refs, caches) -> KvPool:
+    """A pool over page_table [rows, max_pages], held [rows] and refs [pages]
+    (int32) and its caches (tensors, or what make_kv_caches returned). Keeps the
+    tensors alive."""
+    if not isinstance(caches, KvCaches):
+        caches = make_kv_caches(cfg, caches)
+    rows, width = page_table.shape
+    out = KvPool(_typed("page_table", page_table, "i32", (rows, width)),
+                 _typed("held", held, "i32", (rows,)),
+                 _typed("refs", refs, "i32", (caches.num_pages,)), rows, width, caches)
+    out.keep = (page_table, held, refs, caches)
+    return out
+
+
+def kv_pool_workspace_size(cfg, pool, n=0) -> int:
+    return lib().moe_kv_pool_workspace_size(ctypes.byref(cfg), ctypes.byref(pool), n)
+
+
+def moe_kv_fork(cfg, pool, n, parents, children, tokens, ws=None, stream=None):
+    _check("moe_kv_fork", lib().moe_kv_fork(
+        ctypes.byref(cfg), ctypes.byref(pool), n, _typed("parents", parents, "i32", (n,)),
+        _typed("children", children, "i32", (n,)), _typed("tokens", tokens, "i32", (n,)), _p(ws),
+        _nbytes(ws), _stream(stream)))
+
+
+def moe_kv_reserve(cfg, pool, n, rows, start, end, ws, stream=None):
+    _check("moe_kv_reserve", lib().moe_kv_reserve(
+        ctypes.byref(cfg), ctypes.byref(pool), n, _typed("rows", rows, "i32", (n,)),
+        _typed("start", start, "i32", (n,)), _typed("end", end, "i32", (n,)), _p(ws),
+        _nbytes(ws), _stream(stream)))
+
+
+def moe_kv_release(cfg, pool, n, rows, keep=None, ws=None, stream=None):
+    _check("moe_kv_release", lib().moe_kv_release(
+        ctypes.byref(cfg), ctypes.byref(pool), n, _typed("rows", rows, "i32", (n,)),
+        _typed("keep", keep, "i32", (n,)), _p(ws), _nbytes(ws), _stream(stream)))
+
+
+def moe_kv_compact(cfg, pool, used, ws, stream=None):
+    _check("moe_kv_compact", lib().moe_kv_compact(
+        ctypes.byref(cfg), ctypes.byref(pool), _typed("used", used, "i32", (1,)), _p(ws),
+        _nbytes(ws), _stream(stream)))
+
+
+def moe_kv_copy_pages(cfg, src_caches, dst_caches, n, src, dst, ws=None, stream=None):
+    _check("moe_kv_copy_pages", lib().moe_kv_copy_pages(
+        ctypes.byref(cfg), ctypes.byref(src_caches), ctypes.byref(dst_caches), n,
+        _typed("src", src, "i32", (n,)), _typed("dst", dst, "i32", (n,)), _p(ws), _nbytes(ws),
+        _stream(stream)))
+
+
+# ---------------------------------------------------------------------- norms
+def validate_norm_config(cfg: NormConfig) -> int:
+    return lib().moe_validate_norm_config(ctypes.byref(cfg))
+
+
+def _norm_rows(name, t, dtype, T, H):
+    """(pointer, row stride) of a [T, H] tensor whose channels are contiguous."""
+    if t is None:
+        return None, 0
+    if t.dtype is not _dt(dtype):
+        raise ValueError(f"{name} must be {_dt(dtype)}; got {t.dtype}")
+    if t.shape != (T, H):
+        raise ValueError(f"{name} must have shape {(T, H)}; got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError("libmoe takes device tensors; got one on " + str(t.device))
+    st, sd = t.stride()
+    if sd != 1 and H > 1:
+        raise ValueError(f"the channels of {name} must be contiguous")
+    return t.data_ptr(), st
+
+
+def _gate(gate, cfg, T):
+    """(pointer, token stride, channel stride) of a gate [H], [T, 1] or [T, H]."""
+    if gate is None:
+        return None, 0, 0
+    H = cfg.hidden_size
+    if gate.dtype is not _dt(cfg.act_dtype):
+        raise ValueError(f"gate must be {_dt(cfg.act_dtype)}; got {gate.dtype}")
+    if not gate.is_cuda:
+        raise ValueError("libmoe takes device tensors; got one on " + str(gate.device))
+    if gate.shape == (H,):
+        token, channel = 0, gate.stride(0)
+    elif gate.shape == (T, H):
+        token, channel = gate.stride()
+    elif gate.shape == (T, 1):
+        token, channel = gate.stride(0), 0
+    else:
+        raise ValueError(f"gate must have shape {(H,)}, {(T, 1)} or {(T, H)}; "
+                         f"got {tuple(gate.shape)}")
+    if H == 1:
+        channel = 0
+    if channel not in (0, 1):
+        raise ValueError("the channels of the gate must be contiguous")
+    return gate.data_ptr(), token, channel
+
+
+def moe_norm(cfg, T, y, x, post_w, post_b, gate, pre_w, pre_b, x_out, h, ws=None, stream=None):
+    H = cfg.hidden_size
+    _check("moe_norm", lib().moe_norm(
+        ctypes.byref(cfg), T, *_norm_rows("y", y, cfg.act_dtype, T, H),
+        *_norm_rows("x", x, cfg.residual_dtype, T, H), _typed("post_w", post_w, "f32", (H,)),
+        _typed("post_b", post_b, "f32", (H,)), *_gate(gate, cfg, T),
+        _typed("pre_w", pre_w, "f32", (H,)), _typed("pre_b", pre_b, "f32", (H,)),
+        _typed("x_out", x_out, cfg.residual_dtype, (T, H)), _typed("h", h, cfg.act_dtype, (T, H)),
+        _p(ws), _nbytes(ws), _stream(stream)))
 
 
 def moe_get_status(ws, stream=None) -> tuple[int, int]:

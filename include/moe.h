@@ -92,6 +92,9 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
 #define MOE_DEV_BAD_SLOT 0x20u     /* cache slot outside the cache          */
 #define MOE_DEV_BAD_PAGE 0x40u     /* page id outside the cache, or a length
                                       outside the page table                */
+#define MOE_DEV_BAD_ROW 0x80u      /* page table row outside the pool, named
+                                      twice, or not in the state a call needs */
+#define MOE_DEV_NO_PAGE 0x100u     /* not enough free pages                  */
 
 /* Layer description. The field names follow the FusedMoE arguments the
  * pages pass (num_experts, top_k, hidden_size, intermediate_size,
@@ -645,6 +648,143 @@ MOE_API int moe_kv_attention(const moe_attn_config* cfg, int num_seqs, int T, in
                              const int32_t* page_table, int max_pages, const void* cache,
                              int64_t num_pages, void* out, float* lse, void* ws,
                              size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Pages that several requests share. The source pages leave a cache's pages to
+ * the serving engine; these entry points keep the page table, so that a batch
+ * can fork, grow and shrink inside a captured loop.
+ *
+ * A pool is a page table with num_rows rows of max_pages entries (the page_table
+ * of moe_kv_attention), `held` (how many entries of a row are in use, from its
+ * first on) and `refs` (how many rows hold a page; 0 = free). Fresh pools are all
+ * zeros in held and refs. `caches` are the caches, one per layer, that these page
+ * ids index. The struct and the array of pointers are read on the host, by the
+ * call.
+ *
+ * Every call is one atomic step: it decides by the pool as it finds it, and what
+ * comes out does not depend on the order in which the GPU runs it. n items are
+ * given in device arrays of int32 [n]; n may be up to 2^18. An item that does
+ * not fit (see each call) changes nothing, sets MOE_DEV_BAD_ROW, and leaves the
+ * others as they are. An entry outside [0, num_pages) among those held, or a
+ * count that would fall below 0, sets MOE_DEV_BAD_PAGE and is passed over. */
+#define MOE_KV_MAX_CACHES 256
+
+typedef struct {
+  int num_caches;       /* 1 .. MOE_KV_MAX_CACHES                             */
+  int64_t num_pages;    /* pages of each                                      */
+  void* const* caches;  /* host array of num_caches device pointers, each to
+                           [num_pages, num_kv_heads, B] bytes                 */
+} moe_kv_caches;
+
+typedef struct {
+  int32_t* page_table;  /* [num_rows, max_pages]                              */
+  int32_t* held;        /* [num_rows]                                         */
+  int32_t* refs;        /* [num_pages]                                        */
+  int num_rows;         /* 1 .. 2^18                                          */
+  int max_pages;        /* 1 .. 2^20                                          */
+  moe_kv_caches caches; /* num_pages up to 2^30                               */
+} moe_kv_pool;
+
+/* Bytes of `ws` that the pool calls of up to n items need (0: invalid). */
+MOE_API size_t moe_kv_pool_workspace_size(const moe_attn_config* cfg, const moe_kv_pool* pool,
+                                          int n);
+
+/* moe_kv_fork: row children[i] gets the pages of the first tokens[i] tokens of
+ * row parents[i], which both hold from then on; nothing is copied. The page that
+ * the tokens end in is shared too: moe_kv_reserve gives each row its own before
+ * it is written to. A child holds nothing (released, or fresh) and is named once;
+ * a row is not parent and child in one call; the parent holds that many tokens.
+ * ws: NULL, or >= 4 bytes for the status word. */
+MOE_API int moe_kv_fork(const moe_attn_config* cfg, const moe_kv_pool* pool, int n,
+                        const int32_t* parents, const int32_t* children, const int32_t* tokens,
+                        void* ws, size_t ws_bytes, void* stream);
+
+/* moe_kv_reserve: row rows[i] (row i when rows is NULL) is about to be given the
+ * tokens start[i] .. end[i] - 1. Afterwards it holds pages for end[i] tokens (or
+ * the more that it held), and no other row holds a page that these tokens lie on:
+ * a shared one is replaced, and if it begins before token start[i] its contents
+ * are copied in every cache. Fresh pages are the lowest free ones, given to the
+ * items in their order and to an item's entries in theirs. A page that every
+ * holder left stays free until the next call. An item that finds too few free
+ * pages, and every later one that needs any, gets none and sets MOE_DEV_NO_PAGE.
+ * 0 <= start <= end <= max_pages * page_size; of items with the same row the first
+ * counts. ws: moe_kv_pool_workspace_size(cfg, pool, n) bytes. */
+MOE_API int moe_kv_reserve(const moe_attn_config* cfg, const moe_kv_pool* pool, int n,
+                           const int32_t* rows, const int32_t* start, const int32_t* end,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/* moe_kv_release: row rows[i] (row i when rows is NULL) keeps the pages of its
+ * first keep[i] tokens (none when keep is NULL) and gives the others back: their
+ * entries become -1, and pages that no row holds are free. A row that holds no
+ * more than that is left as it is; one that is named twice keeps the least.
+ * ws: NULL, or >= 4 bytes for the status word. */
+MOE_API int moe_kv_release(const moe_attn_config* cfg, const moe_kv_pool* pool, int n,
+                           const int32_t* rows, const int32_t* keep, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/* moe_kv_compact: afterwards the pages in use are the first ones. With U pages in
+ * use, the k-th of those from page U on moves to the k-th free page before it, in
+ * every cache, in the counts and in every row that holds it. (U: pages with a
+ * count other than 0.) The pages that were left keep their old bytes.
+ *   used  [1] int32 out, nullable: U
+ * ws: moe_kv_pool_workspace_size(cfg, pool, 0) bytes. */
+MOE_API int moe_kv_compact(const moe_attn_config* cfg, const moe_kv_pool* pool, int32_t* used,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/* moe_kv_copy_pages: page dst[i] of every cache of `to` becomes page src[i] of
+ * the cache of `from` with the same number (as many of each; they may be the same
+ * caches). -1 in either leaves item i out. No page may be written twice, or
+ * written and read, in one call. A page outside its caches sets MOE_DEV_BAD_PAGE
+ * and the item is left out. ws: NULL, or >= 4 bytes for the status word. */
+MOE_API int moe_kv_copy_pages(const moe_attn_config* cfg, const moe_kv_caches* from,
+                              const moe_kv_caches* to, int n, const int32_t* src,
+                              const int32_t* dst, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Norms before and after a block (attention, or the MoE layer), with the
+ * residual that runs past it:
+ *   u = y, or N(y; post_w, post_b) with post_norm
+ *   r = x + residual_scale * g * u         g: the gate, 1 without
+ *   h = N(r; pre_w, pre_b)
+ *   N(v; w, b) = (v - m) / sqrt(mean((v - m)^2) + eps) * (w + weight_offset) + b
+ * with m = mean(v) for MOE_NORM_LAYER and 0 for MOE_NORM_RMS, over the H channels
+ * of a row. Everything is fp32 in between; h is taken from r before its rounding.
+ * Elements beyond 2^56 may overflow the sum of squares. */
+#define MOE_NORM_RMS 0
+#define MOE_NORM_LAYER 1
+#define MOE_GATE_LINEAR 0  /* g is the gate tensor's value                      */
+#define MOE_GATE_SIGMOID 1 /* g is 1 / (1 + exp(-value))                        */
+
+typedef struct {
+  int hidden_size;          /* H: 1 .. 16384                                  */
+  moe_dtype act_dtype;      /* y, gate, h                                     */
+  moe_dtype residual_dtype; /* x, x_out                                       */
+  int kind;                 /* MOE_NORM_*                                     */
+  int post_norm;            /* 1: y is normed before it joins the residual    */
+  int gate;                 /* MOE_GATE_*                                     */
+  float residual_scale;     /* finite                                         */
+  float weight_offset;      /* finite; 1 for weights stored less one          */
+  float eps;                /* > 0                                            */
+} moe_norm_config;
+
+/* moe_norm: T rows (tokens, or heads of tokens), up to 2^24.
+ *   y      [T, H], nullable: no block before; then post_w, post_b, gate and
+ *          x_out are NULL and r = x
+ *   x      [T, H] residual_dtype. y and x take a row stride in elements.
+ *   post_w, post_b, pre_w, pre_b  [H] fp32, nullable (1 and 0)
+ *   gate   nullable; value of (t, c) at gate[t * gate_token_stride +
+ *          c * gate_channel_stride], channel stride 0 or 1: one per channel
+ *          (0, 1), per token (1, 0) or per element (H, 1)
+ *   x_out  [T, H] out, r in residual_dtype, nullable; may be x where that is
+ *          contiguous
+ *   h      [T, H] out, nullable (not both); may be y where that is contiguous
+ * ws: NULL, or >= 4 bytes for the status word (no flag is set here). */
+MOE_API int moe_validate_norm_config(const moe_norm_config* cfg);
+MOE_API int moe_norm(const moe_norm_config* cfg, int T, const void* y, int64_t y_stride,
+                     const void* x, int64_t x_stride, const float* post_w, const float* post_b,
+                     const void* gate, int64_t gate_token_stride, int64_t gate_channel_stride,
+                     const float* pre_w, const float* pre_b, void* x_out, void* h, void* ws,
+                     size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Synchronises `stream` and reads the device status word at the start of
