@@ -24,8 +24,8 @@ LIB_DEBUG = os.path.join(PKG, "libmoe_debug.so")
 
 SOURCES = ["moe_api.cu", "kernels_gemm.cu", "kernels_gemm_pair.cu", "kernels_mlp_fused.cu",
            "kernels_route.cu", "kernels_align.cu", "attn_api.cu", "kernels_rope.cu",
-           "kernels_attn.cu", "kernels_attn_prompt.cu", "serve_api.cu", "kernels_pool.cu",
-           "kernels_norm.cu"]
+           "kernels_attn.cu", "kernels_attn_prompt.cu", "kernels_attn_shared.cu", "serve_api.cu",
+           "kernels_pool.cu", "kernels_norm.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "launch.cuh", "align_block.cuh", "topk_warp.cuh", "act.cuh",
            "dbg.cuh", "attn.h", "kv4.cuh",
            "attn_dev.cuh", "attn_split.cuh", "attn_prompt.cuh", "serve.h"]

@@ -200,6 +200,9 @@ _SIGS = {
     "moe_kv_attention_workspace_size": (_SZ, [_ACFG, _I, _I, _I]),
     "moe_kv_attention": (_I, [_ACFG, _I, _I, _I] + _ROWS + [_VP] * 3 + [_I, _VP, _I64] +
                          [_VP, _VP, _VP, _SZ, _VP]),
+    "moe_kv_attention_shared_workspace_size": (_SZ, [_ACFG] + [_I] * 5),
+    "moe_kv_attention_shared": (_I, [_ACFG] + [_I] * 5 + _ROWS + [_VP] * 3 + [_I] + [_VP] * 3 +
+                                [_I64] + [_VP, _VP, _VP, _SZ, _VP]),
     "moe_kv_pool_workspace_size": (_SZ, [_ACFG, _POOL, _I]),
     "moe_kv_fork": (_I, [_ACFG, _POOL, _I] + [_VP] * 4 + [_SZ, _VP]),
     "moe_kv_reserve": (_I, [_ACFG, _POOL, _I] + [_VP] * 4 + [_SZ, _VP]),
@@ -532,6 +535,28 @@ def moe_kv_attention(cfg, num_seqs, T, max_q_len, q, q_offsets, seq_lens, page_t
         *_cache(cache, cfg), _typed("out", out, cfg.act_dtype, (T, cfg.num_heads, cfg.head_dim)),
         _typed("lse", lse, "f32", (T, cfg.num_heads)), _p(ws), _nbytes(ws),
         _stream(stream)))
+
+
+def kv_attention_shared_workspace_size(cfg, num_seqs, T, max_q_len, num_groups,
+                                       max_group_len) -> int:
+    return lib().moe_kv_attention_shared_workspace_size(ctypes.byref(cfg), num_seqs, T, max_q_len,
+                                                        num_groups, max_group_len)
+
+
+def moe_kv_attention_shared(cfg, num_seqs, T, max_q_len, num_groups, max_group_len, q, q_offsets,
+                            seq_lens, page_table, group_offsets, prefix_lens, cache, out, lse, ws,
+                            stream=None):
+    max_pages = page_table.shape[-1]
+    _check("moe_kv_attention_shared", lib().moe_kv_attention_shared(
+        ctypes.byref(cfg), num_seqs, T, max_q_len, num_groups, max_group_len,
+        *_rows("q", q, cfg, T, cfg.num_heads),
+        _typed("q_offsets", q_offsets, "i32", (num_seqs + 1,)),
+        _typed("seq_lens", seq_lens, "i32", (num_seqs,)),
+        _typed("page_table", page_table, "i32", (num_seqs, max_pages)), max_pages,
+        _typed("group_offsets", group_offsets, "i32", (num_groups + 1,)),
+        _typed("prefix_lens", prefix_lens, "i32", (num_groups,)), *_cache(cache, cfg),
+        _typed("out", out, cfg.act_dtype, (T, cfg.num_heads, cfg.head_dim)),
+        _typed("lse", lse, "f32", (T, cfg.num_heads)), _p(ws), _nbytes(ws), _stream(stream)))
 
 
 # --------------------------------------------------------------- shared pages

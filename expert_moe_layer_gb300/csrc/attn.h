@@ -83,12 +83,57 @@ struct SeqInfo {
   int q0, q_len, len, first_key;
 };
 
+// What a kernel computes: a request's whole attention; a group's rows over the
+// prefix that its requests share (all keys seen, sums left in fp32); or a
+// request's own keys behind that prefix, to which those sums are added.
+enum AttnPart { kWhole = 0, kPrefix = 1, kOwn = 2 };
+
+// Where a request's rows lie in the prefix kernel's list (len 0: no prefix).
+struct OwnPrefix {
+  long base;  // first list entry of its group
+  int tok0;   // its first query token within the group's
+  int len;    // list entries of a segment
+};
+
+// The sums over shared prefixes. Segments that one CTA took leave each row in
+// row_*, others leave pieces as the whole kernels do, which the own kernel joins.
+struct PrefixSums {
+  float2* row_stats = nullptr;  // [T * heads]
+  float4* row_sums = nullptr;   // [T * heads, D / 4]
+  const float2* stats = nullptr;
+  const float4* sums = nullptr;
+  const OwnPrefix* own = nullptr;  // [B]
+  const long* per = nullptr;       // list entries per CTA
+  int tile_rows = 0;               // of the prefix kernel
+  int chunk = 0;                   // float4s from a row's four channels to its next four
+  int lo = 0, hi = 0;              // a segment's CTAs: (begin + lo) / per .. (end - hi) / per
+};
+template <int kPart>
+struct PartArgs {
+  PrefixSums p;
+};
+template <>
+struct PartArgs<kWhole> {};
+
 // Rows of a row tile of the prompt kernel (query tokens times heads of a
 // group), and the rows per request it is used from (uses_prompt_kernel has the
 // times of both sides).
 constexpr int prompt_tile(int head_dim) { return head_dim == 256 ? 128 : 256; }
 constexpr int kPromptRows = 64;
 cudaError_t launch_prompt(const AttnArgs& a, void* ws, const AttnLayout& L, cudaStream_t st);
+
+// Rows per request from which a call does not share (shares_prefix).
+constexpr int kSharedRows = 128;
+bool shares_prefix(const moe_attn_config* c, int max_q, int groups);
+struct SharedLayout {
+  size_t status, per, counters, info, own, starts, limit, first, groups, bases, firsts, row_tiles,
+      row_starts, stats, partial, prefix_stats, prefix_partial, row_stats, row_sums, total;
+};
+SharedLayout shared_layout(const moe_attn_config* c, int B, int T, int groups, int max_group);
+cudaError_t launch_kv_attention_shared(const moe_attn_config* c, const AttnArgs& a, int groups,
+                                       const int32_t* group_offsets, const int32_t* prefix_lens,
+                                       int max_group, void* ws, const SharedLayout& L,
+                                       cudaStream_t st);
 
 cudaError_t launch_kv_attention(const moe_attn_config* c, const AttnArgs& a, void* ws,
                                 const AttnLayout& L, cudaStream_t st);

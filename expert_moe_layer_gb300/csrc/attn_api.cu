@@ -290,14 +290,13 @@ size_t moe_kv_attention_workspace_size(const moe_attn_config* cfg, int num_seqs,
   return attn_layout(cfg, num_seqs, T, max_q_len).total;
 }
 
-int moe_kv_attention(const moe_attn_config* cfg, int num_seqs, int T, int max_q_len,
-                     const void* q, int64_t q_token_stride, int64_t q_head_stride,
-                     const int32_t* q_offsets, const int32_t* seq_lens,
-                     const int32_t* page_table, int max_pages, const void* cache,
-                     int64_t num_pages, void* out, float* lse, void* ws, size_t ws_bytes,
-                     void* stream) {
-  MOE_TRY(validate_attention(cfg, num_seqs, T, max_q_len));
-  if (T == 0) return MOE_OK;
+// What moe_kv_attention and moe_kv_attention_shared are handed alike, checked;
+// the workspace aside.
+static int attention_args(const moe_attn_config* cfg, int num_seqs, int T, int max_q_len,
+                          const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                          const int32_t* q_offsets, const int32_t* seq_lens,
+                          const int32_t* page_table, int max_pages, const void* cache,
+                          int64_t num_pages, void* out, float* lse, AttnArgs* args) {
   const int eb = ebytes(cfg);
   MOE_TRY(validate_rows(cfg, q, q_token_stride, q_head_stride, cfg->num_heads));
   if (!aligned(q, 16) || q_token_stride * eb % 16 != 0 || q_head_stride * eb % 16 != 0)
@@ -309,12 +308,7 @@ int moe_kv_attention(const moe_attn_config* cfg, int num_seqs, int T, int max_q_
       !aligned(page_table, 4) || !aligned(q_offsets, 4) || !aligned(lse, 4))
     return MOE_ERR_INVALID_ARG;
   MOE_TRY(validate_cache(cache, num_pages));
-  const AttnLayout L = attn_layout(cfg, num_seqs, T, max_q_len);
-  if (!ws || ws_bytes < L.total || !aligned(ws, 16)) return MOE_ERR_WORKSPACE;
-  AttnArgs a;
-  a.sms = sm_count();
-  if (a.sms < 1) return MOE_ERR_CUDA;
-  if (a.sms > kAttnMaxSms) a.sms = kAttnMaxSms;
+  AttnArgs& a = *args;
   a.B = num_seqs, a.T = T, a.max_q = max_q_len;
   a.heads = cfg->num_heads, a.kv_heads = cfg->num_kv_heads;
   a.D = cfg->head_dim, a.page_size = cfg->page_size;
@@ -332,7 +326,76 @@ int moe_kv_attention(const moe_attn_config* cfg, int num_seqs, int T, int max_q_
   a.max_pages = max_pages;
   a.cache = static_cast<const uint8_t*>(cache), a.num_pages = static_cast<long>(num_pages);
   a.out = out, a.lse = lse;
+  return MOE_OK;
+}
+
+static int attention_sms(AttnArgs* a) {
+  a->sms = sm_count();
+  if (a->sms < 1) return MOE_ERR_CUDA;
+  if (a->sms > kAttnMaxSms) a->sms = kAttnMaxSms;
+  return MOE_OK;
+}
+
+int moe_kv_attention(const moe_attn_config* cfg, int num_seqs, int T, int max_q_len,
+                     const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                     const int32_t* q_offsets, const int32_t* seq_lens,
+                     const int32_t* page_table, int max_pages, const void* cache,
+                     int64_t num_pages, void* out, float* lse, void* ws, size_t ws_bytes,
+                     void* stream) {
+  MOE_TRY(validate_attention(cfg, num_seqs, T, max_q_len));
+  if (T == 0) return MOE_OK;
+  AttnArgs a;
+  MOE_TRY(attention_args(cfg, num_seqs, T, max_q_len, q, q_token_stride, q_head_stride, q_offsets,
+                         seq_lens, page_table, max_pages, cache, num_pages, out, lse, &a));
+  const AttnLayout L = attn_layout(cfg, num_seqs, T, max_q_len);
+  if (!ws || ws_bytes < L.total || !aligned(ws, 16)) return MOE_ERR_WORKSPACE;
+  MOE_TRY(attention_sms(&a));
   return cuda_ok(launch_kv_attention(cfg, a, ws, L, static_cast<cudaStream_t>(stream)));
+}
+
+static int validate_groups(int num_groups, int max_group_len) {
+  return num_groups < 0 || num_groups > kMaxT || max_group_len < 0 ? MOE_ERR_INVALID_ARG : MOE_OK;
+}
+
+size_t moe_kv_attention_shared_workspace_size(const moe_attn_config* cfg, int num_seqs, int T,
+                                              int max_q_len, int num_groups, int max_group_len) {
+  if (validate_attention(cfg, num_seqs, T, max_q_len) != MOE_OK ||
+      validate_groups(num_groups, max_group_len) != MOE_OK)
+    return 0;
+  return shares_prefix(cfg, max_q_len, num_groups)
+             ? shared_layout(cfg, num_seqs, T, num_groups, max_group_len).total
+             : attn_layout(cfg, num_seqs, T, max_q_len).total;
+}
+
+int moe_kv_attention_shared(const moe_attn_config* cfg, int num_seqs, int T, int max_q_len,
+                            int num_groups, int max_group_len, const void* q,
+                            int64_t q_token_stride, int64_t q_head_stride,
+                            const int32_t* q_offsets, const int32_t* seq_lens,
+                            const int32_t* page_table, int max_pages,
+                            const int32_t* group_offsets, const int32_t* prefix_lens,
+                            const void* cache, int64_t num_pages, void* out, float* lse, void* ws,
+                            size_t ws_bytes, void* stream) {
+  MOE_TRY(validate_attention(cfg, num_seqs, T, max_q_len));
+  MOE_TRY(validate_groups(num_groups, max_group_len));
+  if (T == 0) return MOE_OK;
+  AttnArgs a;
+  MOE_TRY(attention_args(cfg, num_seqs, T, max_q_len, q, q_token_stride, q_head_stride, q_offsets,
+                         seq_lens, page_table, max_pages, cache, num_pages, out, lse, &a));
+  if (num_groups > 0 && (!group_offsets || !prefix_lens || !aligned(group_offsets, 4) ||
+                         !aligned(prefix_lens, 4) || max_group_len < 1))
+    return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!shares_prefix(cfg, max_q_len, num_groups)) {
+    const AttnLayout L = attn_layout(cfg, num_seqs, T, max_q_len);
+    if (!ws || ws_bytes < L.total || !aligned(ws, 16)) return MOE_ERR_WORKSPACE;
+    MOE_TRY(attention_sms(&a));
+    return cuda_ok(launch_kv_attention(cfg, a, ws, L, st));
+  }
+  const SharedLayout L = shared_layout(cfg, num_seqs, T, num_groups, max_group_len);
+  if (!ws || ws_bytes < L.total || !aligned(ws, 16)) return MOE_ERR_WORKSPACE;
+  MOE_TRY(attention_sms(&a));
+  return cuda_ok(launch_kv_attention_shared(cfg, a, num_groups, group_offsets, prefix_lens,
+                                            max_group_len, ws, L, st));
 }
 
 }  // extern "C"

@@ -315,7 +315,7 @@ struct Piece {
 // Walks a CTA's range of the list, whose cuts move to a segment's ends where
 // those are near (kSnap < kMinTiles, so that no two cuts move to the same end).
 // Every warp keeps one.
-template <int D>
+template <int D, int kPart>
 struct Cursor {
   using H = Shape<D>;
   long at, end, per, total;
@@ -352,6 +352,7 @@ struct Cursor {
       const int before = p.sq.len - p.sq.q_len;
       p.lo = a.window > 0 ? max(0, before + p.row0 / group - a.window + 1) : 0;
       p.hi = before + last / group + 1;
+      if constexpr (kPart == kPrefix) p.lo = 0, p.hi = p.sq.len;
       const int tiles = p.hi <= 0 ? 0 : (p.hi + H::kKeys - 1) / H::kKeys - p.lo / H::kKeys;
       const int len = kSetup + tiles;
       p.kvh = static_cast<int>((at - starts[r]) / len);
@@ -378,11 +379,13 @@ struct Cursor {
   }
 };
 
-template <int D>
+// kPart kPrefix: a request is a group of requests, its first_key names the row of
+// the page table, every row sees all keys, and sums are left in fp32.
+template <int D, int kPart = kWhole>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_prompt_kernel(AttnArgs a, unsigned* status, int* counters, const SeqInfo* info,
                        const int* firsts, const RowTile* row_tiles, const long* starts,
-                       float2* stats, float4* partial) {
+                       float2* stats, float4* partial, PartArgs<kPart> part) {
   using H = Shape<D>;
   constexpr int kKeys = H::kKeys;
   extern __shared__ uint8_t smem_raw[];
@@ -433,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait_warp = [&](const uint64_t& b, uint32_t parity) {
     return __all_sync(~0u, wait(b, parity)) != 0;
   };
-  Cursor<D> cur;
+  Cursor<D, kPart> cur;
   Piece t;
   auto begin = [&] { cur.begin(starts, firsts[a.B], lane); };
   auto next = [&] { return cur.next(a, info, row_tiles, starts, t); };
@@ -555,12 +558,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool more = x < H::kHalves && advance();
     if (more) load_queries();
     while (more) {
-      const int p = t.sq.len - t.sq.q_len + tok;
+      const int p = kPart == kPrefix ? t.sq.len - 1 : t.sq.len - t.sq.q_len + tok;
       const int last = live ? p : 0x7ffffff0;  // (one more is added below)
       const int first = live && a.window > 0 ? p - a.window + 1 : 0;
       // keys that every row of the half sees
       const int r_lo = t.row0 + x * kHalf, r_hi = min(t.rows, r_lo + kHalf) - 1;
-      const int all_last = t.sq.len - t.sq.q_len + r_lo / group;
+      const int all_last = kPart == kPrefix ? t.sq.len - 1 : t.sq.len - t.sq.q_len + r_lo / group;
       const int all_first = a.window > 0 ? t.sq.len - t.sq.q_len + r_hi / group - a.window + 1 : 0;
       const bool frees = x == t.halves - 1 && threadIdx.x % 128 == 0;
       float m = -INFINITY, mbase = -kLift;  // m: a whole number
@@ -683,7 +686,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         unpair_f32(add_f32x2(l2[0], l2[1]), l0, l1);
         l = l0 + l1;
       }
-      if (alone) {
+      if constexpr (kPart == kPrefix) {
+        if (alone) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            tmem_ld32(to + 32 * c, v);
+            tmem_landed(v);
+            if (there)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                part.p.row_sums[at_row * (D / 4) + 8 * c + i] =
+                    make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+          }
+          if (there)
+            part.p.row_stats[at_row] = make_float2(m == -INFINITY ? -INFINITY : mbase, l);
+          ptx::tc_fence_before();
+          continue;
+        }
+      } else if (alone) {
         const float f = out_factor(l, a.v_scale);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -716,6 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         stats[slot * kHalf + row_l] = make_float2(m == -INFINITY ? -INFINITY : mbase, l);
       }
       ptx::tc_fence_before();
+      if constexpr (kPart == kPrefix) continue;  // the own kernel joins them
       __threadfence();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(bars.written[x]));
@@ -796,7 +819,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t kc = 0;
     begin();
     while (next()) {
-      const int32_t* pages = a.page_table + static_cast<long>(t.b) * a.max_pages;
+      const int32_t* pages =
+          a.page_table + static_cast<long>(kPart == kPrefix ? t.sq.first_key : t.b) * a.max_pages;
       // The page of eight keys from `key` (0 where no row sees one of them).
       auto page_of = [&](int key) {
         return key < t.hi && key + 7 >= t.lo ? pages[key >> page_shift] : 0;

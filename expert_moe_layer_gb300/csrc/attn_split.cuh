@@ -208,6 +208,56 @@ __device__ __forceinline__ void load_values(ValueRegs<D>& t, const uint8_t* stag
   }
 }
 
+// Four channels of a row's sums over the shared prefix, its pieces in CTA order,
+// added to the row's own. `at` is the row within the group, `c` its chunk.
+__device__ __forceinline__ void add_pieces(const PrefixSums& p, const OwnPrefix& own, int at,
+                                           int kvh, int kv_heads, long at_row, int chunks, int c,
+                                           float4& sum, float& top, float& den) {
+  constexpr int kBatch = 8;  // pieces asked for together
+  const long per = *p.per;
+  const int tile = at / p.tile_rows, r = at - tile * p.tile_rows;
+  const long seg = own.base + (static_cast<long>(tile) * kv_heads + kvh) * own.len;
+  const long cta0 = (seg + p.lo) / per, cta1 = max(cta0, (seg + own.len - p.hi) / per);
+  const int n = static_cast<int>(cta1 - cta0) + 1;
+  const float2* stat = p.row_stats + at_row;
+  const float4* v0 = p.row_sums + at_row * chunks + c;
+  long rows = 0, slot = 0;  // of a slot; every CTA has two, the first one's piece is in the second
+  if (n > 1) {
+    rows = p.tile_rows;
+    slot = rows * chunks;
+    stat = p.stats + 2 * cta0 * rows + r;
+    v0 = p.sums + 2 * cta0 * slot + c * p.chunk +
+         (p.chunk == 1 ? r * chunks : (r / p.chunk) * p.chunk * chunks + r % p.chunk);
+  }
+  for (int k0 = 0; k0 < n; k0 += kBatch) {
+    float2 st[kBatch];
+    float4 v[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int k = k0 + i;
+      st[i] = make_float2(-INFINITY, 0.0f);
+      v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (k < n) {
+        const long at_slot = 2l * k + (k == 0);
+        st[i] = __ldcg(stat + at_slot * rows);
+        v[i] = __ldcg(v0 + at_slot * slot);
+      }
+    }
+    float most = top;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) most = fmaxf(most, st[i].x);
+    const float f = top == -INFINITY ? 0.0f : ex2(top - most);
+    den *= f, sum.x *= f, sum.y *= f, sum.z *= f, sum.w *= f;
+    top = most;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float g = st[i].x == -INFINITY ? 0.0f : ex2(st[i].x - most);
+      den += g * st[i].y;
+      sum.x += g * v[i].x, sum.y += g * v[i].y, sum.z += g * v[i].z, sum.w += g * v[i].w;
+    }
+  }
+}
+
 template <int D, int kRows>
 __host__ __device__ constexpr int split_smem() {
   constexpr int stages = kWarps * kStages * TileBytes<D>::kTileBytes, sums = kWarps * kRows * D * 4;
@@ -239,10 +289,15 @@ __host__ __device__ constexpr int ctas_per_sm() {
 // own accumulation truncates. (All D channels of both terms in one accumulator
 // lost up to 18.4 * 2^-23 of a score at 256 channels, now 4.6; the additions cost
 // 8 requests of 8 to 16 thousand tokens 39.6 us instead of 39.1, with 128 channels.)
-template <typename T, int D, int kRows, int kTerms, bool kInline>
+//
+// kPart kPrefix: a request is a group of requests here, its first_key names the
+// row of the page table. kOwn: lists of the kernel two places before, so that it
+// waits for the prefix kernel as late as a kInline one for the clearing kernel.
+template <typename T, int D, int kRows, int kTerms, bool kInline, int kPart = kWhole>
 __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
     attn_split_kernel(AttnArgs a, unsigned* status, int* counters, const SeqInfo* info_in,
-                      const long* starts_in, float* stats, float* partial, int page_shift) {
+                      const long* starts_in, float* stats, float* partial, int page_shift,
+                      PartArgs<kPart> part) {
   constexpr bool kBoth = kRows == 4;             // columns 4-7 repeat rows 0-3
   constexpr int NT = kBoth ? 1 : kRows / 8;      // column tiles of the scores
   constexpr int NP = kBoth ? 1 : 2 * NT;         // column tiles of the sums
@@ -257,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
   // The kernel before this one only clears status and counters, which are not
   // touched before the first segment's join: everything else that is read was
   // written before that kernel began, and the wait for it comes that late.
-  bool entered = !kInline;
+  bool entered = !kInline && kPart != kOwn;
   unsigned flags = 0;
   if constexpr (kInline) {
     __shared__ SeqInfo s_info[kInlineSeqs];
@@ -267,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
     __syncthreads();
     info = s_info;
     starts = s_starts;
-  } else {
+  } else if (kPart != kOwn) {
     pdl_enter();
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -295,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
   int row_tile = 0, kvh = 0;
   while (at < end) {
     const SeqInfo sq = info[b];
-    const int first_tile = sq.first_key / kTile;
+    const int first_tile = kPart == kPrefix ? 0 : sq.first_key / kTile;
     const int rows = sq.q_len * group;
     const int per_seg = kSetup + max(0, (sq.len + kTile - 1) / kTile - first_tile);
     if (seg_start < 0) {
@@ -323,13 +378,17 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
       for (int j = 0; j < 2; ++j) {
         const int r = row0 + nt * 8 + (kBoth ? (2 * c + j) & 3 : 2 * c + j);
         // padding rows (zero queries whose columns are never written) see all
-        const int p = sq.len - sq.q_len + token_of(r);
+        const int p = kPart == kPrefix ? sq.len - 1 : sq.len - sq.q_len + token_of(r);
         last[nt][j] = r < rows ? p : 0x7fffffff;
         first[nt][j] = r < rows && a.window > 0 ? max(0, p - a.window + 1) : 0;
       }
     {
       const int r_end = min(rows, row0 + kRows) - 1;
-      const int pos0 = sq.len - sq.q_len + token_of(row0), pos1 = sq.len - sq.q_len + token_of(r_end);
+      int pos0 = sq.len - 1, pos1 = sq.len - 1;
+      if constexpr (kPart != kPrefix) {
+        pos0 = sq.len - sq.q_len + token_of(row0);
+        pos1 = sq.len - sq.q_len + token_of(r_end);
+      }
       tile_last = pos1;
       tile_first = a.window > 0 ? max(0, pos0 - a.window + 1) : 0;
       // tokens that every row of the tile sees
@@ -340,7 +399,8 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
     // tiles of this row tile that hold a visible token
     const int tA = max(t0, tile_first / kTile - first_tile);
     const int tB = min(t1, tile_last < 0 ? 0 : tile_last / kTile + 1 - first_tile);
-    const int32_t* pages = a.page_table + static_cast<long>(b) * a.max_pages;
+    const int32_t* pages =
+        a.page_table + static_cast<long>(kPart == kPrefix ? sq.first_key : b) * a.max_pages;
     // The CTA's warps take the tiles of the range in turn. Each keeps a ring of
     // kStages tiles: the copies run kStages - 1 tiles ahead, the page ids one
     // more. The two sub-tiles may lie on two pages.
@@ -693,6 +753,17 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
     auto finish = [&](int r, int ch, float4 sum, float top, float den) {
       const int tok = token_of(row0 + r), h = kvh * group + (row0 + r) - tok * group;
       const long at_row = static_cast<long>(sq.q0 + tok) * a.heads + h;
+      if constexpr (kPart == kPrefix) {
+        part.p.row_sums[at_row * (D / 4) + ch / 4] = sum;
+        if (ch == 0) part.p.row_stats[at_row] = make_float2(top, den);
+        return;
+      }
+      if constexpr (kPart == kOwn) {
+        const OwnPrefix own = part.p.own[b];
+        if (own.len > 0)
+          add_pieces(part.p, own, own.tok0 * group + row0 + r, kvh, a.kv_heads, at_row, D / 4,
+                     ch / 4, sum, top, den);
+      }
       const float f = out_factor(den, a.v_scale);
       store4(static_cast<T*>(a.out) + at_row * D + ch,
              make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f));
@@ -726,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
         }
       }
     }
-    if (!alone) {
+    if (kPart != kPrefix && !alone) {
       const int cta0 = static_cast<int>((seg_start + kSetup - 1) / per);
       const int cta1 = static_cast<int>((seg_end - 1) / per);
       __threadfence();

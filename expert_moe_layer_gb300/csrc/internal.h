@@ -264,6 +264,7 @@ cudaError_t launch_combine(bool bf16, const void* y_perm, int cap, const int32_t
 cudaError_t set_wait_limit_gemm(unsigned long long ns);
 cudaError_t set_wait_limit_gemm_pair(unsigned long long ns);
 cudaError_t set_wait_limit_attn(unsigned long long ns);
+cudaError_t set_wait_limit_attn_shared(unsigned long long ns);
 cudaError_t set_wait_limit_mlp_fused(unsigned long long ns);
 cudaError_t set_wait_limit_route(unsigned long long ns);
 cudaError_t set_wait_limit_align(unsigned long long ns);

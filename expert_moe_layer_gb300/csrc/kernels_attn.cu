@@ -34,7 +34,7 @@ cudaError_t launch_split_as(const AttnArgs& a, void* ws, const AttnLayout& L, cu
   return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, a, status, counters,
                     const_cast<const SeqInfo*>(info), const_cast<const long*>(starts),
                     reinterpret_cast<float*>(w + L.stats), reinterpret_cast<float*>(w + L.partial),
-                    log2);
+                    log2, PartArgs<kWhole>());
 }
 template <typename T, int D, int kRows, int kTerms>
 cudaError_t launch_split(const AttnArgs& a, void* ws, const AttnLayout& L, cudaStream_t st) {

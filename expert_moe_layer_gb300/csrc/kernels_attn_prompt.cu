@@ -38,7 +38,7 @@ cudaError_t launch_dim(const AttnArgs& a, void* ws, const AttnLayout& L, cudaStr
                     status, counters, const_cast<const SeqInfo*>(info),
                     const_cast<const int*>(firsts), const_cast<const RowTile*>(row_tiles),
                     const_cast<const long*>(starts), reinterpret_cast<float2*>(w + L.stats),
-                    reinterpret_cast<float4*>(w + L.partial));
+                    reinterpret_cast<float4*>(w + L.partial), PartArgs<kWhole>());
 }
 
 }  // namespace

@@ -649,6 +649,39 @@ MOE_API int moe_kv_attention(const moe_attn_config* cfg, int num_seqs, int T, in
                              int64_t num_pages, void* out, float* lse, void* ws,
                              size_t ws_bytes, void* stream);
 
+/* moe_kv_attention_shared: moe_kv_attention for requests whose first tokens are
+ * the same (samples of one prompt, questions on one document). The results are
+ * those of moe_kv_attention, with sums in another order; a prefix is read once
+ * for all requests of its group, not once for each.
+ *   group_offsets [num_groups + 1] int32: group g is the requests
+ *     group_offsets[g] .. group_offsets[g+1] - 1; requests outside every group
+ *     have no shared prefix
+ *   prefix_lens [num_groups] int32: the first prefix_lens[g] cached tokens of the
+ *     group's requests are the same. They are read from the pages of its first
+ *     request that has queries (the others hold the same pages, or copies). What
+ *     reaches past the tokens that every request with queries has before them is
+ *     not taken as shared.
+ *   max_group_len: at least the most query tokens of a group
+ * The other arguments and flags are those of moe_kv_attention. MOE_DEV_BAD_SEGMENT
+ * is also set, and nothing shared, for group_offsets that decrease or leave
+ * [0, num_seqs], a prefix below 0, or a group of more than max_group_len query
+ * tokens (of that group): results are right all the same. With a window, or from
+ * 128 rows per request (max_q_len times the heads of a group, bf16), the call is
+ * moe_kv_attention and does not look at the groups. num_groups may be up to 2^18.
+ * ws: moe_kv_attention_shared_workspace_size(...) bytes (0: invalid); it has room
+ * for T * num_heads * head_dim fp32 sums. */
+MOE_API size_t moe_kv_attention_shared_workspace_size(const moe_attn_config* cfg, int num_seqs,
+                                                      int T, int max_q_len, int num_groups,
+                                                      int max_group_len);
+MOE_API int moe_kv_attention_shared(const moe_attn_config* cfg, int num_seqs, int T, int max_q_len,
+                                    int num_groups, int max_group_len, const void* q,
+                                    int64_t q_token_stride, int64_t q_head_stride,
+                                    const int32_t* q_offsets, const int32_t* seq_lens,
+                                    const int32_t* page_table, int max_pages,
+                                    const int32_t* group_offsets, const int32_t* prefix_lens,
+                                    const void* cache, int64_t num_pages, void* out, float* lse,
+                                    void* ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------------ */
 /* Pages that several requests share. The source pages leave a cache's pages to
  * the serving engine; these entry points keep the page table, so that a batch
