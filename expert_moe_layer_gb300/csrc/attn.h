@@ -88,6 +88,19 @@ struct SeqInfo {
 // request's own keys behind that prefix, to which those sums are added.
 enum AttnPart { kWhole = 0, kPrefix = 1, kOwn = 2 };
 
+// A row tile of the prompt kernel over a prefix: its group's rows and keys (the
+// first_key names the row of the page table), its first list entry, its first row.
+struct PrefixTile {
+  SeqInfo sq;
+  long start;
+  int row0, pad;
+};
+struct PrefixHead {
+  long total, per;  // list entries over the prefixes, and entries per CTA
+  long own_per;     // the same of the own kernel
+  int own_len, pad;  // entries of every segment there; 0: as many as it has tiles
+};
+
 // Where a request's rows lie in the prefix kernel's list (len 0: no prefix).
 struct OwnPrefix {
   long base;  // first list entry of its group
@@ -103,9 +116,10 @@ struct PrefixSums {
   const float2* stats = nullptr;
   const float4* sums = nullptr;
   const OwnPrefix* own = nullptr;  // [B]
-  const long* per = nullptr;       // list entries per CTA
-  int tile_rows = 0;               // of the prefix kernel
-  int chunk = 0;                   // float4s from a row's four channels to its next four
+  const PrefixHead* head = nullptr;
+  const PrefixTile* tiles = nullptr;  // prompt kernel: the row tiles and one past them
+  const int* begins = nullptr;  // row tile, group or request that each CTA of the kernel begins in
+  int tile_rows = 0;            // of the prefix kernel
   int lo = 0, hi = 0;              // a segment's CTAs: (begin + lo) / per .. (end - hi) / per
 };
 template <int kPart>
@@ -126,8 +140,8 @@ cudaError_t launch_prompt(const AttnArgs& a, void* ws, const AttnLayout& L, cuda
 constexpr int kSharedRows = 128;
 bool shares_prefix(const moe_attn_config* c, int max_q, int groups);
 struct SharedLayout {
-  size_t status, per, counters, info, own, starts, limit, first, groups, bases, firsts, row_tiles,
-      row_starts, stats, partial, prefix_stats, prefix_partial, row_stats, row_sums, total;
+  size_t status, head, counters, own_begins, prefix_begins, info, own, starts, limit, first, groups,
+      bases, firsts, tiles, stats, partial, prefix_stats, prefix_partial, row_stats, row_sums, total;
 };
 SharedLayout shared_layout(const moe_attn_config* c, int B, int T, int groups, int max_group);
 cudaError_t launch_kv_attention_shared(const moe_attn_config* c, const AttnArgs& a, int groups,

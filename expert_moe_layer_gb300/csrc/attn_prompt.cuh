@@ -35,6 +35,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "attn_dev.cuh"
 #include "internal.h"
@@ -315,7 +316,7 @@ struct Piece {
 // Walks a CTA's range of the list, whose cuts move to a segment's ends where
 // those are near (kSnap < kMinTiles, so that no two cuts move to the same end).
 // Every warp keeps one.
-template <int D, int kPart>
+template <int D>
 struct Cursor {
   using H = Shape<D>;
   long at, end, per, total;
@@ -352,7 +353,6 @@ struct Cursor {
       const int before = p.sq.len - p.sq.q_len;
       p.lo = a.window > 0 ? max(0, before + p.row0 / group - a.window + 1) : 0;
       p.hi = before + last / group + 1;
-      if constexpr (kPart == kPrefix) p.lo = 0, p.hi = p.sq.len;
       const int tiles = p.hi <= 0 ? 0 : (p.hi + H::kKeys - 1) / H::kKeys - p.lo / H::kKeys;
       const int len = kSetup + tiles;
       p.kvh = static_cast<int>((at - starts[r]) / len);
@@ -373,6 +373,63 @@ struct Cursor {
       p.alone = p0 == 0 && p1 == len;
       p.cta0 = static_cast<int>((seg + kSnap) / per);
       p.cta1 = max(p.cta0, static_cast<int>((seg + len - kSnap - 1) / per));
+      at = seg + p1;
+      return true;
+    }
+  }
+};
+
+// The same over prefixes: all row tiles of a group have as many entries, and the
+// plan has looked up where each CTA begins. A cut in a segment's first kSetup
+// entries, which stand for no tiles, moves to its begin; near the end only one
+// tile is not cut off, since joining pieces is cheap here and a CTA with four
+// tiles more holds up the others (56 us instead of 48, 256 rows over 32768 tokens).
+constexpr int kPrefixSnap = 1;
+template <int D>
+struct PrefixCursor {
+  using H = Shape<D>;
+  long at, end, per;
+  const PrefixTile* t;
+  __device__ __forceinline__ void begin(const PrefixSums& p) {
+    const PrefixHead h = *p.head;
+    t = p.tiles + p.begins[blockIdx.x];
+    per = h.per;
+    at = blockIdx.x * per;
+    end = min(h.total, at + per);
+  }
+  __device__ __forceinline__ bool next(const AttnArgs& a, Piece& p) {
+    for (;;) {
+      if (at >= end) return false;
+      long after = t[1].start;
+      PrefixTile tile = *t;
+      while (after <= at) {
+        tile = *++t;
+        after = t[1].start;
+      }
+      p.sq = tile.sq;
+      p.row0 = tile.row0;
+      p.rows = p.sq.q_len * (a.heads / a.kv_heads);
+      p.halves = min(p.rows, p.row0 + H::kTile) > p.row0 + kHalf ? 2 : 1;
+      p.lo = 0;
+      p.hi = p.sq.len;
+      const int len = kSetup + (p.hi + H::kKeys - 1) / H::kKeys;
+      p.kvh = static_cast<int>(at - tile.start) / len;
+      const long seg = tile.start + static_cast<long>(p.kvh) * len;
+      int p0 = static_cast<int>(at - seg);
+      if (p0 <= kSetup) {
+        p0 = 0;
+      } else if (len - p0 <= kPrefixSnap) {  // the CTA before takes all of it
+        at = seg + len;
+        continue;
+      }
+      int p1 = static_cast<int>(min(static_cast<long>(len), end - seg));
+      if (p1 < len && p1 <= kSetup) return false;  // the next CTA takes all of it
+      if (len - p1 <= kPrefixSnap) p1 = len;
+      p.first = max(0, p0 - kSetup);
+      p.tiles = p1 - kSetup - p.first;
+      p.alone = p0 == 0 && p1 == len;
+      p.cta0 = static_cast<int>((seg + kSetup) / per);
+      p.cta1 = max(p.cta0, static_cast<int>((seg + len - kPrefixSnap - 1) / per));
       at = seg + p1;
       return true;
     }
@@ -436,10 +493,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait_warp = [&](const uint64_t& b, uint32_t parity) {
     return __all_sync(~0u, wait(b, parity)) != 0;
   };
-  Cursor<D, kPart> cur;
+  std::conditional_t<kPart == kPrefix, PrefixCursor<D>, Cursor<D>> cur;
   Piece t;
-  auto begin = [&] { cur.begin(starts, firsts[a.B], lane); };
-  auto next = [&] { return cur.next(a, info, row_tiles, starts, t); };
+  auto begin = [&] {
+    if constexpr (kPart == kPrefix)
+      cur.begin(part.p);
+    else
+      cur.begin(starts, firsts[a.B], lane);
+  };
+  auto next = [&] {
+    if constexpr (kPart == kPrefix)
+      return cur.next(a, t);
+    else
+      return cur.next(a, info, row_tiles, starts, t);
+  };
 
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
@@ -482,7 +549,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The warp's rows of queries, whole rows by neighbouring lanes, scaled to
     // f16; each lane keeps its own row's gain.
     auto load_queries = [&] {
-      constexpr int kRowLanes = D / 8, kRowsStep = 32 / kRowLanes, kBatch = 4;
+      // rows asked for together: over a prefix a CTA has one piece, as a rule, and
+      // its queries are what the first product waits for
+      constexpr int kRowLanes = D / 8, kRowsStep = 32 / kRowLanes;
+      constexpr int kBatch = kPart == kPrefix ? (D == 64 ? 8 : 16) : 4;
       const long src = (t.sq.q0 + (live ? tok : 0)) * a.q.token + (live ? head : 0) * a.q.head;
 #pragma unroll 1
       for (int first = 0; first < kRowLanes; first += kBatch) {
@@ -550,6 +620,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (store)
             *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D + 32 * c +
                                       16 * q + 8 * (lane & 1)) = w;
+        }
+      }
+    };
+
+    // The same of fp32 sums, eight columns at a time.
+    auto store_sums = [&](float4* dst, int c, const uint32_t* v, long row, bool there) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int flip = (lane >> 2) & 1;
+        __syncwarp();
+        sts128(stage + lane * 32 + 16 * flip, v[8 * q], v[8 * q + 1], v[8 * q + 2], v[8 * q + 3]);
+        sts128(stage + lane * 32 + 16 * (flip ^ 1), v[8 * q + 4], v[8 * q + 5], v[8 * q + 6],
+               v[8 * q + 7]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int rl = 16 * i + (lane >> 1);
+          const long at = __shfl_sync(~0u, row, rl);
+          const bool store = __shfl_sync(~0u, static_cast<int>(there), rl);
+          const uint4 w = lds128(stage + rl * 32 + 16 * ((lane & 1) ^ ((rl >> 2) & 1)));
+          if (store)
+            reinterpret_cast<uint4*>(dst)[at * (D / 4) + 8 * c + 2 * q + (lane & 1)] = w;
         }
       }
     };
@@ -687,24 +779,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         l = l0 + l1;
       }
       if constexpr (kPart == kPrefix) {
-        if (alone) {
+        // sums and statistics by row: whole segments to the rows' places, pieces
+        // to the CTA's slot (1 where the segment begins in it)
+        const long row = alone ? at_row
+                               : (2l * blockIdx.x + (blockIdx.x == cta0)) * H::kTile + x * kHalf + row_l;
+        const bool store = there || !alone;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t v[32];
-            tmem_ld32(to + 32 * c, v);
-            tmem_landed(v);
-            if (there)
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                part.p.row_sums[at_row * (D / 4) + 8 * c + i] =
-                    make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
-                                __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
-          }
-          if (there)
-            part.p.row_stats[at_row] = make_float2(m == -INFINITY ? -INFINITY : mbase, l);
-          ptx::tc_fence_before();
-          continue;
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(to + 32 * c, v);
+          tmem_landed(v);
+          store_sums(alone ? part.p.row_sums : partial, c, v, row, store);
         }
+        if (store)
+          (alone ? part.p.row_stats : stats)[row] = make_float2(m == -INFINITY ? -INFINITY : mbase, l);
+        ptx::tc_fence_before();
+        continue;
       } else if (alone) {
         const float f = out_factor(l, a.v_scale);
 #pragma unroll 1
@@ -738,7 +828,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         stats[slot * kHalf + row_l] = make_float2(m == -INFINITY ? -INFINITY : mbase, l);
       }
       ptx::tc_fence_before();
-      if constexpr (kPart == kPrefix) continue;  // the own kernel joins them
       __threadfence();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(bars.written[x]));

@@ -210,11 +210,10 @@ __device__ __forceinline__ void load_values(ValueRegs<D>& t, const uint8_t* stag
 
 // Four channels of a row's sums over the shared prefix, its pieces in CTA order,
 // added to the row's own. `at` is the row within the group, `c` its chunk.
-__device__ __forceinline__ void add_pieces(const PrefixSums& p, const OwnPrefix& own, int at,
-                                           int kvh, int kv_heads, long at_row, int chunks, int c,
+__device__ __forceinline__ void add_pieces(const PrefixSums& p, long per, const OwnPrefix& own,
+                                           int at, int kvh, int kv_heads, long at_row, int chunks, int c,
                                            float4& sum, float& top, float& den) {
   constexpr int kBatch = 8;  // pieces asked for together
-  const long per = *p.per;
   const int tile = at / p.tile_rows, r = at - tile * p.tile_rows;
   const long seg = own.base + (static_cast<long>(tile) * kv_heads + kvh) * own.len;
   const long cta0 = (seg + p.lo) / per, cta1 = max(cta0, (seg + own.len - p.hi) / per);
@@ -226,8 +225,7 @@ __device__ __forceinline__ void add_pieces(const PrefixSums& p, const OwnPrefix&
     rows = p.tile_rows;
     slot = rows * chunks;
     stat = p.stats + 2 * cta0 * rows + r;
-    v0 = p.sums + 2 * cta0 * slot + c * p.chunk +
-         (p.chunk == 1 ? r * chunks : (r / p.chunk) * p.chunk * chunks + r % p.chunk);
+    v0 = p.sums + 2 * cta0 * slot + r * chunks + c;
   }
   for (int k0 = 0; k0 < n; k0 += kBatch) {
     float2 st[kBatch];
@@ -329,14 +327,27 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
   const int g = lane >> 2, c = lane & 3;
   const int group = a.heads / a.kv_heads;
   const KvBlock blk = kv_block(a.page_size, D);
-  const long total = starts[a.B];
-  const long per = range_len(total, gridDim.x);
+  long total, per;
+  int same_len = 0;  // kOwn: list entries of every segment, or 0
+  if constexpr (kPart == kPrefix) {
+    total = part.p.head->total;
+    per = part.p.head->per;
+  } else if constexpr (kPart == kOwn) {
+    total = starts[a.B];
+    per = part.p.head->own_per;
+    same_len = part.p.head->own_len;
+  } else {
+    total = starts[a.B];
+    per = range_len(total, gridDim.x);
+  }
   long at = blockIdx.x * per;
   const long end = min(total, at + per);
   // the request of the first tile: the last b with starts[b] <= at (requests
   // without query rows have no tiles and share their start with the next)
   int b = 0;
-  {
+  if constexpr (kPart != kWhole) {
+    b = part.p.begins[blockIdx.x];
+  } else {
     int lo = 0, hi = a.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
@@ -352,7 +363,8 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
     const SeqInfo sq = info[b];
     const int first_tile = kPart == kPrefix ? 0 : sq.first_key / kTile;
     const int rows = sq.q_len * group;
-    const int per_seg = kSetup + max(0, (sq.len + kTile - 1) / kTile - first_tile);
+    int per_seg = kSetup + max(0, (sq.len + kTile - 1) / kTile - first_tile);
+    if (kPart == kOwn && same_len > 0) per_seg = same_len;
     if (seg_start < 0) {
       const long seg = (at - starts[b]) / per_seg;
       seg_start = starts[b] + seg * per_seg;
@@ -368,6 +380,12 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
     const int t0 = max(0, p0 - kSetup), t1 = p1 - kSetup;
     const int row0 = row_tile * kRows;
     auto token_of = [&](int r) { return sq.q_len == 1 ? 0 : r / group; };
+    OwnPrefix own = {0, 0, 0};
+    long prefix_per = 1;
+    if constexpr (kPart == kOwn) {
+      own = part.p.own[b];
+      prefix_per = part.p.head->per;
+    }
 
     // this lane's score columns are rows nt*8 + 2c and + 1: their token limits
     int last[NT][2], first[NT][2];
@@ -759,9 +777,8 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
         return;
       }
       if constexpr (kPart == kOwn) {
-        const OwnPrefix own = part.p.own[b];
         if (own.len > 0)
-          add_pieces(part.p, own, own.tok0 * group + row0 + r, kvh, a.kv_heads, at_row, D / 4,
+          add_pieces(part.p, prefix_per, own, own.tok0 * group + row0 + r, kvh, a.kv_heads, at_row, D / 4,
                      ch / 4, sum, top, den);
       }
       const float f = out_factor(den, a.v_scale);

@@ -99,11 +99,12 @@ __device__ __forceinline__ int used_page(const Work& w, long pages, long k) {
 template <bool kRanks>
 __device__ __forceinline__ int scan_chunk(const PoolArgs& a, const Work& w, long* warp_sum) {
   const long begin = blockIdx.x * w.chunk, end = min(begin + w.chunk, a.pages);
+  const bool wide = reinterpret_cast<uintptr_t>(a.refs) % 16 == 0;
   long found = 0;
   for (long at = begin; at < end; at += kScan) {
     const long p0 = at + threadIdx.x * kPer;
     int refs[kPer];
-    if (p0 + kPer <= end) {
+    if (wide && p0 + kPer <= end) {
 #pragma unroll
       for (int i = 0; i < kPer / 4; ++i) {
         const int4 v = reinterpret_cast<const int4*>(a.refs + p0)[i];

@@ -46,9 +46,7 @@ int validate_pool(const moe_attn_config* cfg, const moe_kv_pool* p) {
   if (p->num_rows < 1 || p->num_rows > kMaxRows || p->max_pages < 1 || p->max_pages > kMaxWidth ||
       p->caches.num_pages > kMaxPoolPages)
     return MOE_ERR_INVALID_ARG;
-  if (!ints(p->page_table) || !ints(p->held) || !p->refs || !aligned(p->refs, 16))
-    return MOE_ERR_INVALID_ARG;
-  return MOE_OK;
+  return ints(p->page_table) && ints(p->held) && ints(p->refs) ? MOE_OK : MOE_ERR_INVALID_ARG;
 }
 int validate_items(int n) { return n < 0 || n > kMaxItems ? MOE_ERR_INVALID_ARG : MOE_OK; }
 

@@ -17,7 +17,7 @@ TORCH = {"bf16": torch.bfloat16, "f32": torch.float32}
 class Pool:
     """A pool on the GPU beside its oracle."""
 
-    def __init__(self, rows, width, pages, page=16, caches=2, kv=1, dim=64, seed=0, fill=True):
+    def __init__(self, rows, width, pages, page=16, caches=2, kv=1, dim=64, seed=0, fill=True, skew=0):
         rng = np.random.default_rng(seed)
         self.cfg = B.make_attn_config(kv, kv, dim, page)
         size = page * dim * 9 // 8
@@ -28,7 +28,7 @@ class Pool:
                        [torch.zeros(pages, kv, size, dtype=torch.uint8, device="cuda") for _ in range(caches)])
         self.table = torch.full((rows, width), -1, dtype=torch.int32, device="cuda")
         self.held = torch.zeros(rows, dtype=torch.int32, device="cuda")
-        self.refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+        self.refs = torch.zeros(pages + skew, dtype=torch.int32, device="cuda")[skew:]
         self.pool = B.make_kv_pool(self.cfg, self.table, self.held, self.refs, self.caches)
         self.ws = torch.full((B.kv_pool_workspace_size(self.cfg, self.pool, 4096),), 0x5a,
                              dtype=torch.uint8, device="cuda")
@@ -101,7 +101,8 @@ def test_random_runs(pages, seed):
     rng = np.random.default_rng(100 * pages + seed)
     rows, ps = int(rng.integers(2, 40)), 16
     width = max(2, min(40, pages // 4))
-    p = Pool(rows, width, pages, ps, caches=1 if pages > 8000 else 3, kv=2 if pages < 100 else 1, seed=seed)
+    p = Pool(rows, width, pages, ps, caches=1 if pages > 8000 else 3, kv=2 if pages < 100 else 1, seed=seed,
+             skew=seed)
     # pages in use all over the pool, by no row that the calls below name
     p.o.refs[rng.random(pages) < (0.0 if pages < 10 else 0.6)] = 1
     p.load()

@@ -71,7 +71,7 @@ def _pool(rows=4, width=8, table=FAKE, held=FAKE, refs=FAKE, **kw):
 
 POOLS = [
     (dict(), 0), (dict(rows=0), 1), (dict(rows=(1 << 18) + 1), 1), (dict(width=0), 1),
-    (dict(width=(1 << 20) + 1), 1), (dict(table=None), 1), (dict(held=FAKE + 2), 1), (dict(refs=FAKE + 4), 1),
+    (dict(width=(1 << 20) + 1), 1), (dict(table=None), 1), (dict(held=FAKE + 2), 1), (dict(refs=FAKE + 4), 0), (dict(refs=FAKE + 1), 1),
     (dict(n=0), 1), (dict(n=257), 1), (dict(pages=0), 1), (dict(pages=(1 << 30) + 1), 1),
     (dict(pointer=None), 1), (dict(pointer=FAKE + 8), 1),
 ]
