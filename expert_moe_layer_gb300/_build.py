@@ -28,7 +28,8 @@ SOURCES = ["moe_api.cu", "kernels_gemm.cu", "kernels_gemm_pair.cu", "kernels_mlp
            "kernels_pool.cu", "kernels_norm.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "launch.cuh", "align_block.cuh", "topk_warp.cuh", "act.cuh",
            "dbg.cuh", "attn.h", "kv4.cuh",
-           "attn_dev.cuh", "attn_split.cuh", "attn_prompt.cuh", "serve.h"]
+           "attn_dev.cuh", "attn_groups.cuh", "attn_split.cuh",
+           "attn_prompt.cuh", "serve.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # hidden visibility: only the MOE_API entry points of include/moe.h are
 # exported, so two builds in one process share no internal symbol

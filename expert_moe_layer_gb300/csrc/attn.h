@@ -88,16 +88,24 @@ struct SeqInfo {
 // request's own keys behind that prefix, to which those sums are added.
 enum AttnPart { kWhole = 0, kPrefix = 1, kOwn = 2 };
 
-// A row tile of the prompt kernel over a prefix: its group's rows and keys (the
-// first_key names the row of the page table), its first list entry, its first row.
-struct PrefixTile {
-  SeqInfo sq;
-  long start;
-  int row0, pad;
+// Groups of requests, as the caller gives them, and the shape of the list of the
+// kernel over their prefixes.
+struct Groups {
+  int n = 0;
+  const int32_t* offsets = nullptr;  // [n + 1] requests
+  const int32_t* prefix = nullptr;   // [n] tokens
+  int max_len = 0;                   // query tokens
 };
+struct PrefixShape {
+  int tile_rows = 0, tile_keys = 0, setup = 0, min_tiles = 0, ctas = 0;
+};
+// Up to so many groups every CTA of the prefix kernel sums up the list itself, in
+// shared memory, while the plan kernel still works on the own kernel's.
+constexpr int kSmallGroups = 64;
+
 struct PrefixHead {
-  long total, per;  // list entries over the prefixes, and entries per CTA
-  long own_per;     // the same of the own kernel
+  long per;          // entries per CTA of the list over the prefixes
+  long own_per;      // and of the own kernel's
   int own_len, pad;  // entries of every segment there; 0: as many as it has tiles
 };
 
@@ -110,16 +118,21 @@ struct OwnPrefix {
 
 // The sums over shared prefixes. Segments that one CTA took leave each row in
 // row_*, others leave pieces as the whole kernels do, which the own kernel joins.
+// Sums lie in blocks of eight rows, [row / 8][D / 4][row % 8] of four channels, so
+// that a warp with a row per lane writes whole lines, and the rows of one request
+// can be read as whole sectors.
 struct PrefixSums {
   float2* row_stats = nullptr;  // [T * heads]
-  float4* row_sums = nullptr;   // [T * heads, D / 4]
+  float4* row_sums = nullptr;   // [T * heads, rounded up to 8, D / 4]
   const float2* stats = nullptr;
   const float4* sums = nullptr;
   const OwnPrefix* own = nullptr;  // [B]
   const PrefixHead* head = nullptr;
-  const PrefixTile* tiles = nullptr;  // prompt kernel: the row tiles and one past them
-  const int* begins = nullptr;  // row tile, group or request that each CTA of the kernel begins in
-  int tile_rows = 0;            // of the prefix kernel
+  const int* begins = nullptr;  // request that each CTA of the own kernel begins in
+  Groups gr;
+  PrefixShape shape;
+  const SeqInfo* groups = nullptr;  // of more than kSmallGroups: what the plan summed up
+  const long* bases = nullptr;
   int lo = 0, hi = 0;              // a segment's CTAs: (begin + lo) / per .. (end - hi) / per
 };
 template <int kPart>
@@ -140,8 +153,8 @@ cudaError_t launch_prompt(const AttnArgs& a, void* ws, const AttnLayout& L, cuda
 constexpr int kSharedRows = 128;
 bool shares_prefix(const moe_attn_config* c, int max_q, int groups);
 struct SharedLayout {
-  size_t status, head, counters, own_begins, prefix_begins, info, own, starts, limit, first, groups,
-      bases, firsts, tiles, stats, partial, prefix_stats, prefix_partial, row_stats, row_sums, total;
+  size_t status, head, counters, begins, info, own, starts, limit, first, groups, bases, stats,
+      partial, prefix_stats, prefix_partial, row_stats, row_sums, total;
 };
 SharedLayout shared_layout(const moe_attn_config* c, int B, int T, int groups, int max_group);
 cudaError_t launch_kv_attention_shared(const moe_attn_config* c, const AttnArgs& a, int groups,

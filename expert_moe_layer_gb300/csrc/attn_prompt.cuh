@@ -38,6 +38,7 @@
 #include <type_traits>
 
 #include "attn_dev.cuh"
+#include "attn_groups.cuh"
 #include "internal.h"
 #include "launch.cuh"
 #include "ptx.cuh"
@@ -379,42 +380,46 @@ struct Cursor {
   }
 };
 
-// The same over prefixes: all row tiles of a group have as many entries, and the
-// plan has looked up where each CTA begins. A cut in a segment's first kSetup
-// entries, which stand for no tiles, moves to its begin; near the end only one
-// tile is not cut off, since joining pieces is cheap here and a CTA with four
-// tiles more holds up the others (56 us instead of 48, 256 rows over 32768 tokens).
+// The same over prefixes: all segments of a group have as many entries. A cut in
+// a segment's first kSetup entries, which stand for no tiles, moves to its begin;
+// near the end only one tile is not cut off, since joining pieces is cheap here
+// and a CTA with four tiles more holds up the others (56 us instead of 48, 256
+// rows over 32768 tokens).
 constexpr int kPrefixSnap = 1;
+// Smallest range of a CTA: pieces of two tiles.
+constexpr int kMinPrefix = 2;
+static_assert(kMinPrefix > kPrefixSnap, "cuts do not cross");
 template <int D>
 struct PrefixCursor {
   using H = Shape<D>;
+  const SeqInfo* groups;
+  const long* bases;
   long at, end, per;
-  const PrefixTile* t;
-  __device__ __forceinline__ void begin(const PrefixSums& p) {
-    const PrefixHead h = *p.head;
-    t = p.tiles + p.begins[blockIdx.x];
-    per = h.per;
+  int g;
+  __device__ __forceinline__ void begin(const PrefixSums& p, const SeqInfo* groups_in,
+                                        const long* bases_in) {
+    groups = groups_in;
+    bases = bases_in;
+    const long total = bases[p.gr.n];
+    per = prefix_per(p.shape, total);
     at = blockIdx.x * per;
-    end = min(h.total, at + per);
+    end = min(total, at + per);
+    g = last_at_most(bases, p.gr.n, at);
   }
   __device__ __forceinline__ bool next(const AttnArgs& a, Piece& p) {
     for (;;) {
       if (at >= end) return false;
-      long after = t[1].start;
-      PrefixTile tile = *t;
-      while (after <= at) {
-        tile = *++t;
-        after = t[1].start;
-      }
-      p.sq = tile.sq;
-      p.row0 = tile.row0;
+      while (bases[g + 1] <= at) ++g;
+      p.sq = groups[g];
+      const int len = kSetup + (p.sq.len + H::kKeys - 1) / H::kKeys;
+      const int i = static_cast<int>(quotient(at - bases[g], len)), row_tile = i / a.kv_heads;
+      p.kvh = i - row_tile * a.kv_heads;
+      p.row0 = row_tile * H::kTile;
       p.rows = p.sq.q_len * (a.heads / a.kv_heads);
       p.halves = min(p.rows, p.row0 + H::kTile) > p.row0 + kHalf ? 2 : 1;
       p.lo = 0;
       p.hi = p.sq.len;
-      const int len = kSetup + (p.hi + H::kKeys - 1) / H::kKeys;
-      p.kvh = static_cast<int>(at - tile.start) / len;
-      const long seg = tile.start + static_cast<long>(p.kvh) * len;
+      const long seg = bases[g] + static_cast<long>(i) * len;
       int p0 = static_cast<int>(at - seg);
       if (p0 <= kSetup) {
         p0 = 0;
@@ -428,8 +433,7 @@ struct PrefixCursor {
       p.first = max(0, p0 - kSetup);
       p.tiles = p1 - kSetup - p.first;
       p.alone = p0 == 0 && p1 == len;
-      p.cta0 = static_cast<int>((seg + kSetup) / per);
-      p.cta1 = max(p.cta0, static_cast<int>((seg + len - kPrefixSnap - 1) / per));
+      p.cta0 = static_cast<int>(quotient(seg + kSetup, per));
       at = seg + p1;
       return true;
     }
@@ -482,7 +486,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(~0u, s_tmem, 0);  // (known to be uniform)
-  pdl_enter();
+  // Over prefixes every CTA sums up the list itself. What the kernel before this
+  // one, the call's plan, writes concerns the own kernel: an idle warp waits for it
+  // (behind its group's register release, which all four warps take part in).
+  const SeqInfo* groups = nullptr;
+  const long* bases = nullptr;
+  bool planned = true;
+  if constexpr (kPart == kPrefix) {
+    __shared__ GroupSmem s_groups;
+    __shared__ long s_sum[kThreads / 32];
+    groups = part.p.groups;
+    bases = part.p.bases;
+    planned = part.p.gr.n > kSmallGroups;
+    if (!planned) {
+      unsigned reported = 0;  // by the plan
+      plan_groups<kThreads>(a, part.p.gr, part.p.shape, s_groups.lists(), &s_groups, s_sum, reported,
+                            [](int, const SeqInfo&, int) {});
+      groups = s_groups.groups;
+      bases = s_groups.bases;
+    }
+  }
+  if (planned) pdl_enter();
   const int group = a.heads / a.kv_heads;
   const uint64_t limit = ptx::wait_limit();
   auto wait = [&](const uint64_t& b, uint32_t parity) {
@@ -497,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Piece t;
   auto begin = [&] {
     if constexpr (kPart == kPrefix)
-      cur.begin(part.p);
+      cur.begin(part.p, groups, bases);
     else
       cur.begin(starts, firsts[a.B], lane);
   };
@@ -620,28 +644,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (store)
             *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D + 32 * c +
                                       16 * q + 8 * (lane & 1)) = w;
-        }
-      }
-    };
-
-    // The same of fp32 sums, eight columns at a time.
-    auto store_sums = [&](float4* dst, int c, const uint32_t* v, long row, bool there) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int flip = (lane >> 2) & 1;
-        __syncwarp();
-        sts128(stage + lane * 32 + 16 * flip, v[8 * q], v[8 * q + 1], v[8 * q + 2], v[8 * q + 3]);
-        sts128(stage + lane * 32 + 16 * (flip ^ 1), v[8 * q + 4], v[8 * q + 5], v[8 * q + 6],
-               v[8 * q + 7]);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int rl = 16 * i + (lane >> 1);
-          const long at = __shfl_sync(~0u, row, rl);
-          const bool store = __shfl_sync(~0u, static_cast<int>(there), rl);
-          const uint4 w = lds128(stage + rl * 32 + 16 * ((lane & 1) ^ ((rl >> 2) & 1)));
-          if (store)
-            reinterpret_cast<uint4*>(dst)[at * (D / 4) + 8 * c + 2 * q + (lane & 1)] = w;
         }
       }
     };
@@ -784,12 +786,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long row = alone ? at_row
                                : (2l * blockIdx.x + (blockIdx.x == cta0)) * H::kTile + x * kHalf + row_l;
         const bool store = there || !alone;
+        float4* dst = (alone ? part.p.row_sums : partial) + sums_at(row, 0, D / 4);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t v[32];
           tmem_ld32(to + 32 * c, v);
           tmem_landed(v);
-          store_sums(alone ? part.p.row_sums : partial, c, v, row, store);
+          if (store)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[(8 * c + i) * 8] =
+                  make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                              __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
         }
         if (store)
           (alone ? part.p.row_stats : stats)[row] = make_float2(m == -INFINITY ? -INFINITY : mbase, l);
@@ -1062,6 +1070,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+    if (!planned && warp == kMmaWarp + 1) pdl_enter();
   }
   if (warp == kMmaWarp) {
     // -------------------------------------------------------- the matrix warp

@@ -35,6 +35,7 @@
 #include <cmath>
 
 #include "attn_dev.cuh"
+#include "attn_groups.cuh"
 #include "launch.cuh"
 #include "ptx.cuh"
 
@@ -213,19 +214,19 @@ __device__ __forceinline__ void load_values(ValueRegs<D>& t, const uint8_t* stag
 __device__ __forceinline__ void add_pieces(const PrefixSums& p, long per, const OwnPrefix& own,
                                            int at, int kvh, int kv_heads, long at_row, int chunks, int c,
                                            float4& sum, float& top, float& den) {
-  constexpr int kBatch = 8;  // pieces asked for together
-  const int tile = at / p.tile_rows, r = at - tile * p.tile_rows;
+  constexpr int kBatch = 10;  // pieces asked for together
+  const int tile = at / p.shape.tile_rows, r = at - tile * p.shape.tile_rows;
   const long seg = own.base + (static_cast<long>(tile) * kv_heads + kvh) * own.len;
-  const long cta0 = (seg + p.lo) / per, cta1 = max(cta0, (seg + own.len - p.hi) / per);
+  const long cta0 = quotient(seg + p.lo, per), cta1 = max(cta0, quotient(seg + own.len - p.hi, per));
   const int n = static_cast<int>(cta1 - cta0) + 1;
   const float2* stat = p.row_stats + at_row;
-  const float4* v0 = p.row_sums + at_row * chunks + c;
+  const float4* v0 = p.row_sums + sums_at(at_row, c, chunks);
   long rows = 0, slot = 0;  // of a slot; every CTA has two, the first one's piece is in the second
   if (n > 1) {
-    rows = p.tile_rows;
+    rows = p.shape.tile_rows;
     slot = rows * chunks;
     stat = p.stats + 2 * cta0 * rows + r;
-    v0 = p.sums + 2 * cta0 * slot + r * chunks + c;
+    v0 = p.sums + 2 * cta0 * slot + sums_at(r, c, chunks);
   }
   for (int k0 = 0; k0 < n; k0 += kBatch) {
     float2 st[kBatch];
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
   // The kernel before this one only clears status and counters, which are not
   // touched before the first segment's join: everything else that is read was
   // written before that kernel began, and the wait for it comes that late.
-  bool entered = !kInline && kPart != kOwn;
+  bool entered = !kInline && kPart == kWhole;
   unsigned flags = 0;
   if constexpr (kInline) {
     __shared__ SeqInfo s_info[kInlineSeqs];
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
     __syncthreads();
     info = s_info;
     starts = s_starts;
-  } else if (kPart != kOwn) {
+  } else if (kPart == kWhole) {
     pdl_enter();
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -330,8 +331,22 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
   long total, per;
   int same_len = 0;  // kOwn: list entries of every segment, or 0
   if constexpr (kPart == kPrefix) {
-    total = part.p.head->total;
-    per = part.p.head->per;
+    __shared__ GroupSmem s_groups;
+    __shared__ long s_sum[kWarps];
+    info = part.p.groups;
+    starts = part.p.bases;
+    if (part.p.gr.n <= kSmallGroups) {
+      unsigned reported = 0;  // by the plan
+      plan_groups<kThreads>(a, part.p.gr, part.p.shape, s_groups.lists(), &s_groups, s_sum, reported,
+                            [](int, const SeqInfo&, int) {});
+      info = s_groups.groups;
+      starts = s_groups.bases;
+    } else {
+      pdl_enter();
+      entered = true;
+    }
+    total = starts[part.p.gr.n];
+    per = prefix_per(part.p.shape, total);
   } else if constexpr (kPart == kOwn) {
     total = starts[a.B];
     per = part.p.head->own_per;
@@ -345,8 +360,10 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
   // the request of the first tile: the last b with starts[b] <= at (requests
   // without query rows have no tiles and share their start with the next)
   int b = 0;
-  if constexpr (kPart != kWhole) {
+  if constexpr (kPart == kOwn) {
     b = part.p.begins[blockIdx.x];
+  } else if constexpr (kPart == kPrefix) {
+    b = last_at_most(starts, part.p.gr.n, at);
   } else {
     int lo = 0, hi = a.B;
     while (hi - lo > 1) {
@@ -734,6 +751,10 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
       }
     }
 
+    // Sums over prefixes are read and written with rows on neighbouring lanes; four
+    // channels of a row then move within it, so that the rows use other banks.
+    constexpr bool by_rows = kPart != kWhole;
+    auto place = [](int r, int ch) { return by_rows ? ch ^ (4 * (r & 7)) : ch; };
     // join the warps: sums [row][channel] and statistics (base, l) in shared
     // memory, in the place of the stages
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -757,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
         for (int i = 0; i < D / 32; ++i)
 #pragma unroll
           for (int up = 0; up < 2; ++up) {
-            float* dst = smem + (warp * kRows + r) * D + g * (D / 8) + 4 * i + 2 * up;
+            float* dst = smem + (warp * kRows + r) * D + place(r, g * (D / 8) + 4 * i) + 2 * up;
             if constexpr (kBoth)
               dst[c >> 1] = o[i][0][2 * up + j];
             else
@@ -772,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
       const int tok = token_of(row0 + r), h = kvh * group + (row0 + r) - tok * group;
       const long at_row = static_cast<long>(sq.q0 + tok) * a.heads + h;
       if constexpr (kPart == kPrefix) {
-        part.p.row_sums[at_row * (D / 4) + ch / 4] = sum;
+        part.p.row_sums[sums_at(at_row, ch / 4, D / 4)] = sum;
         if (ch == 0) part.p.row_stats[at_row] = make_float2(top, den);
         return;
       }
@@ -790,7 +811,8 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
     // range ends inside the segment), later ones in slot 0
     const long my_slot = 2l * blockIdx.x + (p0 == 0 ? 1 : 0);
     for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
-      const int r = i / (D / 4), ch = (i % (D / 4)) * 4;
+      const int r = by_rows ? i % kRows : i / (D / 4);
+      const int ch = (by_rows ? i / kRows : i % (D / 4)) * 4;
       float top = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_stat[(w * kRows + r) * 2]);
@@ -800,14 +822,17 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
       for (int w = 0; w < kWarps; ++w) {
         const float b2 = s_stat[(w * kRows + r) * 2];
         const float f = b2 == -INFINITY ? 0.0f : ex2(b2 - top);
-        const float4 v = *reinterpret_cast<const float4*>(smem + (w * kRows + r) * D + ch);
+        const float4 v = *reinterpret_cast<const float4*>(smem + (w * kRows + r) * D + place(r, ch));
         den += f * s_stat[(w * kRows + r) * 2 + 1];
         sum.x += f * v.x, sum.y += f * v.y, sum.z += f * v.z, sum.w += f * v.w;
       }
       if (alone) {
         if (row0 + r < rows) finish(r, ch, sum, top, den);
       } else {
-        *reinterpret_cast<float4*>(partial + (my_slot * kRows + r) * D + ch) = sum;
+        if constexpr (kPart == kPrefix)
+          reinterpret_cast<float4*>(partial)[sums_at(my_slot * kRows + r, ch / 4, D / 4)] = sum;
+        else
+          *reinterpret_cast<float4*>(partial + (my_slot * kRows + r) * D + ch) = sum;
         if (ch == 0) {
           stats[(my_slot * kRows + r) * 2] = top;
           stats[(my_slot * kRows + r) * 2 + 1] = den;
@@ -830,7 +855,8 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
         auto slot_of = [](int k) { return (2l * k + (k == 0)) * kRows; };
         if (n <= kJoin) {  // statistics and sums are fetched together
           for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), ch = (i % (D / 4)) * 4;
+            const int r = by_rows ? i % kRows : i / (D / 4);
+            const int ch = (by_rows ? i / kRows : i % (D / 4)) * 4;
             if (row0 + r >= rows) continue;
             float2 st[kJoin];
             float4 v[kJoin];
@@ -885,7 +911,8 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
           }
           __syncthreads();
           for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), ch = (i % (D / 4)) * 4;
+            const int r = by_rows ? i % kRows : i / (D / 4);
+            const int ch = (by_rows ? i / kRows : i % (D / 4)) * 4;
             if (row0 + r >= rows) continue;
             float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             for (int k0 = 0; k0 < n; k0 += kJoin) {  // kJoin pieces on the way at a time
