@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // rows asked for together: over a prefix a CTA has one piece, as a rule, and
       // its queries are what the first product waits for
       constexpr int kRowLanes = D / 8, kRowsStep = 32 / kRowLanes;
-      constexpr int kBatch = kPart == kPrefix ? (D == 64 ? 8 : 16) : 4;
+      constexpr int kBatch = kPart == kPrefix ? 8 : 4;
       const long src = (t.sq.q0 + (live ? tok : 0)) * a.q.token + (live ? head : 0) * a.q.head;
 #pragma unroll 1
       for (int first = 0; first < kRowLanes; first += kBatch) {

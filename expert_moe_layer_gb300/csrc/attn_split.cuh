@@ -209,25 +209,35 @@ __device__ __forceinline__ void load_values(ValueRegs<D>& t, const uint8_t* stag
   }
 }
 
-// Four channels of a row's sums over the shared prefix, its pieces in CTA order,
-// added to the row's own. `at` is the row within the group, `c` its chunk.
-__device__ __forceinline__ void add_pieces(const PrefixSums& p, long per, const OwnPrefix& own,
-                                           int at, int kvh, int kv_heads, long at_row, int chunks, int c,
-                                           float4& sum, float& top, float& den) {
-  constexpr int kBatch = 10;  // pieces asked for together
+// Where the sums of one of a request's rows over the shared prefix lie: n pieces
+// in slots of CTAs that follow one another (two slots each; the first one's piece
+// is in its second), or one whole row (n 1, no slots between).
+struct RowPieces {
+  const float2* stat;
+  const float4* sum;
+  int n, slot_rows;
+};
+__device__ __forceinline__ RowPieces find_pieces(const PrefixSums& p, long per, const OwnPrefix& own,
+                                                 int at, int kvh, int kv_heads, long at_row,
+                                                 int chunks) {
+  if (own.len == 0) return {nullptr, nullptr, 0, 0};
   const int tile = at / p.shape.tile_rows, r = at - tile * p.shape.tile_rows;
   const long seg = own.base + (static_cast<long>(tile) * kv_heads + kvh) * own.len;
-  const long cta0 = quotient(seg + p.lo, per), cta1 = max(cta0, quotient(seg + own.len - p.hi, per));
-  const int n = static_cast<int>(cta1 - cta0) + 1;
-  const float2* stat = p.row_stats + at_row;
-  const float4* v0 = p.row_sums + sums_at(at_row, c, chunks);
-  long rows = 0, slot = 0;  // of a slot; every CTA has two, the first one's piece is in the second
-  if (n > 1) {
-    rows = p.shape.tile_rows;
-    slot = rows * chunks;
-    stat = p.stats + 2 * cta0 * rows + r;
-    v0 = p.sums + 2 * cta0 * slot + sums_at(r, c, chunks);
-  }
+  const long cta0 = quotient(seg + p.lo, per), cta1 = quotient(seg + own.len - p.hi, per);
+  if (cta1 <= cta0) return {p.row_stats + at_row, p.row_sums + sums_at(at_row, 0, chunks), 1, 0};
+  const long rows = 2 * cta0 * p.shape.tile_rows;
+  return {p.stats + rows + r, p.sums + rows * chunks + sums_at(r, 0, chunks),
+          static_cast<int>(cta1 - cta0) + 1, p.shape.tile_rows};
+}
+
+// Four channels (chunk c) of those sums, pieces in CTA order, added to the row's own.
+__device__ __forceinline__ void add_pieces(const RowPieces& p, int chunks, int c, float4& sum,
+                                           float& top, float& den) {
+  constexpr int kBatch = 10;  // pieces asked for together
+  const int n = p.n;
+  const long rows = p.slot_rows, slot = rows * chunks;
+  const float2* stat = p.stat;
+  const float4* v0 = p.sum + 8 * c;
   for (int k0 = 0; k0 < n; k0 += kBatch) {
     float2 st[kBatch];
     float4 v[kBatch];
@@ -397,12 +407,6 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
     const int t0 = max(0, p0 - kSetup), t1 = p1 - kSetup;
     const int row0 = row_tile * kRows;
     auto token_of = [&](int r) { return sq.q_len == 1 ? 0 : r / group; };
-    OwnPrefix own = {0, 0, 0};
-    long prefix_per = 1;
-    if constexpr (kPart == kOwn) {
-      own = part.p.own[b];
-      prefix_per = part.p.head->per;
-    }
 
     // this lane's score columns are rows nt*8 + 2c and + 1: their token limits
     int last[NT][2], first[NT][2];
@@ -493,6 +497,17 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) copy(t + i * kWarps, i, ids[i]);
     int2 next_ids = pages_of(t + (kStages - 1) * kWarps);
+    // (where the prefix's sums lie is known before they are there)
+    __shared__ RowPieces s_pieces[kPart == kOwn ? kRows : 1];
+    if constexpr (kPart == kOwn) {
+      const int r = row0 + lane, tok = token_of(r);
+      if (warp == kWarps - 1 && lane < kRows && r < rows) {  // it has the fewest tiles
+        const OwnPrefix own = part.p.own[b];
+        s_pieces[lane] = find_pieces(
+            part.p, part.p.head->per, own, own.tok0 * group + r, kvh, a.kv_heads,
+            static_cast<long>(sq.q0 + tok) * a.heads + kvh * group + r - tok * group, D / 4);
+      }
+    }
 
     // q^T as the B operand: column g (+ 8 nt), channels c*D/4 ..
     uint32_t qf[kTerms][NT][D / 8];
@@ -797,11 +812,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
         if (ch == 0) part.p.row_stats[at_row] = make_float2(top, den);
         return;
       }
-      if constexpr (kPart == kOwn) {
-        if (own.len > 0)
-          add_pieces(part.p, prefix_per, own, own.tok0 * group + row0 + r, kvh, a.kv_heads, at_row, D / 4,
-                     ch / 4, sum, top, den);
-      }
+      if constexpr (kPart == kOwn) add_pieces(s_pieces[r], D / 4, ch / 4, sum, top, den);
       const float f = out_factor(den, a.v_scale);
       store4(static_cast<T*>(a.out) + at_row * D + ch,
              make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f));
