@@ -106,7 +106,7 @@ constexpr int kSmallGroups = 64;
 struct PrefixHead {
   long per;          // entries per CTA of the list over the prefixes
   long own_per;      // and of the own kernel's
-  int own_len, pad;  // entries of every segment there; 0: as many as it has tiles
+  int own_piece, pad;  // tiles of a piece there, where segments are cut into whole pieces; 0: else
 };
 
 // Where a request's rows lie in the prefix kernel's list (len 0: no prefix).

@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
   const int group = a.heads / a.kv_heads;
   const KvBlock blk = kv_block(a.page_size, D);
   long total, per;
-  int same_len = 0;  // kOwn: list entries of every segment, or 0
+  int piece = 0;  // kOwn: segments are whole pieces of so many tiles, without set-up entries
   if constexpr (kPart == kPrefix) {
     __shared__ GroupSmem s_groups;
     __shared__ long s_sum[kWarps];
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
   } else if constexpr (kPart == kOwn) {
     total = starts[a.B];
     per = part.p.head->own_per;
-    same_len = part.p.head->own_len;
+    piece = part.p.head->own_piece;
   } else {
     total = starts[a.B];
     per = range_len(total, gridDim.x);
@@ -390,8 +390,12 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
     const SeqInfo sq = info[b];
     const int first_tile = kPart == kPrefix ? 0 : sq.first_key / kTile;
     const int rows = sq.q_len * group;
-    int per_seg = kSetup + max(0, (sq.len + kTile - 1) / kTile - first_tile);
-    if (kPart == kOwn && same_len > 0) per_seg = same_len;
+    int per_seg = max(0, (sq.len + kTile - 1) / kTile - first_tile);
+    const int setup = kPart == kOwn && piece > 0 ? 0 : kSetup;
+    if (setup == 0)
+      per_seg = max(1, (per_seg + piece - 1) / piece) * piece;
+    else
+      per_seg += kSetup;
     if (seg_start < 0) {
       const long seg = (at - starts[b]) / per_seg;
       seg_start = starts[b] + seg * per_seg;
@@ -399,12 +403,12 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
       kvh = static_cast<int>(seg - static_cast<long>(row_tile) * a.kv_heads);
     }
     const long seg_end = seg_start + per_seg;
-    if (at - seg_start < kSetup) at = seg_start;
-    if (end - seg_start < kSetup) break;  // a later CTA takes all of it
+    if (at - seg_start < setup) at = seg_start;
+    if (end - seg_start < setup) break;  // a later CTA takes all of it
     // this CTA's part [p0, p1) of the segment's list, and of its tiles
     const int p0 = static_cast<int>(at - seg_start);
     const int p1 = static_cast<int>(min(seg_end, end) - seg_start);
-    const int t0 = max(0, p0 - kSetup), t1 = p1 - kSetup;
+    const int t0 = max(0, p0 - setup), t1 = p1 - setup;
     const int row0 = row_tile * kRows;
     auto token_of = [&](int r) { return sq.q_len == 1 ? 0 : r / group; };
 
@@ -851,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, kRows, kTerms>()))
       }
     }
     if (kPart != kPrefix && !alone) {
-      const int cta0 = static_cast<int>((seg_start + kSetup - 1) / per);
+      const int cta0 = static_cast<int>((seg_start + max(0, setup - 1)) / per);
       const int cta1 = static_cast<int>((seg_end - 1) / per);
       __threadfence();
       __syncthreads();

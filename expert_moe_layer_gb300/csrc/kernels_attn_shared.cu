@@ -32,9 +32,11 @@ constexpr int kPlanThreads = 256;
 constexpr int kSmallSeqs = 1024;
 static_assert(kPrefixCut == split::kTile, "own keys begin with a tile");
 
-// (Tiles: 64 requests of up to 1024 own tokens 36 us, with twice the set-up 39; up to
-// 4096 45 us, with 1000 tiles 52.)
-constexpr int kSameSlack = 96;
+// Pieces are not cut below kShortPiece tiles, and not taken where they are longer
+// than a CTA's share of all entries and kPieceSlack more. Equal ranges and pieces,
+// prefixes of 4096 tokens, heads as above: 64 requests of up to 1024 own tokens 39
+// and 32 us, 4 of up to 4096 25 and 22; 64 of up to 4096 39 and 46, so ranges there.
+constexpr int kPieceSlack = 8, kShortPiece = 12;
 // The list of the own kernel.
 struct OwnList {
   int rows, ctas;
@@ -54,7 +56,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ GroupSmem s_groups;
   __shared__ SeqInfo s_info[kSmallSeqs];
   __shared__ long s_starts[kSmallSeqs];
-  __shared__ int s_group[kSmallSeqs], s_longest;
+  __shared__ int s_group[kSmallSeqs], s_longest, s_enough[kPlanThreads / 32];
   if (threadIdx.x == 0) s_longest = 0;
   // the prefix kernel may report before this one ends: the status first
   pdl_wait();
@@ -108,23 +110,53 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (threadIdx.x % 32 == 0) atomicMax(&s_longest, most);
   }
   __syncthreads();
-  const int longest = split::kSetup + s_longest;
-  sum += segs * split::kSetup;
-  // Segments of one length, cut into the same number of pieces, one to a CTA, as
-  // long as the longest does not hold up the others: a CTA with parts of two
-  // segments takes about twice as long as with one, whatever its tiles.
-  const int cuts = segs > 0 && segs <= o.ctas ? o.ctas / static_cast<int>(segs) : 0;
-  long own_per = cuts > 0 ? (longest + cuts - 1) / cuts : 0;
-  if (cuts > 0 && (own_per - kSameSlack) * o.ctas <= sum) {
-    own_per = max(own_per, static_cast<long>(min(longest, split::kMinTiles + split::kSetup)));
-    const int len = (longest + static_cast<int>(own_per) - 1) / static_cast<int>(own_per) *
-                    static_cast<int>(own_per);
-    for (int b = threadIdx.x; b <= a.B; b += kPlanThreads) {
-      const long at = (b < a.B ? starts[b] : segs) * len;
-      o.starts[b] = at;
-      if (b < a.B && few_seqs) starts[b] = at;
+  // Whole pieces, one to a CTA: of as few tiles as give no more pieces than CTAs. A
+  // part of a segment takes a CTA as long as 16 tiles beside its own, so that equal
+  // ranges, where most CTAs have parts of two segments, pay only where there are
+  // more segments than CTAs, few of them, or some much longer than the others.
+  const int fours = (s_longest + 3) / 4;  // pieces of whole fours, a tile for each warp
+  long own_per = 0;
+  int piece = 0;
+  if (few_seqs && segs <= o.ctas) {
+    int hi = max(1, fours), lo = min(kShortPiece / 4 - 1, hi - 1);  // lo fours are too few, hi are enough
+    while (hi - lo > 1) {            // a warp per candidate
+      const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = kPlanThreads / 32;
+      auto candidate = [&](int w) {
+        return lo + max(1, static_cast<int>(static_cast<long>(hi - lo) * (w + 1) / (warps + 1)));
+      };
+      const int tiles = 4 * candidate(warp);
+      long n = 0;
+      for (int b = lane; b < a.B; b += 32) {
+        const int t = tiles_of(info[b]);
+        n += segments(info[b].q_len) * max(1, (t + tiles - 1) / tiles);
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d /= 2) n += __shfl_xor_sync(~0u, n, d);
+      if (lane == 0) s_enough[warp] = n <= o.ctas;
+      __syncthreads();
+      int most = lo, least = hi;
+      for (int w = 0; w < warps; ++w) {
+        if (s_enough[w]) least = min(least, candidate(w));
+        else most = max(most, candidate(w));
+      }
+      lo = most, hi = least;
+      __syncthreads();
     }
-    if (threadIdx.x == 0) head->own_len = static_cast<int>(len);
+    own_per = piece = 4 * hi;
+    if (piece > kShortPiece &&
+        (piece - kPieceSlack) * static_cast<long>(o.ctas) > sum + segs * split::kSetup)
+      piece = 0;
+  }
+  if (piece > 0) {
+    long at = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+      const int b = b0 + threadIdx.x;
+      long n = 0;
+      if (b < a.B) n = segments(info[b].q_len) * max(1, (tiles_of(info[b]) + piece - 1) / piece) * piece;
+      const long before = block_scan<kPlanThreads>(n, warp_sum, at);
+      if (b < a.B) starts[b] = o.starts[b] = before;
+    }
+    if (threadIdx.x == 0) o.starts[a.B] = at, head->own_piece = piece;
   } else {
     long at = 0;
     for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
@@ -138,7 +170,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       }
     }
     own_per = split::range_len(at, o.ctas);
-    if (threadIdx.x == 0) o.starts[a.B] = at, head->own_len = 0;
+    if (threadIdx.x == 0) o.starts[a.B] = at, head->own_piece = 0;
   }
   if (threadIdx.x == 0) head->own_per = own_per;
   __syncthreads();
