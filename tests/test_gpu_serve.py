@@ -260,6 +260,15 @@ NORMS = [  # T, H, act, residual, kind, post, gate, strided
     (4, 16384, "bf16", "bf16", "layer", True, "full", False), (3, 16384, "f32", "f32", "rms", True, "none", True),
     (2, 16383, "bf16", "f32", "layer", True, "channel", False), (300, 1000, "bf16", "bf16", "rms", True, "full", True),
     (1000, 136, "f32", "bf16", "layer", False, "channel", False),
+    # rows that lie anywhere: no tensor's begin like another's
+    (7, 1000, "bf16", "f32", "rms", True, "full", 3), (9, 130, "f32", "bf16", "layer", True, "channel", 3),
+    # many rows for each block, in every kernel
+    (20000, 64, "bf16", "bf16", "rms", True, "channel", False), (8000, 256, "f32", "bf16", "layer", True, "full", False),
+    (3000, 2048, "bf16", "f32", "layer", True, "full", True), (2500, 2056, "bf16", "bf16", "rms", False, "token", False),
+    (2500, 1001, "bf16", "f32", "rms", True, "full", False), (20000, 99, "f32", "f32", "layer", True, "channel", False),
+    (9000, 333, "bf16", "bf16", "rms", True, "full", 3), (1100, 4100, "bf16", "bf16", "rms", False, "none", False),
+    (900, 12288, "bf16", "bf16", "rms", True, "channel", False), (400, 16383, "f32", "f32", "layer", True, "none", False),
+    (2000, 1000, "f32", "bf16", "rms", False, "full", 3),
 ]
 
 
@@ -270,10 +279,12 @@ def _norm_case(T, H, act, res, kind, post, gate, strided, seed):
     def rows(dt, m):
         if not strided:
             return torch.from_numpy(m).to(TORCH[dt]).cuda()
-        wide = torch.full((T, H + 24), float("nan"), dtype=TORCH[dt], device="cuda")
-        wide[:, 8:8 + H] = torch.from_numpy(m).to(TORCH[dt])
-        return wide[:, 8:8 + H]
+        at, more = (8, 24) if strided is True else next(places)
+        wide = torch.full((T, H + more), float("nan"), dtype=TORCH[dt], device="cuda")
+        wide[:, at:at + H] = torch.from_numpy(m).to(TORCH[dt])
+        return wide[:, at:at + H]
 
+    places = iter([(3, 5), (2, 7)])
     y, x = rows(act, 3 * rand(T, H) + 0.3), rows(res, 2 * rand(T, H) - 1)
     w = {k: torch.from_numpy(rand(H)).cuda() for k in ("post_w", "pre_w", "post_b", "pre_b")}
     if kind == "rms":
