@@ -12,7 +12,6 @@
 // memory: a warp takes 4 KB of a page, eight 16-byte loads per lane on the way.
 #include <cuda_runtime.h>
 
-#include "attn_dev.cuh"
 #include "launch.cuh"
 #include "ptx.cuh"
 #include "serve.h"
@@ -26,6 +25,7 @@ constexpr int kApplyThreads = 256;
 constexpr int kPiece = 4096;       // bytes of a page that a warp copies at a time
 constexpr int kCopyCtasPerSm = 6;  // of kApplyThreads
 constexpr int kMaxApplyCtas = 2048;
+constexpr int kAhead = 4;          // entries that a thread has under way
 
 struct Item {
   int first;  // rank of its first fresh page; -1: nothing is done
@@ -57,6 +57,42 @@ Work work_of(const PoolArgs& a, void* ws, const PoolLayout& L) {
   k.chunk = pool_chunk(a.pages);
   k.chunks = static_cast<int>((a.pages + k.chunk - 1) / k.chunk);
   return k;
+}
+
+// A token's entry, and the entries that so many tokens take.
+__device__ __forceinline__ int entry_of(const PoolArgs& a, long token) {
+  return static_cast<int>(token >> a.page_shift);
+}
+__device__ __forceinline__ int entries_of(const PoolArgs& a, long tokens) {
+  return static_cast<int>((tokens + (1l << a.page_shift) - 1) >> a.page_shift);
+}
+__device__ __forceinline__ long tokens_of_row(const PoolArgs& a) {
+  return static_cast<long>(a.max_pages) << a.page_shift;
+}
+
+// Sum of the values of the threads before this one in a block of kScanThreads,
+// plus `base`, to which the block's sum is added.
+template <typename T>
+__device__ __forceinline__ T scan(T v, T* warp_sum, T& base) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T sum = v;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const T u = __shfl_up_sync(~0u, sum, d);
+    if (lane >= d) sum += u;
+  }
+  if (lane == 31) warp_sum[warp] = sum;
+  __syncthreads();
+  T warps = warp_sum[lane];  // (as many warps as lanes)
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const T u = __shfl_up_sync(~0u, warps, d);
+    if (lane >= d) warps += u;
+  }
+  const T before = base + (warp > 0 ? __shfl_sync(~0u, warps, (warp + 31) & 31) : 0);
+  base += __shfl_sync(~0u, warps, 31);
+  __syncthreads();
+  return before + sum - v;
 }
 
 __device__ __forceinline__ void report(const PoolArgs& a, unsigned flags) {
@@ -97,10 +133,10 @@ __device__ __forceinline__ int used_page(const Work& w, long pages, long k) {
 // A CTA's chunk: its free pages and its pages in use into the list, and with
 // kRanks each page's place among its kind. Returns the free ones' number.
 template <bool kRanks>
-__device__ __forceinline__ int scan_chunk(const PoolArgs& a, const Work& w, long* warp_sum) {
+__device__ __forceinline__ int scan_chunk(const PoolArgs& a, const Work& w, int* warp_sum) {
   const long begin = blockIdx.x * w.chunk, end = min(begin + w.chunk, a.pages);
   const bool wide = reinterpret_cast<uintptr_t>(a.refs) % 16 == 0;
-  long found = 0;
+  int found = 0;
   for (long at = begin; at < end; at += kScan) {
     const long p0 = at + threadIdx.x * kPer;
     int refs[kPer];
@@ -117,7 +153,7 @@ __device__ __forceinline__ int scan_chunk(const PoolArgs& a, const Work& w, long
     int n = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) n += refs[i] == 0;
-    long f = block_scan<kScanThreads>(n, warp_sum, found);  // free ones before p0
+    int f = scan(n, warp_sum, found);  // free ones before p0
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const long p = p0 + i;
@@ -125,7 +161,7 @@ __device__ __forceinline__ int scan_chunk(const PoolArgs& a, const Work& w, long
       const long u = p - begin - f;  // pages in use before p
       if (refs[i] == 0) {
         w.list[begin + f] = static_cast<int32_t>(p);
-        if (kRanks) w.ranks[p] = static_cast<int32_t>(f);
+        if (kRanks) w.ranks[p] = f;
         ++f;
       } else {
         w.list[end - 1 - u] = static_cast<int32_t>(p);
@@ -133,33 +169,33 @@ __device__ __forceinline__ int scan_chunk(const PoolArgs& a, const Work& w, long
       }
     }
   }
-  return static_cast<int>(found);
+  return found;
 }
 
 // Puts the chunk's count behind those of the others. True in the CTA that came
 // last, where prefix[] is then summed up and `total` holds all free pages.
-__device__ __forceinline__ bool last_to_scan(const Work& w, int found, long* warp_sum, long& total) {
+__device__ __forceinline__ bool last_to_scan(const Work& w, int found, int* warp_sum, int& total) {
   __shared__ int s_last;
-  if (w.chunks > 1) {
-    __threadfence();
+  if (w.chunks == 1) {
+    if (threadIdx.x == 0) w.prefix[0] = 0, w.prefix[1] = found;
+    total = found;
     __syncthreads();
-    if (threadIdx.x == 0) {
-      w.prefix[blockIdx.x] = found;
-      s_last = ptx::add_acq_rel(&w.head->done, 1) == w.chunks - 1;
-    }
-    __syncthreads();
-    if (!s_last) return false;
-    __threadfence();
-  } else {
-    if (threadIdx.x == 0) w.prefix[0] = found;
-    __syncthreads();
+    return true;
   }
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    w.prefix[blockIdx.x] = found;
+    s_last = ptx::add_acq_rel(&w.head->done, 1) == w.chunks - 1;
+  }
+  __syncthreads();
+  if (!s_last) return false;
+  __threadfence();
   total = 0;
   const int c = threadIdx.x;  // kMaxChunks is the number of threads
-  const long n = c < w.chunks ? __ldcg(w.prefix + c) : 0;
-  const long before = block_scan<kScanThreads>(n, warp_sum, total);
-  if (c < w.chunks) w.prefix[c] = static_cast<int>(before);
-  if (threadIdx.x == 0) w.prefix[w.chunks] = static_cast<int>(total);
+  const int before = scan(c < w.chunks ? __ldcg(w.prefix + c) : 0, warp_sum, total);
+  if (c < w.chunks) w.prefix[c] = before;
+  if (threadIdx.x == 0) w.prefix[w.chunks] = total;
   __syncthreads();
   return true;
 }
@@ -174,11 +210,11 @@ __device__ __forceinline__ Span span_of(const PoolArgs& a, int i, const int32_t*
   Span s = {rows ? rows[i] : i, 0, 0, 0, false};
   const long from = start[i], to = end[i];
   if (s.row < 0 || s.row >= a.rows || from < 0 || to < from ||
-      to > static_cast<long>(a.max_pages) * a.page_size)
+      to > tokens_of_row(a))
     return s;
   s.held = a.held[s.row];
-  s.hi = static_cast<int>((to + a.page_size - 1) / a.page_size);
-  s.lo = from < to ? static_cast<int>(from / a.page_size) : s.hi;
+  s.hi = entries_of(a, to);
+  s.lo = from < to ? entry_of(a, from) : s.hi;
   s.ok = s.held >= 0 && s.held <= a.max_pages;
   return s;
 }
@@ -195,7 +231,7 @@ __device__ __forceinline__ bool shared_page(const PoolArgs& a, int page, unsigne
 __global__ void __launch_bounds__(kScanThreads)
     reserve_plan_kernel(PoolArgs a, Work w, int n, const int32_t* rows, const int32_t* start,
                         const int32_t* end) {
-  __shared__ long warp_sum[kScanThreads / 32];
+  __shared__ int warp_sum[kScanThreads / 32];
   pdl_enter();
   if (w.chunks == 1) {
     if (threadIdx.x == 0) *w.head = {};
@@ -204,8 +240,9 @@ __global__ void __launch_bounds__(kScanThreads)
     __syncthreads();
   }
   const int found = scan_chunk<false>(a, w, warp_sum);
-  long all_free;
+  int all_free;
   if (!last_to_scan(w, found, warp_sum, all_free)) return;
+  __shared__ long item_sum[kScanThreads / 32];
   unsigned flags = 0;
   if (rows) {  // the first item of a row has it
     for (int i = threadIdx.x; i < n; i += kScanThreads)
@@ -226,7 +263,7 @@ __global__ void __launch_bounds__(kScanThreads)
     }
     const int stop = s.ok ? min(s.hi, s.held) : 0;
     int32_t* entries = a.table + static_cast<long>(s.row) * a.max_pages;
-    const bool cut = s.ok && start[i] % a.page_size != 0;  // the first page keeps tokens
+    const bool cut = s.ok && (start[i] & ((1 << a.page_shift) - 1)) != 0;  // the first page keeps tokens
     if (s.ok && s.lo < stop) {
       const int page = entries[s.lo];
       if (shared_page(a, page, flags)) {
@@ -252,7 +289,7 @@ __global__ void __launch_bounds__(kScanThreads)
     }
     if (s.ok) fresh = marked + max(0, s.hi - s.held);
     const long mine = fresh + (old >= 0 ? 1l << 40 : 0);
-    const long before = block_scan<kScanThreads>(mine, warp_sum, taken);
+    const long before = scan(mine, item_sum, taken);
     const long first = before & ((1l << 40) - 1);
     if (i < n) {
       const bool served = fresh == 0 || first + fresh <= all_free;
@@ -268,32 +305,46 @@ __global__ void __launch_bounds__(kScanThreads)
   report(a, flags);
 }
 
-// `bytes` of a page from src to dst by a warp, piece by piece of a grid-wide list
-// of units: (page of the list, cache, piece).
+// The pages of a list, in every cache, cut into pieces: (page of the list, cache,
+// piece). Each warp has a range of neighbouring pieces, so that it looks up a pair
+// of pages once for all pieces of it (compacting, where a page is found by rank in
+// two dependent loads, took 200 us with pieces dealt out in turn, the case below).
 template <class Pair>
 __device__ __forceinline__ void copy_units(const CacheList& from, const CacheList& to, long pairs,
                                            long warp, long warps, Pair pair) {
   const int lane = threadIdx.x & 31;
   const int pieces = static_cast<int>((from.page_bytes + kPiece - 1) / kPiece);
-  const long units = pairs * from.n * pieces;
-  for (long u = warp; u < units; u += warps) {
-    const long rest = u / pieces;
-    const int piece = static_cast<int>(u - rest * pieces);
-    const long j = rest / from.n;
-    const int c = static_cast<int>(rest - j * from.n);
-    const int2 ids = pair(j);
-    if (ids.x < 0) continue;
-    const long at = static_cast<long>(piece) * kPiece;
-    const int left = static_cast<int>(min(static_cast<long>(kPiece), from.page_bytes - at)) / 16;
-    const uint4* s = reinterpret_cast<const uint4*>(from.p[c] + ids.x * from.page_bytes + at);
-    uint4* d = reinterpret_cast<uint4*>(to.p[c] + ids.y * from.page_bytes + at);
-    uint4 v[kPiece / 512];
+  const long units = pairs * from.n * pieces, per = (units + warps - 1) / warps;
+  long u = warp * per;
+  const long end = min(units, u + per);
+  if (u >= end) return;
+  long rest = u / pieces;
+  int piece = static_cast<int>(u - rest * pieces);
+  long j = rest / from.n;
+  int c = static_cast<int>(rest - j * from.n);
+  int2 ids = pair(j);
+  for (; u < end; ++u) {
+    if (ids.x >= 0) {
+      const long at = static_cast<long>(piece) * kPiece;
+      const int left = static_cast<int>(min(static_cast<long>(kPiece), from.page_bytes - at)) / 16;
+      const uint4* s = reinterpret_cast<const uint4*>(from.p[c] + ids.x * from.page_bytes + at);
+      uint4* d = reinterpret_cast<uint4*>(to.p[c] + ids.y * from.page_bytes + at);
+      uint4 v[kPiece / 512];
 #pragma unroll
-    for (int i = 0; i < kPiece / 512; ++i)
-      if (32 * i + lane < left) v[i] = __ldcs(s + 32 * i + lane);
+      for (int i = 0; i < kPiece / 512; ++i)
+        if (32 * i + lane < left) v[i] = __ldcs(s + 32 * i + lane);
 #pragma unroll
-    for (int i = 0; i < kPiece / 512; ++i)
-      if (32 * i + lane < left) __stcs(d + 32 * i + lane, v[i]);
+      for (int i = 0; i < kPiece / 512; ++i)
+        if (32 * i + lane < left) __stcs(d + 32 * i + lane, v[i]);
+    }
+    if (++piece == pieces) {
+      piece = 0;
+      if (++c == from.n) {
+        c = 0;
+        ++j;
+        if (u + 1 < end) ids = pair(j);
+      }
+    }
   }
 }
 
@@ -351,14 +402,14 @@ __global__ void __launch_bounds__(kApplyThreads)
 
 __global__ void __launch_bounds__(kScanThreads)
     compact_plan_kernel(PoolArgs a, Work w, int32_t* used_out) {
-  __shared__ long warp_sum[kScanThreads / 32];
+  __shared__ int warp_sum[kScanThreads / 32];
   pdl_enter();
   if (w.chunks == 1) {
     if (threadIdx.x == 0) *w.head = {};
     __syncthreads();
   }
   const int found = scan_chunk<true>(a, w, warp_sum);
-  long all_free;
+  int all_free;
   if (!last_to_scan(w, found, warp_sum, all_free) || threadIdx.x != 0) return;
   const long used = a.pages - all_free;
   long moves = all_free;  // free pages below `used`
@@ -426,6 +477,13 @@ __global__ void __launch_bounds__(kApplyThreads)
   report(a, flags);
 }
 
+__global__ void clear_kernel(int* words, long n) {
+  pdl_enter();
+  for (long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+       i += static_cast<long>(gridDim.x) * blockDim.x)
+    words[i] = 0;
+}
+
 // A block per item. A child that an earlier item names too, or that is a parent
 // in this call, is refused by looking through the children: nothing that a block
 // reads is written by another then.
@@ -438,8 +496,8 @@ __global__ void __launch_bounds__(kApplyThreads)
     const int parent = parents[i], child = children[i];
     const long t = tokens[i];
     bool ok = parent >= 0 && parent < a.rows && child >= 0 && child < a.rows && t >= 0 &&
-              t <= static_cast<long>(a.max_pages) * a.page_size;
-    const int need = ok ? static_cast<int>((t + a.page_size - 1) / a.page_size) : 0;
+              t <= tokens_of_row(a);
+    const int need = ok ? entries_of(a, t) : 0;
     bool clash = false;
     for (int j = threadIdx.x; j < n; j += kApplyThreads) {
       const int other = children[j];
@@ -455,13 +513,23 @@ __global__ void __launch_bounds__(kApplyThreads)
     }
     const int32_t* from = a.table + static_cast<long>(parent) * a.max_pages;
     int32_t* to = a.table + static_cast<long>(child) * a.max_pages;
-    for (int e = threadIdx.x; e < need; e += kApplyThreads) {
-      const int page = from[e];
-      to[e] = page;
-      if (page >= 0 && page < a.pages)
-        atomicAdd(a.refs + page, 1);
-      else
-        flags |= MOE_DEV_BAD_PAGE;
+    for (int e0 = threadIdx.x; e0 < need; e0 += kAhead * kApplyThreads) {
+      int page[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int e = e0 + i * kApplyThreads;
+        page[i] = e < need ? from[e] : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int e = e0 + i * kApplyThreads;
+        if (e >= need) continue;
+        to[e] = page[i];
+        if (page[i] >= 0 && page[i] < a.pages)
+          atomicAdd(a.refs + page[i], 1);
+        else
+          flags |= MOE_DEV_BAD_PAGE;
+      }
     }
     if (threadIdx.x == 0) a.held[child] = need;
   }
@@ -482,21 +550,39 @@ __global__ void __launch_bounds__(kApplyThreads)
       flags |= MOE_DEV_BAD_ROW;
       continue;
     }
-    const long pages = (t + a.page_size - 1) / a.page_size;
-    const int left = static_cast<int>(min(pages, static_cast<long>(a.max_pages)));
+    const int left = min(entries_of(a, t), a.max_pages);
     __syncthreads();
     if (threadIdx.x == 0) s_held = atomicMin(a.held + row, left);
     __syncthreads();
     const int held = s_held;
     if (held < 0 || held > a.max_pages) flags |= MOE_DEV_BAD_ROW;
     int32_t* entries = a.table + static_cast<long>(row) * a.max_pages;
-    for (int e = left + threadIdx.x; e < min(held, a.max_pages); e += kApplyThreads) {
-      const int page = entries[e];
-      entries[e] = -1;
-      if (page >= 0 && page < a.pages)
-        drop(a, page, flags);
-      else
-        flags |= MOE_DEV_BAD_PAGE;
+    const int stop = min(held, a.max_pages);
+    for (int e0 = left + threadIdx.x; e0 < stop; e0 += kAhead * kApplyThreads) {
+      int page[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int e = e0 + i * kApplyThreads;
+        page[i] = e < stop ? entries[e] : 0;
+      }
+      int before[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int e = e0 + i * kApplyThreads;
+        before[i] = 1;
+        if (e >= stop) continue;
+        entries[e] = -1;
+        if (page[i] >= 0 && page[i] < a.pages)
+          before[i] = atomicSub(a.refs + page[i], 1);
+        else
+          flags |= MOE_DEV_BAD_PAGE;
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (before[i] <= 0) {
+          atomicAdd(a.refs + page[i], 1);
+          flags |= MOE_DEV_BAD_PAGE;
+        }
     }
   }
   report(a, flags);
@@ -530,6 +616,14 @@ int copy_ctas(const CacheList& caches, long pairs, int sms) {
 }
 
 }  // namespace
+
+// (A kernel, not a memset: it can be scheduled while the one before it ends, and
+// the one after it while it runs.)
+cudaError_t launch_clear(void* words, long n, cudaStream_t st) {
+  const long blocks = (n + 1023) / 1024;
+  return launch_pdl(&clear_kernel, dim3(static_cast<unsigned>(blocks < 64 ? blocks : 64)),
+                    dim3(n < 32 ? 32 : 1024), 0, st, static_cast<int*>(words), n);
+}
 
 bool pool_clears(long pages) { return pages <= pool_chunk(pages); }
 

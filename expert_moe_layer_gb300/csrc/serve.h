@@ -37,7 +37,7 @@ struct PoolArgs {
   int32_t* table = nullptr;  // [rows, max_pages]
   int32_t* held = nullptr;   // [rows]
   int32_t* refs = nullptr;   // [pages]
-  int rows = 0, max_pages = 0, page_size = 0;
+  int rows = 0, max_pages = 0, page_shift = 0;  // log2 of the page size
   long pages = 0;
   unsigned* status = nullptr;  // nullptr where a call has no workspace
 };
@@ -65,6 +65,9 @@ struct PoolLayout {
   size_t claims, items, copies, prefix, list, ranks, total;
 };
 PoolLayout pool_layout(long pages, int rows, int n);
+
+// Clears n words, the first of which is a call's status.
+cudaError_t launch_clear(void* words, long n, cudaStream_t st);
 
 // Callers clear the header (and the claims where `rows` is given) first, unless
 // pool_clears says that the kernel does so itself.

@@ -60,7 +60,8 @@ CacheList cache_list(const moe_attn_config* cfg, const moe_kv_caches& c) {
 PoolArgs pool_args(const moe_attn_config* cfg, const moe_kv_pool* p, void* status) {
   PoolArgs a;
   a.table = p->page_table, a.held = p->held, a.refs = p->refs;
-  a.rows = p->num_rows, a.max_pages = p->max_pages, a.page_size = cfg->page_size;
+  a.rows = p->num_rows, a.max_pages = p->max_pages, a.page_shift = 0;
+  while ((1 << a.page_shift) < cfg->page_size) ++a.page_shift;
   a.pages = static_cast<long>(p->caches.num_pages);
   a.status = static_cast<unsigned*>(status);
   return a;
@@ -70,7 +71,7 @@ int validate_status_ws(const void* ws, size_t ws_bytes) {
   return ws && (ws_bytes < 4 || !aligned(ws, 4)) ? MOE_ERR_WORKSPACE : MOE_OK;
 }
 int clear_status(void* ws, cudaStream_t st) {
-  return ws ? cuda_ok(cudaMemsetAsync(ws, 0, 4, st)) : MOE_OK;
+  return ws ? cuda_ok(launch_clear(ws, 1, st)) : MOE_OK;
 }
 int sms_or_fail(int* sms) {
   *sms = sm_count();
@@ -137,7 +138,7 @@ int moe_kv_reserve(const moe_attn_config* cfg, const moe_kv_pool* pool, int n, c
   MOE_TRY(sms_or_fail(&sms));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!pool_clears(a.pages))
-    MOE_TRY(cuda_ok(cudaMemsetAsync(ws, 0, L.claims + (rows ? 4 * static_cast<size_t>(a.rows) : 0), st)));
+    MOE_TRY(cuda_ok(launch_clear(ws, static_cast<long>(L.claims) / 4 + (rows ? a.rows : 0), st)));
   return cuda_ok(
       launch_reserve(a, cache_list(cfg, pool->caches), n, rows, start, end, ws, L, sms, st));
 }
@@ -165,7 +166,7 @@ int moe_kv_compact(const moe_attn_config* cfg, const moe_kv_pool* pool, int32_t*
   int sms;
   MOE_TRY(sms_or_fail(&sms));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (!pool_clears(a.pages)) MOE_TRY(cuda_ok(cudaMemsetAsync(ws, 0, L.claims, st)));
+  if (!pool_clears(a.pages)) MOE_TRY(cuda_ok(launch_clear(ws, static_cast<long>(L.claims) / 4, st)));
   return cuda_ok(launch_compact(a, cache_list(cfg, pool->caches), used, ws, L, sms, st));
 }
 
