@@ -280,10 +280,17 @@ def _p(t):
     return t.data_ptr()
 
 
+_current_stream = None  # (imports torch on first use)
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        global _current_stream
+        if _current_stream is None:
+            import torch
+            raw, device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+            _current_stream = lambda: raw(device())  # noqa: E731
+        return _current_stream()
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -442,6 +449,9 @@ def _typed(name, t, key, shape):
     passes through; a None in the shape is not checked)."""
     if t is None:
         return None
+    # (what fits takes the short way: a call's checks cost as much as its launch)
+    if t.dtype is _DT.get(key) and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not _dt(key):
         raise ValueError(f"{name} must be {_dt(key)}; got {t.dtype}")
     have = t.shape
@@ -636,6 +646,10 @@ def _norm_rows(name, t, dtype, T, H):
     """(pointer, row stride) of a [T, H] tensor whose channels are contiguous."""
     if t is None:
         return None, 0
+    if t.dtype is _DT.get(dtype) and t.shape == (T, H) and t.is_cuda:
+        st, sd = t.stride()
+        if sd == 1:
+            return t.data_ptr(), st
     if t.dtype is not _dt(dtype):
         raise ValueError(f"{name} must be {_dt(dtype)}; got {t.dtype}")
     if t.shape != (T, H):
@@ -674,14 +688,14 @@ def _gate(gate, cfg, T):
 
 
 def moe_norm(cfg, T, y, x, post_w, post_b, gate, pre_w, pre_b, x_out, h, ws=None, stream=None):
-    H = cfg.hidden_size
+    H, act, res = cfg.hidden_size, cfg.act_dtype, cfg.residual_dtype
+    vec, rows = (H,), (T, H)
     _check("moe_norm", lib().moe_norm(
-        ctypes.byref(cfg), T, *_norm_rows("y", y, cfg.act_dtype, T, H),
-        *_norm_rows("x", x, cfg.residual_dtype, T, H), _typed("post_w", post_w, "f32", (H,)),
-        _typed("post_b", post_b, "f32", (H,)), *_gate(gate, cfg, T),
-        _typed("pre_w", pre_w, "f32", (H,)), _typed("pre_b", pre_b, "f32", (H,)),
-        _typed("x_out", x_out, cfg.residual_dtype, (T, H)), _typed("h", h, cfg.act_dtype, (T, H)),
-        _p(ws), _nbytes(ws), _stream(stream)))
+        ctypes.byref(cfg), T, *_norm_rows("y", y, act, T, H), *_norm_rows("x", x, res, T, H),
+        _typed("post_w", post_w, "f32", vec), _typed("post_b", post_b, "f32", vec),
+        *_gate(gate, cfg, T), _typed("pre_w", pre_w, "f32", vec),
+        _typed("pre_b", pre_b, "f32", vec), _typed("x_out", x_out, res, rows),
+        _typed("h", h, act, rows), _p(ws), _nbytes(ws), _stream(stream)))
 
 
 def moe_get_status(ws, stream=None) -> tuple[int, int]:
