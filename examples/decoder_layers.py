@@ -4,8 +4,8 @@ and attention over it, then the MoE layer.
     python examples/decoder_layers.py
 
 runs a prompt through a few random layers and decodes further tokens from a
-CUDA graph. The projections around attention are plain matrix products and the
-norms plain torch; everything else goes through the library.
+CUDA graph. The projections around attention are plain matrix products;
+everything else goes through the library.
 """
 from __future__ import annotations
 
@@ -61,6 +61,7 @@ class Decoder:
         self.attn = B.make_attn_config(heads, kv_heads, head_dim, page_size, rotary_dim=head_dim,
                                        rope_positions=max_positions)
         self.moe = B.make_config(experts, 2, hidden, intermediate)
+        self.norm = B.make_norm_config(hidden)
         self.table = torch.empty(max_positions, head_dim, device="cuda")
         B.moe_rope_table(self.attn, max_positions, None, B.make_rope_scaling(), self.table)
         self.layers = [dict(qkv=w((heads + 2 * kv_heads) * head_dim, hidden),
@@ -75,23 +76,33 @@ class Decoder:
                    B.workspace_size(self.moe, tokens))
         return torch.empty(size, dtype=torch.uint8, device="cuda")
 
+    def attend(self, t, longest, q, q_offsets, seq_lens, cache, pages, out, ws):
+        B.moe_kv_attention(self.attn, seq_lens.shape[0], t, longest, q, q_offsets, seq_lens,
+                           cache.page_table, pages, out, None, ws)
+
     def forward(self, x, cache, positions, slots, q_offsets, seq_lens, longest, ws):
         """x [T, hidden] of all requests' new tokens -> the same after the layers."""
         t = x.shape[0]
+        y, h = None, torch.empty_like(x)    # the block before, and its sum's norm
         for w, pages in zip(self.layers, cache.layers):
-            qkv = (_norm(x) @ w["qkv"].T).unflatten(1, (-1, self.head_dim))
+            x = self._join(y, x, h)
+            qkv = (h @ w["qkv"].T).unflatten(1, (-1, self.head_dim))
             q, k, v = qkv.split([self.heads, self.kv_heads, self.kv_heads], dim=1)
             turned = torch.empty(t, self.heads, self.head_dim, dtype=x.dtype, device="cuda")
             B.moe_kv_append(self.attn, t, q, k, v, positions, slots, self.table, turned, pages)
             out = torch.empty_like(turned)
-            B.moe_kv_attention(self.attn, seq_lens.shape[0], t, longest, turned, q_offsets, seq_lens,
-                               cache.page_table, pages, out, None, ws)
-            x = x + out.flatten(1) @ w["o"].T
+            self.attend(t, longest, turned, q_offsets, seq_lens, cache, pages, out, ws)
+            x = self._join(out.flatten(1) @ w["o"].T, x, h)
             y = torch.empty_like(x)
-            B.moe_forward(self.moe, t, _norm(x), w["router"], None, w["w13"], w["w2"], None, None,
-                          None, y, ws)
-            x = x + y
-        return x
+            B.moe_forward(self.moe, t, h, w["router"], None, w["w13"], w["w2"], None, None, None, y, ws)
+        return self._join(y, x, None)
+
+    def _join(self, y, x, h):
+        """The residual x with a block's output y added (there is none before the
+        first), and into h its norm for the next block."""
+        out = x if y is None else torch.empty_like(x)
+        B.moe_norm(self.norm, x.shape[0], y, x, None, None, None, None, None, None if y is None else out, h)
+        return out
 
 
 def prompt(model, cache, xs):
