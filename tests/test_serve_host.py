@@ -160,6 +160,38 @@ def test_norm_arguments_are_checked():
     assert L.moe_norm(None, *[0] * 16, None) == 1
 
 
+def test_shared_attention_arguments_are_checked():
+    cfg = B.make_attn_config(**CFG)
+    L, c = B.lib(), ctypes.byref(cfg)
+    size = lambda *a: B.kv_attention_shared_workspace_size(cfg, *a)  # noqa: E731
+    for bad in ((-1, 4, 1, 1, 4), (4, -1, 1, 1, 4), (4, 4, -1, 1, 4), (4, 4, 1, -1, 4), (4, 4, 1, 1, -1),
+                (4, (1 << 18) + 1, 1, 1, 4), (4, 4, 1, (1 << 18) + 1, 4)):
+        assert size(*bad) == 0
+    need = size(4, 4, 1, 1, 4)
+    assert need > 4 * 4 * 8 * 64 and size(4, 4, 1, 1, 400) > need      # (the prompt kernel's pieces)
+    # without groups, with a window, or with many rows per request: as moe_kv_attention
+    assert size(4, 4, 1, 0, 0) == B.kv_attention_workspace_size(cfg, 4, 4, 1)
+    assert size(4, 128, 32, 1, 128) == B.kv_attention_workspace_size(cfg, 4, 128, 32)
+    w = B.make_attn_config(**CFG, window=9)
+    assert B.kv_attention_shared_workspace_size(w, 4, 4, 1, 1, 4) == B.kv_attention_workspace_size(w, 4, 4, 1)
+
+    def call(seqs=4, T=4, mq=1, groups=1, mg=4, q=FAKE, ts=512, hs=64, offs=None, lens=FAKE, table=FAKE, mp=8,
+             go=FAKE, pl=FAKE, cache=FAKE, pages=9, out=FAKE, lse=None, ws=FAKE, size=need, cfg=c):
+        return L.moe_kv_attention_shared(cfg, seqs, T, mq, groups, mg, q, ts, hs, offs, lens, table, mp, go, pl,
+                                         cache, pages, out, lse, ws, size, None)
+
+    assert call(T=0, seqs=0, q=None) == 0
+    for kw in (dict(groups=-1), dict(mg=-1), dict(mg=0), dict(go=None), dict(pl=None), dict(go=FAKE + 2),
+               dict(pl=FAKE + 1), dict(q=None), dict(q=FAKE + 8), dict(ts=509), dict(hs=60), dict(seqs=3),
+               dict(lens=None), dict(table=None), dict(mp=0), dict(mp=(1 << 20) + 1), dict(cache=None),
+               dict(pages=0), dict(out=FAKE + 4), dict(lse=FAKE + 2), dict(mq=0), dict(T=-1)):
+        assert call(**kw) == 1, kw
+    assert call(size=need - 1) == 3 and call(ws=None) == 3 and call(ws=FAKE + 8) == 3
+    assert call(groups=0, go=None, pl=None, size=8) == 3
+    bad = B.make_attn_config(**{**CFG, "head_dim": 96})
+    assert call(cfg=ctypes.byref(bad)) == 2
+
+
 def test_binding_refuses_wrong_tensors():
     cfg = B.make_attn_config(**CFG)
     with pytest.raises(ValueError, match="at least one"):
