@@ -149,9 +149,10 @@ constexpr int prompt_tile(int head_dim) { return head_dim == 256 ? 128 : 256; }
 constexpr int kPromptRows = 64;
 cudaError_t launch_prompt(const AttnArgs& a, void* ws, const AttnLayout& L, cudaStream_t st);
 
-// Rows per request from which a call does not share (shares_prefix).
-constexpr int kSharedRows = 128;
-bool shares_prefix(const moe_attn_config* c, int max_q, int groups);
+// Whether a call can share prefixes at all, and whether it pays for requests whose
+// rows of the page table have so many entries.
+bool can_share(const moe_attn_config* c, int max_q, int groups);
+bool worth_sharing(const moe_attn_config* c, int B, int max_q, int max_pages);
 struct SharedLayout {
   size_t status, head, counters, begins, info, own, starts, limit, first, groups, bases, stats,
       partial, prefix_stats, prefix_partial, row_stats, row_sums, total;

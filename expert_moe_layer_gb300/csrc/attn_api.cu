@@ -362,9 +362,10 @@ size_t moe_kv_attention_shared_workspace_size(const moe_attn_config* cfg, int nu
   if (validate_attention(cfg, num_seqs, T, max_q_len) != MOE_OK ||
       validate_groups(num_groups, max_group_len) != MOE_OK)
     return 0;
-  return shares_prefix(cfg, max_q_len, num_groups)
-             ? shared_layout(cfg, num_seqs, T, num_groups, max_group_len).total
-             : attn_layout(cfg, num_seqs, T, max_q_len).total;
+  const size_t plain = attn_layout(cfg, num_seqs, T, max_q_len).total;
+  if (!can_share(cfg, max_q_len, num_groups)) return plain;
+  const size_t shared = shared_layout(cfg, num_seqs, T, num_groups, max_group_len).total;
+  return shared > plain ? shared : plain;
 }
 
 int moe_kv_attention_shared(const moe_attn_config* cfg, int num_seqs, int T, int max_q_len,
@@ -385,15 +386,16 @@ int moe_kv_attention_shared(const moe_attn_config* cfg, int num_seqs, int T, int
                          !aligned(prefix_lens, 4) || max_group_len < 1))
     return MOE_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (!shares_prefix(cfg, max_q_len, num_groups)) {
-    const AttnLayout L = attn_layout(cfg, num_seqs, T, max_q_len);
-    if (!ws || ws_bytes < L.total || !aligned(ws, 16)) return MOE_ERR_WORKSPACE;
-    MOE_TRY(attention_sms(&a));
-    return cuda_ok(launch_kv_attention(cfg, a, ws, L, st));
-  }
-  const SharedLayout L = shared_layout(cfg, num_seqs, T, num_groups, max_group_len);
-  if (!ws || ws_bytes < L.total || !aligned(ws, 16)) return MOE_ERR_WORKSPACE;
+  if (!ws || !aligned(ws, 16) ||
+      ws_bytes < moe_kv_attention_shared_workspace_size(cfg, num_seqs, T, max_q_len, num_groups,
+                                                        max_group_len))
+    return MOE_ERR_WORKSPACE;
   MOE_TRY(attention_sms(&a));
+  if (!can_share(cfg, max_q_len, num_groups) ||
+      !worth_sharing(cfg, num_seqs, max_q_len, max_pages))
+    return cuda_ok(
+        launch_kv_attention(cfg, a, ws, attn_layout(cfg, num_seqs, T, max_q_len), st));
+  const SharedLayout L = shared_layout(cfg, num_seqs, T, num_groups, max_group_len);
   return cuda_ok(launch_kv_attention_shared(cfg, a, num_groups, group_offsets, prefix_lens,
                                             max_group_len, ws, L, st));
 }

@@ -295,14 +295,32 @@ cudaError_t launch_dim(const moe_attn_config* c, Launch& l) {
 
 }  // namespace
 
-// Requests of that many rows fill half a row tile of the prompt kernel by
+// Requests of so many rows (bf16) fill half a row tile of the prompt kernel by
 // themselves: its matrix work is no longer shared then, and their own keys are
 // better off there than with the split kernel, which goes through them once per
 // 16 rows. A window ends the sharing too: it begins elsewhere for each request.
-bool shares_prefix(const moe_attn_config* c, int max_q, int groups) {
+constexpr int kMostRows = 128;
+bool can_share(const moe_attn_config* c, int max_q, int groups) {
   if (groups == 0 || c->window > 0) return false;
   return c->act_dtype != MOE_BF16 ||
-         static_cast<long>(max_q) * (c->num_heads / c->num_kv_heads) < kSharedRows;
+         static_cast<long>(max_q) * (c->num_heads / c->num_kv_heads) < kMostRows;
+}
+
+// Sharing takes one kernel more, and some 4 us; reading the keys of every request
+// takes as long from about 40 MB on: 4 requests of 4160 tokens (8 kv heads of 128,
+// 19 MB) unshared 14.6 us and shared 16.4, of 16448 (76 MB) 25.9 and 22.1; 16 of
+// 1088 (19 MB) 14.2 and 17.9, of 4160 (76 MB) 25.1 and 22.0; 64 of 320 (20 MB)
+// 17.4 and 20.5, of 1088 (77 MB) 27.5 and 22.6; fp32, 32 of 2064 (37 MB) 23.5 and
+// 24.0. Lengths are not known here: the page table's width bounds them. From
+// kPromptRows rows a request the unshared call takes the prompt kernel, whose row
+// tiles are then half empty (4 requests of 72 rows, 9 MB: 49 and 24 us).
+constexpr double kShareBytes = 40e6;
+bool worth_sharing(const moe_attn_config* c, int B, int max_q, int max_pages) {
+  if (c->act_dtype == MOE_BF16 &&
+      static_cast<long>(max_q) * (c->num_heads / c->num_kv_heads) >= kPromptRows)
+    return true;
+  const double tokens = static_cast<double>(B) * max_pages * c->page_size;
+  return tokens * c->num_kv_heads * (c->head_dim * 9 / 8) > kShareBytes;
 }
 
 SharedLayout shared_layout(const moe_attn_config* c, int B, int T, int groups, int max_group) {

@@ -665,9 +665,11 @@ MOE_API int moe_kv_attention(const moe_attn_config* cfg, int num_seqs, int T, in
  * The other arguments and flags are those of moe_kv_attention. MOE_DEV_BAD_SEGMENT
  * is also set, and nothing shared, for group_offsets that decrease or leave
  * [0, num_seqs], a prefix below 0, or a group of more than max_group_len query
- * tokens (of that group): results are right all the same. With a window, or from
- * 128 rows per request (max_q_len times the heads of a group, bf16), the call is
- * moe_kv_attention and does not look at the groups. num_groups may be up to 2^18.
+ * tokens (of that group): results are right all the same. With a window, from 128
+ * rows per request (max_q_len times the heads of a group, bf16), and for requests
+ * whose pages together (num_seqs rows of max_pages) are too few to gain by it, the
+ * call is moe_kv_attention and does not look at the groups. num_groups may be up to
+ * 2^18.
  * ws: moe_kv_attention_shared_workspace_size(...) bytes (0: invalid); it has room
  * for T * num_heads * head_dim fp32 sums. */
 MOE_API size_t moe_kv_attention_shared_workspace_size(const moe_attn_config* cfg, int num_seqs,

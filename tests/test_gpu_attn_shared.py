@@ -25,10 +25,11 @@ def _views(cache, page, D):
 
 class Shared(Case):
     """Case whose requests groups[g] .. groups[g+1] - 1 have their first prefix[g]
-    tokens in common: whole pages are shared, the page they end in is copied."""
+    tokens in common: whole pages are shared, the page they end in is copied. The
+    page table is wide enough for sharing to be taken up (or, not wide, is not)."""
 
     def __init__(self, seed, dtype, heads, kv, D, page, lens, qs, groups, prefix, told=None, max_group=None,
-                 **kw):
+                 wide=True, **kw):
         super().__init__(seed, dtype, heads, kv, D, page, lens, qs, **kw)
         views = _views(self.cache, page, D)
         for g, p in enumerate(prefix):
@@ -41,7 +42,10 @@ class Shared(Case):
                     for v in views:
                         v[int(self.table[b, n]), :, :rest] = v[int(self.table[a, n]), :, :rest]
                 self.k[b][:p], self.v[b][:p] = self.k[a][:p], self.v[a][:p]
-        self.d["table"].copy_(torch.from_numpy(self.table))
+        if wide:
+            more = 41e6 / (len(lens) * kv * page * D * 9 / 8) - self.table.shape[1]
+            self.table = np.pad(self.table, ((0, 0), (0, max(0, int(more) + 1))), constant_values=-7)
+        self.d["table"] = torch.from_numpy(self.table).cuda()
         self.G = len(prefix)
         self.d["groups"] = torch.tensor(groups if self.G else [0], dtype=torch.int32, device="cuda")
         self.d["prefix"] = torch.tensor(prefix if told is None else told, dtype=torch.int32, device="cuda")
@@ -191,10 +195,10 @@ def test_bad_requests_and_pages(n):
     assert ((lse - c.lse).abs() <= 2.0 ** -15 * (1 + lse.abs())).all()
 
 
-def test_windows_and_many_rows_are_the_unshared_attention():
-    for kw, q in ((dict(window=50), 1), (dict(), 33)):
+def test_windows_many_rows_and_few_pages_are_the_unshared_attention():
+    for kw, q in ((dict(window=50), 1), (dict(), 33), (dict(wide=False), 1)):
         c = Shared(76, "bf16", 8, 2, 128, 16, [300, 290], [q, q], [0, 2], [250], **kw)
-        assert c.sws.numel() == c.ws.numel()
+        assert c.sws.numel() >= c.ws.numel()
         c.shared()
         assert c.status() == (0, 0)
         got = c.out.clone(), c.lse.clone()
