@@ -484,13 +484,44 @@ __global__ void clear_kernel(int* words, long n) {
     words[i] = 0;
 }
 
+// Few items are carried out by the blocks of one cluster, which can agree that the
+// status is cleared before any of them reports (another kernel for that takes a
+// call's host time from 6 to 9 us).
+constexpr int kCluster = 8;
+__device__ __forceinline__ void enter_items(const PoolArgs& a, int n) {
+  pdl_enter();
+  if (n > kFewItems || !a.status) return;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
+  __syncwarp();
+  ptx::cluster_sync();
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch_items(void (*kern)(KArgs...), int n, cudaStream_t st, Args&&... args) {
+  if (n > kFewItems)
+    return launch_pdl(kern, dim3(n < kMaxApplyCtas ? n : kMaxApplyCtas), dim3(kApplyThreads), 0, st,
+                      std::forward<Args>(args)...);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kCluster);
+  cfg.blockDim = dim3(kApplyThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return counted(cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...));
+}
+
 // A block per item. A child that an earlier item names too, or that is a parent
 // in this call, is refused by looking through the children: nothing that a block
 // reads is written by another then.
 __global__ void __launch_bounds__(kApplyThreads)
     fork_kernel(PoolArgs a, int n, const int32_t* parents, const int32_t* children,
                 const int32_t* tokens) {
-  pdl_enter();
+  enter_items(a, n);
   unsigned flags = 0;
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
     const int parent = parents[i], child = children[i];
@@ -541,7 +572,7 @@ __global__ void __launch_bounds__(kApplyThreads)
 __global__ void __launch_bounds__(kApplyThreads)
     release_kernel(PoolArgs a, int n, const int32_t* rows, const int32_t* keep) {
   __shared__ int s_held;
-  pdl_enter();
+  enter_items(a, n);
   unsigned flags = 0;
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
     const int row = rows ? rows[i] : i;
@@ -665,14 +696,12 @@ cudaError_t launch_compact(const PoolArgs& a, const CacheList& caches, int32_t* 
 
 cudaError_t launch_fork(const PoolArgs& a, int n, const int32_t* parents, const int32_t* children,
                         const int32_t* tokens, cudaStream_t st) {
-  return launch_pdl(&fork_kernel, dim3(n < kMaxApplyCtas ? n : kMaxApplyCtas), dim3(kApplyThreads), 0,
-                    st, a, n, parents, children, tokens);
+  return launch_items(&fork_kernel, n, st, a, n, parents, children, tokens);
 }
 
 cudaError_t launch_release(const PoolArgs& a, int n, const int32_t* rows, const int32_t* keep,
                            cudaStream_t st) {
-  return launch_pdl(&release_kernel, dim3(n < kMaxApplyCtas ? n : kMaxApplyCtas),
-                    dim3(kApplyThreads), 0, st, a, n, rows, keep);
+  return launch_items(&release_kernel, n, st, a, n, rows, keep);
 }
 
 cudaError_t launch_copy_pages(const CacheList& from, long from_pages, const CacheList& to,

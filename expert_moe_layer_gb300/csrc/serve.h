@@ -66,6 +66,8 @@ struct PoolLayout {
 };
 PoolLayout pool_layout(long pages, int rows, int n);
 
+// Up to so many items the kernels of fork and release clear the status themselves.
+constexpr int kFewItems = 32;
 // Clears n words, the first of which is a call's status.
 cudaError_t launch_clear(void* words, long n, cudaStream_t st);
 

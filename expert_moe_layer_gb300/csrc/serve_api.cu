@@ -119,7 +119,7 @@ int moe_kv_fork(const moe_attn_config* cfg, const moe_kv_pool* pool, int n, cons
   if (!ints(parents) || !ints(children) || !ints(tokens)) return MOE_ERR_INVALID_ARG;
   MOE_TRY(validate_status_ws(ws, ws_bytes));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  MOE_TRY(clear_status(ws, st));
+  if (n > kFewItems) MOE_TRY(clear_status(ws, st));
   return cuda_ok(launch_fork(pool_args(cfg, pool, ws), n, parents, children, tokens, st));
 }
 
@@ -152,7 +152,7 @@ int moe_kv_release(const moe_attn_config* cfg, const moe_kv_pool* pool, int n, c
   if (!rows && n > pool->num_rows) return MOE_ERR_INVALID_ARG;
   MOE_TRY(validate_status_ws(ws, ws_bytes));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  MOE_TRY(clear_status(ws, st));
+  if (n > kFewItems) MOE_TRY(clear_status(ws, st));
   return cuda_ok(launch_release(pool_args(cfg, pool, ws), n, rows, keep, st));
 }
 
