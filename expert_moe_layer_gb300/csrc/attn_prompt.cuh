@@ -55,6 +55,10 @@ constexpr int kThreads = 512;  // whole groups of four warps (three idle ones)
 // Registers per thread: launched with 128 each (65,536 in all), shared out anew
 // by the groups of four warps: 128 * (2 * 184 + 80 + 64) = 65,536.
 constexpr int kSoftRegs = 184, kFillRegs = 80, kMmaRegs = 64;
+// Over prefixes: parts (a tile's keys, or its values) in shared memory or on the
+// way, and tiles whose bad-page bits are kept (one and a half of those are ahead of
+// the fill warps).
+constexpr int kParts = 3, kPrefixBadRing = 8;
 constexpr int kBadRing = 4;  // tiles whose bad-page bits are kept: a fill warp is at most
                              // two tiles ahead of the slower half
 // List entries of a segment beside its tiles: its set-up and store. (The chunks
@@ -87,11 +91,15 @@ struct Shape {
   static constexpr int kRawVs = kRawV + 64 * 32, kRaw = kRawVs + 64 * 4;
   static constexpr int kBytes =
       kHalves * kQ + 4 * kK + kFillWarps * kRaw + kSoftWarps * kStageBytes + 1024;
+  // Over prefixes: codes and scales of a tile's keys, or of its values.
+  static constexpr int kCodes = kKeys * D / 2, kScales = kKeys * D / 16, kPartBytes = kCodes + kScales;
+  static constexpr int kPrefixBytes = kHalves * kQ + 4 * kK + kParts * kPartBytes + 1024;
 };
 
 struct Bars {
   uint64_t q_ready[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2],
       o_done[2], written[2], joined[2], drain;
+  uint64_t raw_full[kParts], raw_empty[kParts];  // over prefixes
 };
 
 // 32 consecutive columns of this warp's 32 lanes. The values are there after
@@ -229,6 +237,14 @@ __device__ __forceinline__ uint32_t lds8(uint32_t addr) {
 template <int N>
 __device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+
+// Four 8x8 matrices of f16, transposed: lane l holds row l / 4, columns 2 (l % 4)
+// and + 1 of each, and names the place of stored row l % 8 of matrix l / 8.
+__device__ __forceinline__ void stmatrix_trans(uint32_t addr, const uint32_t (&m)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr),
+               "r"(m[0]), "r"(m[1]), "r"(m[2]), "r"(m[3])
+               : "memory");
 }
 
 // Byte offset of 16-byte chunk `chunk` of row `row` in a 128-byte-swizzled
@@ -451,7 +467,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kKeys = H::kKeys;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars bars;
-  __shared__ __align__(16) uint32_t s_bad[kBadRing][4];
+  constexpr int kBadTiles = kPart == kPrefix ? kPrefixBadRing : kBadRing;
+  __shared__ __align__(16) uint32_t s_bad[kBadTiles][4];
   __shared__ uint32_t s_tmem;
   __shared__ int s_last[2];
   __shared__ volatile int s_abort;
@@ -473,6 +490,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(bar(bars.o_done[i]), 1);
       ptx::mbar_init(bar(bars.written[i]), 4);
       ptx::mbar_init(bar(bars.joined[i]), 1);
+    }
+    for (int i = 0; i < kParts; ++i) {
+      ptx::mbar_init(bar(bars.raw_full[i]), 1);
+      ptx::mbar_init(bar(bars.raw_empty[i]), kFillWarps);
     }
     ptx::mbar_init(bar(bars.drain), 1);
     ptx::fence_barrier_init();
@@ -677,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j > 0) ptx::mbar_arrive(bar(bars.v_empty[(tile_no - 1) & 1]));
         }
         const int tok0 = (t.first + j) * kKeys;
-        const uint32_t bad_at = ptx::smem_u32(s_bad[tile_no % kBadRing]);
+        const uint32_t bad_at = ptx::smem_u32(s_bad[tile_no % kBadTiles]);
         const bool inside = tok0 >= all_first && tok0 + kKeys - 1 <= all_last;
 #pragma unroll 1
         for (int c = 0; c < kKeys / 64; ++c) {
@@ -792,12 +813,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t v[32];
           tmem_ld32(to + 32 * c, v);
           tmem_landed(v);
+          // column 8 (4 c + m) + 2 q + b is channel D / 4 q + 8 c + 2 m + b
           if (store)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[(8 * c + i) * 8] =
-                  make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
-                              __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+            for (int i = 0; i < 8; ++i) {
+              const int q = i / 2, at = 16 * (i % 2) + 2 * q;
+              dst[(D / 16 * q + 2 * c + i % 2) * 8] =
+                  make_float4(__uint_as_float(v[at]), __uint_as_float(v[at + 1]),
+                              __uint_as_float(v[at + 8]), __uint_as_float(v[at + 9]));
+            }
         }
         if (store)
           (alone ? part.p.row_stats : stats)[row] = make_float2(m == -INFINITY ? -INFINITY : mbase, l);
@@ -903,6 +927,98 @@ __global__ void __launch_bounds__(kThreads, 1)
     // keys: lane's row kr, all of its channels or half of 256
     constexpr int kChans = H::kChans;
     const int kr = ft % kKeys, kpart = ft / kKeys;
+    if constexpr (kPart == kPrefix) {
+      // Whole parts come from the copying warp, so that all four warps wait for the
+      // same ones; copies issued by these warps took half of their time.
+      // Keys: a lane has a row, its 16-byte chunks in an order of its own, so that
+      // eight lanes read, and write, different banks. Values: a lane has a quarter
+      // of a token's channels; words of eight channels of eight tokens are turned
+      // into rows of tokens by matrix stores. Channel D / 4 q + 8 k + 2 m + b (q:
+      // lane, k: word, m: matrix) becomes row 8 (4 k + m) + 2 q + b of the operand,
+      // so that a matrix's rows follow one another; the sums' columns go back to
+      // their channels as they are stored.
+      constexpr int kChunks = kChans / 32, kWords = D / 32;
+      const int spin = D == 128 ? lane >> 1 : D == 64 ? lane >> 2 : lane;
+      uint32_t kc = 0, slot = 0, phase = 0;
+      auto part_at = [&] { return sm_raw + slot * H::kPartBytes; };
+      auto part_done = [&] {
+        if (lane == 0) ptx::mbar_arrive(bar(bars.raw_empty[slot]));
+        if (++slot == kParts) slot = 0, phase ^= 1;
+      };
+      bool ok = true;
+      begin();
+      while (ok && next()) {
+#pragma unroll 1
+        for (int j = 0; j < t.tiles; ++j, ++kc) {
+          const uint32_t st = kc & 1, parity = ((kc >> 1) & 1) ^ 1;
+          if (!(ok = wait_warp(bars.raw_full[slot], phase) && wait_warp(bars.k_empty[st], parity)))
+            break;
+          const uint32_t codes = part_at() + kr * (D / 2) + kpart * (kChans / 2);
+          const uint32_t scales = part_at() + H::kCodes + kr * (D / 16) + kpart * (kChans / 16);
+#pragma unroll 2
+          for (int n = 0; n < kChunks; ++n) {
+            const int i = (n + spin) % kChunks;
+            const uint4 w = lds128(codes + 16 * i);
+            const uint32_t two = e4m3x2_to_f16(lds16(scales + 2 * i));
+            const uint32_t s2[2] = {f16_low_twice(two), f16_high_twice(two)};
+            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t h[4];
+              e2m1_to_f16(words[c], h);
+              const uint32_t sc = s2[c / 2];
+              sts128(sm_k + st * H::kK + swizzled(kr, kpart * (kChans / 8) + 4 * i + c, kKeys),
+                     hmul2(h[0], sc), hmul2(h[1], sc), hmul2(h[2], sc), hmul2(h[3], sc));
+            }
+          }
+          ptx::fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(bars.k_full[st]));
+          part_done();
+          if (!(ok = wait_warp(bars.raw_full[slot], phase) && wait_warp(bars.v_empty[st], parity)))
+            break;
+#pragma unroll 1
+          for (int n = 0; n < kKeys / 8 / kFillWarps; ++n) {
+            const int eight = fw * (kKeys / 8 / kFillWarps) + n;  // of the tile's tokens
+            const int tok = 8 * eight + lane / 4, q = lane & 3;
+            const uint32_t row = part_at() + tok * (D / 2) + q * (D / 8);
+            uint32_t words[kWords];
+            if constexpr (kWords == 2) {
+              const uint2 w = lds64(row);
+              words[0] = w.x, words[1] = w.y;
+            } else {
+#pragma unroll
+              for (int k = 0; k < kWords; k += 4) {
+                const uint4 w = lds128(row + 4 * k);
+                words[k] = w.x, words[k + 1] = w.y, words[k + 2] = w.z, words[k + 3] = w.w;
+              }
+            }
+            // a key that no row sees may be uninitialised memory: a zero scale keeps
+            // 0 * NaN out of the sum
+            const uint32_t bad = lds32(ptx::smem_u32(&s_bad[kc % kBadTiles][tok / 32]));
+            const bool seen = (t.first + j) * kKeys + tok < t.hi && !((bad >> (tok % 32)) & 1u);
+            const uint32_t at = part_at() + H::kCodes + tok * (D / 16) + q * (D / 64);
+            uint32_t bytes = D == 64 ? lds8(at) : D == 128 ? lds16(at) : lds32(at);
+            if (!seen) bytes = 0;
+            uint32_t two = 0;
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) {
+              if (k % 4 == 0) two = e4m3x2_to_f16(bytes >> (4 * k));
+              const uint32_t sc = k % 4 < 2 ? f16_low_twice(two) : f16_high_twice(two);
+              uint32_t h[4];
+              e2m1_to_f16(words[k], h);
+#pragma unroll
+              for (int m = 0; m < 4; ++m) h[m] = hmul2(h[m], sc);
+              stmatrix_trans(sm_v + st * H::kK + swizzled(32 * k + lane, eight, D), h);
+            }
+          }
+          ptx::fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(bars.v_full[st]));
+          part_done();
+        }
+      }
+    } else {
     // values: 64 tokens from v0, 64 channels from 64 * vq; lane's eight tokens
     // begin at vt, its 16 channels at 16 * vg. Eight neighbouring lanes have
     // different tokens and the same channels: their 16-byte stores fall on the
@@ -993,7 +1109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           if (bad) atomicOr(status, MOE_DEV_BAD_PAGE);
           // (with 64 keys, warps 2 and 3 see the same rows again)
-          *reinterpret_cast<volatile uint32_t*>(&s_bad[kc % kBadRing][fw]) = bad;
+          *reinterpret_cast<volatile uint32_t*>(&s_bad[kc % kBadTiles][fw]) = bad;
         }
         asm volatile("cp.async.wait_group 1;" ::: "memory");  // the keys, not the values
         __syncwarp();
@@ -1068,9 +1184,68 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
     if (!planned && warp == kMmaWarp + 1) pdl_enter();
+  }
+  if (kPart == kPrefix && warp == kMmaWarp + 2) {
+    // ------------------------------------------------------ the copying warp
+    // A tile lies on up to eight pages, one per lane: a bulk copy of the codes and
+    // one of the scales of keys, then of values.
+    const KvBlock blk = kv_block(a.page_size, D);
+    const int seg = min(a.page_size, kKeys), segs = kKeys / seg;
+    uint32_t issued = 0, kc = 0;
+    bool ok = true;
+    begin();
+    while (ok && next()) {
+      const int32_t* pages = a.page_table + static_cast<long>(t.sq.first_key) * a.max_pages;
+      auto page_of = [&](int j) {
+        const int key = (t.first + j) * kKeys + lane * seg;
+        return lane < segs && j < t.tiles && key < t.hi ? pages[key / a.page_size] : 0;
+      };
+      int id = page_of(0);
+#pragma unroll 1
+      for (int j = 0; ok && j < t.tiles; ++j, ++kc) {
+        const int key = (t.first + j) * kKeys + lane * seg;
+        const bool wanted = lane < segs && key < t.hi;
+        const bool good = wanted && id >= 0 && id < a.num_pages;
+        const unsigned bad = __ballot_sync(~0u, wanted && !good);
+        const int copies = __popc(__ballot_sync(~0u, good));
+        const uint8_t* block =
+            a.cache + (static_cast<long>(good ? id : 0) * a.kv_heads + t.kvh) * blk.bytes;
+        const int row = key & (a.page_size - 1);
+        id = page_of(j + 1);
+        if (bad && lane == 0) atomicOr(status, MOE_DEV_BAD_PAGE);
+        if (lane < 4) {  // 32 tokens each
+          uint32_t bits = 0;
+          for (int i = 0; i < segs; ++i)
+            if ((bad >> i) & 1u)
+              bits |= low_bits((i + 1) * seg - 32 * lane) & ~low_bits(i * seg - 32 * lane);
+          *reinterpret_cast<volatile uint32_t*>(&s_bad[kc % kBadTiles][lane]) = bits;
+        }
+        __syncwarp();
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v) {
+          const uint32_t slot = issued % kParts;
+          if (!(ok = wait_warp(bars.raw_empty[slot], ((issued / kParts) & 1) ^ 1))) break;
+          ++issued;
+          const uint32_t full = bar(bars.raw_full[slot]), dst = sm_raw + slot * H::kPartBytes;
+          if (lane == 0) ptx::mbar_arrive_expect_tx(full, copies * seg * (D / 2 + D / 16));
+          __syncwarp();
+          if (good) {
+            ptx::bulk_load(dst + lane * seg * (D / 2), block + (v ? blk.v_code : 0) + row * (D / 2),
+                           seg * (D / 2), full);
+            ptx::bulk_load(dst + H::kCodes + lane * seg * (D / 16),
+                           block + (v ? blk.v_scale : blk.k_scale) + row * (D / 16),
+                           seg * (D / 16), full);
+          }
+        }
+      }
+    }
+    // what was asked for has to land before the CTA's shared memory is given up
+    for (uint32_t i = issued > kParts ? issued - kParts : 0; i < issued; ++i)
+      ptx::mbar_wait_drain(bar(bars.raw_full[i % kParts]), (i / kParts) & 1);
   }
   if (warp == kMmaWarp) {
     // -------------------------------------------------------- the matrix warp

@@ -235,7 +235,7 @@ cudaError_t launch_prefix_split(const Launch& l) {
 template <int D>
 cudaError_t launch_prefix_prompt(const Launch& l) {
   auto* kern = &prompt::attn_prompt_kernel<D, kPrefix>;
-  constexpr int smem = prompt::Shape<D>::kBytes;
+  constexpr int smem = prompt::Shape<D>::kPrefixBytes;
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), smem, done);
   if (e != cudaSuccess) return e;
