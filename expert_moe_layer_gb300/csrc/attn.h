@@ -97,7 +97,13 @@ struct Groups {
   int max_len = 0;                   // query tokens
 };
 struct PrefixShape {
-  int tile_rows = 0, tile_keys = 0, setup = 0, min_tiles = 0, ctas = 0;
+  int tile_rows = 0, tile_keys = 0, ctas = 0;
+  int setup = 0, least = 0, unit = 1;  // list entries of a segment's set-up, of the smallest
+                                       // range of a CTA, of a key tile
+  // Prompt kernel with two halves: a half's rows. In row tiles of no more rows both
+  // halves take those rows, each every other tile of keys, and leave sums of their own;
+  // a key tile has half_unit entries then.
+  int half_rows = 0, half_unit = 1;
 };
 // Up to so many groups every CTA of the prefix kernel sums up the list itself, in
 // shared memory, while the plan kernel still works on the own kernel's.
@@ -113,7 +119,8 @@ struct PrefixHead {
 struct OwnPrefix {
   long base;  // first list entry of its group
   int tok0;   // its first query token within the group's
-  int len;    // list entries of a segment
+  int len, half_len;  // list entries of a segment, and with no more than half_rows rows
+  int rows;   // the group's rows
 };
 
 // The sums over shared prefixes. Segments that one CTA took leave each row in

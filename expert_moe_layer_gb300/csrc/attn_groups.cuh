@@ -29,8 +29,14 @@ struct GroupSmem {
   __device__ GroupLists lists() { return {offsets, limit, first, groups, bases}; }
 };
 
-__device__ __forceinline__ int prefix_entries(const PrefixShape& w, int tokens) {
-  return w.setup + (tokens + w.tile_keys - 1) / w.tile_keys;
+__device__ __forceinline__ int prefix_entries(const PrefixShape& w, int tokens, bool half) {
+  return w.setup + (tokens + w.tile_keys - 1) / w.tile_keys * (half ? w.half_unit : w.unit);
+}
+// Row tiles of a group; `half`: the last has no more than half_rows rows.
+__device__ __forceinline__ int row_tiles_of(const PrefixShape& w, int rows, bool& half) {
+  const int n = (rows + w.tile_rows - 1) / w.tile_rows;
+  half = n > 0 && rows - (n - 1) * w.tile_rows <= w.half_rows;
+  return n;
 }
 // a / b for values that hardly ever need 64 bits.
 __device__ __forceinline__ long quotient(long a, long b) {
@@ -39,7 +45,7 @@ __device__ __forceinline__ long quotient(long a, long b) {
 // Entries per CTA of a list.
 __device__ __forceinline__ long prefix_per(const PrefixShape& w, long entries) {
   const long per = quotient(entries + w.ctas - 1, w.ctas);
-  return per < w.min_tiles ? w.min_tiles : per;
+  return per < w.least ? w.least : per;
 }
 
 // The last of n ascending values that is at most v (0 where there is none).
@@ -122,7 +128,10 @@ __device__ __forceinline__ long plan_groups(const AttnArgs& a, const Groups& gr,
       l.limit[g] = p;
       l.groups[g] = s;
       const int rows = s.q_len * (a.heads / a.kv_heads);
-      n = static_cast<long>((rows + w.tile_rows - 1) / w.tile_rows * a.kv_heads) * prefix_entries(w, p);
+      bool half;
+      const int tiles = row_tiles_of(w, rows, half);
+      n = a.kv_heads * (static_cast<long>(tiles - half) * prefix_entries(w, p, false) +
+                        (half ? prefix_entries(w, p, true) : 0));
     }
     const long before = block_scan<N>(n, warp_sum, entries);
     if (g < gr.n) l.bases[g] = before;

@@ -28,6 +28,19 @@
 // rate. A tile takes about 4700 cycles of an SM, its matrix instructions 2500;
 // the fill warps work 4300 of them and a half's chain of S, softmax and P V
 // takes 4000, so both would have to become shorter at once.
+//
+// Over prefixes (kPrefix) the requests of a group are the rows, every row sees
+// every key, and a fifth kind of warp copies: whole parts, the codes and scales of a
+// tile's keys or of its values, by bulk copies into a ring of three. The fill warps
+// then only convert: keys with their chunks in an order of the lane's own, values
+// through transposing matrix stores, no bank conflicts in either; both take 1900
+// cycles of a tile. A tile of 256 rows takes 3900 cycles (4300 with the fill warps' own
+// copies): softmax 2300 and 1600 of waiting for S. The matrix unit and the fill warps
+// share the SM's shared memory, 2300 cycles of a tile at 128 bytes each, so that
+// products in smaller steps lose: the next tile's first 64 scores ahead of P V took
+// 4500 cycles, P V in two halves 4100. Of row tiles with no more than 128 rows both
+// halves take the same rows and every other key tile: 2900 cycles, where one half
+// alone takes 3900, and then the fill warps are the bound.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -326,6 +339,8 @@ struct Piece {
   int lo, hi;                      // keys [lo, hi) are seen by some row
   int first, tiles;                // its key tiles
   bool alone;                      // it is the whole segment
+  bool keys;                       // over prefixes: both halves have its rows, and every
+                                   // other tile each
   int cta0, cta1;                  // CTAs of the segment's pieces
   SeqInfo sq;
 };
@@ -396,15 +411,21 @@ struct Cursor {
   }
 };
 
-// The same over prefixes: all segments of a group have as many entries. A cut in
-// a segment's first kSetup entries, which stand for no tiles, moves to its begin;
-// near the end only one tile is not cut off, since joining pieces is cheap here
-// and a CTA with four tiles more holds up the others (56 us instead of 48, 256
-// rows over 32768 tokens).
-constexpr int kPrefixSnap = 1;
+// The same over prefixes: a group's segments have as many entries, but those of a
+// last row tile with one half's rows. There both halves take the same rows and every
+// other key tile, which then takes 1.4 us of an SM, and 1.9 with two halves' rows: three
+// entries, and four. (128 rows over 131072 tokens 103 us, and 121 with one half alone;
+// 384 rows 212 and 232. 256 rows over 32768 tokens pay for it with 1 of 56.)
+constexpr int kUnit = 4, kHalfUnit = 3;
+constexpr int kPrefixSetup = kSetup * kUnit;
+// A cut in a segment's set-up entries, which stand for no tiles, moves to its begin;
+// near the end only one tile is not cut off, since joining pieces is cheap here and a
+// CTA with four tiles more holds up the others (56 us instead of 48, 256 rows over
+// 32768 tokens).
+constexpr int kPrefixSnap = kUnit;
 // Smallest range of a CTA: pieces of two tiles.
-constexpr int kMinPrefix = 2;
-static_assert(kMinPrefix > kPrefixSnap, "cuts do not cross");
+constexpr int kMinPrefix = 2 * kUnit;
+static_assert(kMinPrefix >= kPrefixSnap + kUnit, "cuts do not cross, pieces have tiles");
 template <int D>
 struct PrefixCursor {
   using H = Shape<D>;
@@ -427,29 +448,44 @@ struct PrefixCursor {
       if (at >= end) return false;
       while (bases[g + 1] <= at) ++g;
       p.sq = groups[g];
-      const int len = kSetup + (p.sq.len + H::kKeys - 1) / H::kKeys;
-      const int i = static_cast<int>(quotient(at - bases[g], len)), row_tile = i / a.kv_heads;
-      p.kvh = i - row_tile * a.kv_heads;
-      p.row0 = row_tile * H::kTile;
       p.rows = p.sq.q_len * (a.heads / a.kv_heads);
-      p.halves = min(p.rows, p.row0 + H::kTile) > p.row0 + kHalf ? 2 : 1;
+      const int key_tiles = (p.sq.len + H::kKeys - 1) / H::kKeys;
+      int len = kPrefixSetup + key_tiles * kUnit;
+      const int i = static_cast<int>(quotient(at - bases[g], len));
+      const int row_tile = i / a.kv_heads;  // (also in a last one of shorter segments)
+      p.row0 = row_tile * H::kTile;
+      p.halves = p.rows - p.row0 > kHalf ? 2 : 1;
+      p.kvh = i - row_tile * a.kv_heads;
+      long seg = bases[g] + static_cast<long>(i) * len;
+      const bool shorter = H::kHalves == 2 && p.halves == 1;
+      if (shorter) {
+        seg -= static_cast<long>(p.kvh) * len;
+        len = kPrefixSetup + key_tiles * kHalfUnit;
+        p.kvh = static_cast<int>(quotient(at - seg, len));
+        seg += static_cast<long>(p.kvh) * len;
+      }
       p.lo = 0;
       p.hi = p.sq.len;
-      const long seg = bases[g] + static_cast<long>(i) * len;
       int p0 = static_cast<int>(at - seg);
-      if (p0 <= kSetup) {
+      if (p0 <= kPrefixSetup) {
         p0 = 0;
       } else if (len - p0 <= kPrefixSnap) {  // the CTA before takes all of it
         at = seg + len;
         continue;
       }
       int p1 = static_cast<int>(min(static_cast<long>(len), end - seg));
-      if (p1 < len && p1 <= kSetup) return false;  // the next CTA takes all of it
+      if (p1 < len && p1 <= kPrefixSetup) return false;  // the next CTA takes all of it
       if (len - p1 <= kPrefixSnap) p1 = len;
-      p.first = max(0, p0 - kSetup);
-      p.tiles = p1 - kSetup - p.first;
+      // the tiles whose first entry lies between the cuts
+      auto tiles_to = [&](int entry) {
+        const unsigned e = max(0, entry - kPrefixSetup);
+        return static_cast<int>(shorter ? (e + kHalfUnit - 1) / kHalfUnit : (e + kUnit - 1) / kUnit);
+      };
+      p.first = tiles_to(p0);
+      p.tiles = tiles_to(p1) - p.first;
       p.alone = p0 == 0 && p1 == len;
-      p.cta0 = static_cast<int>(quotient(seg + kSetup, per));
+      p.keys = H::kHalves == 2 && p.halves == 1 && p.tiles > 1 && !p.alone;
+      p.cta0 = static_cast<int>(quotient(seg + kPrefixSetup, per));
       at = seg + p1;
       return true;
     }
@@ -553,6 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       return cur.next(a, info, row_tiles, starts, t);
   };
 
+  auto by_keys = [&] { return kPart == kPrefix && t.keys; };
+
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ---------------------------------------------------------------- softmax
@@ -568,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool live;
     float gain = 0.0f;
     auto place = [&] {
-      r = t.row0 + x * kHalf + row_l;
+      r = t.row0 + (by_keys() ? 0 : x * kHalf) + row_l;
       live = r < t.rows;
       tok = r / group;
       head = t.kvh * group + (r - tok * group);
@@ -576,8 +614,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The next piece with keys for this half; what has none is zeroed.
     auto advance = [&] {
       while (next()) {
-        if (x >= t.halves) {
+        if (x >= t.halves && !by_keys()) {
           tile_no += t.tiles;
+          if constexpr (kPart == kPrefix) {
+            if (!t.alone) {  // a single tile: nothing is left for this half
+              const long row = (2l * blockIdx.x + (blockIdx.x == t.cta0)) * H::kTile + kHalf + row_l;
+              stats[row] = make_float2(-INFINITY, 0.0f);
+              for (int i = 0; i < D / 4; ++i)
+                partial[sums_at(row, i, D / 4)] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+          }
           continue;
         }
         place();
@@ -680,22 +726,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r_lo = t.row0 + x * kHalf, r_hi = min(t.rows, r_lo + kHalf) - 1;
       const int all_last = kPart == kPrefix ? t.sq.len - 1 : t.sq.len - t.sq.q_len + r_lo / group;
       const int all_first = a.window > 0 ? t.sq.len - t.sq.q_len + r_hi / group - a.window + 1 : 0;
-      const bool frees = x == t.halves - 1 && threadIdx.x % 128 == 0;
+      const bool keys = by_keys();
+      const bool frees = (keys || x == t.halves - 1) && threadIdx.x % 128 == 0;
       float m = -INFINITY, mbase = -kLift;  // m: a whole number
       uint64_t l2[2] = {0, 0};              // partial sums of P
       const uint64_t gain2 = pair_f32(gain, gain);
       bool ok = true;
+      const uint32_t tile0 = tile_no;
+      const int step = keys ? 2 : 1;
 #pragma unroll 1
-      for (int j = 0; j < t.tiles; ++j, ++tile_no) {
+      for (int j = keys ? x : 0; j < t.tiles; j += step) {
+        tile_no = tile0 + j;
         if (!(ok = wait_warp(bars.s_full[x], s_phase))) break;
         s_phase ^= 1;
         ptx::tc_fence_after();
         // This half's scores are the tile's last ones: the keys are free, and the
         // values of the tile before, whose products were issued earlier. (A
-        // commit for each would hold up the matrix thread.)
+        // commit for each would hold up the matrix thread; where the halves take
+        // tiles in turn there is one for each, since a half's next scores come late.)
         if (frees) {
           ptx::mbar_arrive(bar(bars.k_empty[tile_no & 1]));
-          if (j > 0) ptx::mbar_arrive(bar(bars.v_empty[(tile_no - 1) & 1]));
+          if (j > 0 && !keys) ptx::mbar_arrive(bar(bars.v_empty[(tile_no - 1) & 1]));
         }
         const int tok0 = (t.first + j) * kKeys;
         const uint32_t bad_at = ptx::smem_u32(s_bad[tile_no % kBadTiles]);
@@ -761,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               tmem_st32(ts, w);
             }
-            if (j > 0) {  // the products of the tiles before have landed (s_full)
+            if (j >= step) {  // the products of the tiles before have landed (s_full)
 #pragma unroll 1
               for (int q = 0; q < D / 32; ++q) {
                 uint32_t w[32];
@@ -788,12 +839,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long at_row = static_cast<long>(t.sq.q0 + tok) * a.heads + head;
       const bool there = live, alone = t.alone;
       const int cta0 = t.cta0, cta1 = t.cta1;
+      tile_no = tile0 + t.tiles;
       const uint32_t last_tile = tile_no - 1;
       more = advance();
       if (more) load_queries();
       if (!wait_warp(bars.o_done[x], o_phase)) break;
       o_phase ^= 1;
-      if (frees) ptx::mbar_arrive(bar(bars.v_empty[last_tile & 1]));
+      if (frees && !keys) ptx::mbar_arrive(bar(bars.v_empty[last_tile & 1]));
       ptx::tc_fence_after();
       float l;
       {
@@ -1271,10 +1323,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (next()) {
       const int halves = __shfl_sync(~0u, t.halves, 0), tiles = __shfl_sync(~0u, t.tiles, 0);
       if (tiles == 0) continue;
+      const bool keys = kPart == kPrefix && __shfl_sync(~0u, static_cast<int>(by_keys()), 0);
+      const int both = keys ? 2 : halves;
       bool ok = true;
 #pragma unroll 1
-      for (int x = 0; ok && x < halves; ++x) ok = wait_warp(bars.q_ready[x], (q_phase >> x) & 1);
-      q_phase ^= (1u << halves) - 1u;
+      for (int x = 0; ok && x < both; ++x) ok = wait_warp(bars.q_ready[x], (q_phase >> x) & 1);
+      q_phase ^= (1u << both) - 1u;
+      if constexpr (kPart == kPrefix) {
+        if (keys) {
+          // scores of the first two tiles, then P V of a tile and the scores of the
+          // next but one, by the halves in turn: two chains that overlap
+          for (int j = 0; ok && j < 2; ++j) {
+            const uint32_t n = kc + j;
+            if (!(ok = wait_warp(bars.k_full[n & 1], (n >> 1) & 1))) break;
+            ptx::tc_fence_after();
+            scores(j, n & 1);
+          }
+#pragma unroll 1
+          for (int j = 0; ok && j < tiles; ++j) {
+            const uint32_t n = kc + j, st = n & 1, x = j & 1;
+            if (!(ok = wait_warp(bars.v_full[st], (n >> 1) & 1) &&
+                       wait_warp(bars.p_ready[x], (p_phase >> x) & 1)))
+              break;
+            p_phase ^= 1u << x;
+            ptx::tc_fence_after();
+            const uint64_t db = ptx::sdesc_sw128(sm_v + st * H::kK);
+            const uint32_t d = tmem + kColsO + x * D, p = tmem + kColsS + x * kKeys;
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                mma_ts(d, p + kk * 8, db + (kk / 4) * (D * 8) + (kk % 4) * 2, id_o, j / 2 + kk > 0);
+              ptx::tc_commit(bar(bars.v_empty[st]));
+              if (j + 2 >= tiles) ptx::tc_commit(bar(bars.o_done[x]));
+            }
+            __syncwarp();
+            if (j + 2 < tiles) {
+              if (!(ok = wait_warp(bars.k_full[st], ((n + 2) >> 1) & 1))) break;
+              ptx::tc_fence_after();
+              scores(x, st);
+            }
+          }
+          if (!ok) break;
+          kc += tiles;
+          continue;
+        }
+      }
       ok = ok && wait_warp(bars.k_full[kc & 1], (kc >> 1) & 1);
       if (!ok) break;
       ptx::tc_fence_after();

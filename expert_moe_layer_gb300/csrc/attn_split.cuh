@@ -211,31 +211,35 @@ __device__ __forceinline__ void load_values(ValueRegs<D>& t, const uint8_t* stag
 
 // Where the sums of one of a request's rows over the shared prefix lie: n pieces
 // in slots of CTAs that follow one another (two slots each; the first one's piece
-// is in its second), or one whole row (n 1, no slots between).
+// is in its second), or one whole row (n 1, no slots between). With `twice` 1, a
+// slot has two parts of a piece, one after the other, and n counts parts.
 struct RowPieces {
   const float2* stat;
   const float4* sum;
-  int n, slot_rows;
+  int n, part_rows, twice;
 };
 __device__ __forceinline__ RowPieces find_pieces(const PrefixSums& p, long per, const OwnPrefix& own,
                                                  int at, int kvh, int kv_heads, long at_row,
                                                  int chunks) {
-  if (own.len == 0) return {nullptr, nullptr, 0, 0};
+  if (own.len == 0) return {nullptr, nullptr, 0, 0, 0};
   const int tile = at / p.shape.tile_rows, r = at - tile * p.shape.tile_rows;
-  const long seg = own.base + (static_cast<long>(tile) * kv_heads + kvh) * own.len;
-  const long cta0 = quotient(seg + p.lo, per), cta1 = quotient(seg + own.len - p.hi, per);
-  if (cta1 <= cta0) return {p.row_stats + at_row, p.row_sums + sums_at(at_row, 0, chunks), 1, 0};
+  const bool half = own.rows - tile * p.shape.tile_rows <= p.shape.half_rows;  // the last one
+  const int len = half ? own.half_len : own.len;
+  const long seg = own.base + static_cast<long>(tile) * kv_heads * own.len + static_cast<long>(kvh) * len;
+  const long cta0 = quotient(seg + p.lo, per), cta1 = quotient(seg + len - p.hi, per);
+  if (cta1 <= cta0) return {p.row_stats + at_row, p.row_sums + sums_at(at_row, 0, chunks), 1, 0, 0};
   const long rows = 2 * cta0 * p.shape.tile_rows;
   return {p.stats + rows + r, p.sums + rows * chunks + sums_at(r, 0, chunks),
-          static_cast<int>(cta1 - cta0) + 1, p.shape.tile_rows};
+          static_cast<int>(cta1 - cta0 + 1) << half, half ? p.shape.half_rows : p.shape.tile_rows,
+          half};
 }
 
 // Four channels (chunk c) of those sums, pieces in CTA order, added to the row's own.
 __device__ __forceinline__ void add_pieces(const RowPieces& p, int chunks, int c, float4& sum,
                                            float& top, float& den) {
   constexpr int kBatch = 10;  // pieces asked for together
-  const int n = p.n;
-  const long rows = p.slot_rows, slot = rows * chunks;
+  const int n = p.n, twice = p.twice;
+  const long rows = p.part_rows, slot = rows * chunks;
   const float2* stat = p.stat;
   const float4* v0 = p.sum + 8 * c;
   for (int k0 = 0; k0 < n; k0 += kBatch) {
@@ -247,9 +251,10 @@ __device__ __forceinline__ void add_pieces(const RowPieces& p, int chunks, int c
       st[i] = make_float2(-INFINITY, 0.0f);
       v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (k < n) {
-        const long at_slot = 2l * k + (k == 0);
-        st[i] = __ldcg(stat + at_slot * rows);
-        v[i] = __ldcg(v0 + at_slot * slot);
+        // slot 2 (k >> twice), and 1 instead of 0, part k & twice
+        const int at = 2 * k - (k & twice) + (i <= 1 && k <= twice ? 1 + twice : 0);
+        st[i] = __ldcg(stat + at * rows);
+        v[i] = __ldcg(v0 + at * slot);
       }
     }
     float most = top;

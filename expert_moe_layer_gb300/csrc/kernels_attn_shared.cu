@@ -10,6 +10,16 @@
 // leaves its pieces' sums in fp32 and joins nothing. The split kernel over the
 // own keys then adds them to each row as it stores it: that join is spread over
 // all CTAs, where the last CTA of a segment would do it for a whole row tile.
+//
+// Three kernels: the plan (one block, the lists of the own kernel), the prefix kernel,
+// which sums up its own list in every CTA and so begins beside the plan, and the own
+// kernel, which goes through its keys before it waits for the prefix sums.
+//
+// Measured, 32 query and 8 kv heads of 128: 64 requests behind 32768 tokens with up
+// to 1024 of their own 56 us, from a kernel's start: lists 2.3, first product at 9,
+// 13.5 tiles of 1.9 us, sums out 2.4, own keys 5 to 11, sums in 4. Three groups of 48
+// requests with 2 query tokens behind 20000 to 65535 tokens 249 us, 0.71 PFLOP/s, 37 %
+// of the measured matrix rate (every other row tile there is half empty).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -98,8 +108,9 @@ __global__ void __launch_bounds__(kPlanThreads)
       s.first_key = p;
       info[b] = s;
       if (few_seqs) o.info[b] = s;
-      o.own[b] = p > 0 ? OwnPrefix{l.bases[g], s.q0 - l.groups[g].q0, prefix_entries(w, p)}
-                       : OwnPrefix{0, 0, 0};
+      o.own[b] = p > 0 ? OwnPrefix{l.bases[g], s.q0 - l.groups[g].q0, prefix_entries(w, p, false),
+                                   prefix_entries(w, p, true), l.groups[g].q_len * heads}
+                       : OwnPrefix{0, 0, 0, 0, 0};
       n = segments(s.q_len);
       own_tiles = n > 0 ? tiles_of(s) : 0;
     }
@@ -263,11 +274,13 @@ cudaError_t launch_dim(const moe_attn_config* c, Launch& l) {
   if (by_prompt) {
     using H = prompt::Shape<D>;
     w.tile_rows = H::kTile, w.tile_keys = H::kKeys;
-    w.setup = prompt::kSetup, w.min_tiles = prompt::kMinPrefix, w.ctas = l.a.sms;
-    l.sums.lo = prompt::kSetup, l.sums.hi = prompt::kPrefixSnap + 1;
+    w.setup = prompt::kPrefixSetup, w.least = prompt::kMinPrefix, w.ctas = l.a.sms;
+    w.unit = prompt::kUnit, w.half_unit = prompt::kHalfUnit;
+    w.half_rows = H::kHalves == 2 ? prompt::kHalf : 0;
+    l.sums.lo = prompt::kPrefixSetup, l.sums.hi = prompt::kPrefixSnap + 1;
   } else {
     w.tile_rows = prefix_rows(bf16), w.tile_keys = split::kTile;
-    w.setup = split::kSetup, w.min_tiles = split::kMinTiles;
+    w.setup = split::kSetup, w.least = split::kMinTiles;
     w.ctas = l.a.sms * (bf16 ? split::ctas_per_sm<D, prefix_rows(true), 1>()
                              : split::ctas_per_sm<D, prefix_rows(false), 2>());
     l.sums.lo = split::kSetup - 1, l.sums.hi = 1;
