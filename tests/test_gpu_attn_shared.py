@@ -115,6 +115,30 @@ def test_long_prefixes_are_cut_into_pieces(dtype, heads, kv, D, n, q):
         assert torch.equal(c.out, first)
 
 
+@pytest.mark.parametrize("D,heads,kv,groups", [
+    (128, 8, 4, [(2, 17, 31), (4, 45, 12), (2, 32, 23)]),            # pieces of one tile, of odd numbers
+    (64, 8, 4, [(2, 17, 30), (2, 25, 25), (4, 45, 17), (2, 32, 9)]),
+    (128, 16, 8, [(2, 17 + i % 9, 1 + i % 5) for i in range(30)]),   # several segments to a CTA
+])
+def test_row_tiles_with_half_their_rows(D, heads, kv, groups):
+    """Groups of (requests, query tokens of each, tiles of 128 prefix tokens) whose last
+    row tile has no more than 128 of its 256 rows, beside full ones."""
+    lens, qs, bounds, prefix = [], [], [0], []
+    for g, (n, q, tiles) in enumerate(groups):
+        prefix.append(128 * tiles - 32 * (g % 4))
+        lens += [prefix[-1] + q + 5 * i for i in range(n)]
+        qs += [q] * n
+        bounds.append(bounds[-1] + n)
+    c = Shared(90 + D, "bf16", heads, kv, D, 64, lens, qs, bounds, prefix).shared()
+    assert c.status() == (0, 0)
+    c.check()
+    first = c.out.clone(), c.lse.clone()
+    for _ in range(3):
+        c.sws.fill_(0xff)
+        c.shared()
+        assert torch.equal(c.out, first[0]) and torch.equal(c.lse, first[1])
+
+
 @pytest.mark.parametrize("dtype,n", [("bf16", 3), ("bf16", 20), ("f32", 3)])
 def test_prefixes_reach_no_further_than_the_requests(dtype, n):
     """The prefix is cut to what every request has before its queries."""
