@@ -454,7 +454,7 @@ struct PrefixCursor {
       const int i = static_cast<int>(quotient(at - bases[g], len));
       const int row_tile = i / a.kv_heads;  // (also in a last one of shorter segments)
       p.row0 = row_tile * H::kTile;
-      p.halves = p.rows - p.row0 > kHalf ? 2 : 1;
+      p.halves = H::kHalves == 2 && p.rows - p.row0 > kHalf ? 2 : 1;
       p.kvh = i - row_tile * a.kv_heads;
       long seg = bases[g] + static_cast<long>(i) * len;
       const bool shorter = H::kHalves == 2 && p.halves == 1;

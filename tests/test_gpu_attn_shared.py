@@ -119,10 +119,11 @@ def test_long_prefixes_are_cut_into_pieces(dtype, heads, kv, D, n, q):
     (128, 8, 4, [(2, 17, 31), (4, 45, 12), (2, 32, 23)]),            # pieces of one tile, of odd numbers
     (64, 8, 4, [(2, 17, 30), (2, 25, 25), (4, 45, 17), (2, 32, 9)]),
     (128, 16, 8, [(2, 17 + i % 9, 1 + i % 5) for i in range(30)]),   # several segments to a CTA
+    (256, 8, 4, [(4, 45, 9), (2, 32, 12), (3, 43, 5)]),              # row tiles of 128 rows
 ])
 def test_row_tiles_with_half_their_rows(D, heads, kv, groups):
     """Groups of (requests, query tokens of each, tiles of 128 prefix tokens) whose last
-    row tile has no more than 128 of its 256 rows, beside full ones."""
+    row tile has no more than 128 of its 256 rows (or 128), beside full ones."""
     lens, qs, bounds, prefix = [], [], [0], []
     for g, (n, q, tiles) in enumerate(groups):
         prefix.append(128 * tiles - 32 * (g % 4))
