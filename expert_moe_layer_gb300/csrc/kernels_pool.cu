@@ -218,16 +218,22 @@ __device__ __forceinline__ Span span_of(const PoolArgs& a, int i, const int32_t*
   s.ok = s.held >= 0 && s.held <= a.max_pages;
   return s;
 }
-__device__ __forceinline__ bool shared_page(const PoolArgs& a, int page, unsigned& flags) {
+// Entries that are to be replaced are marked in the table: page p as -2 - p.
+// (What is decided here by counts that the second kernel changes.)
+__device__ __forceinline__ bool is_mark(const PoolArgs& a, int entry) {
+  return entry <= -2 && entry >= -1 - a.pages;
+}
+// Whether an entry's page has other holders. One that reads as a mark becomes -1.
+__device__ __forceinline__ bool shared_page(const PoolArgs& a, int32_t* entry, int page,
+                                            unsigned& flags) {
   if (page < 0 || page >= a.pages) {
     flags |= MOE_DEV_BAD_PAGE;
+    if (is_mark(a, page)) *entry = -1;
     return false;
   }
   return a.refs[page] > 1;
 }
 
-// Entries that are to be replaced are marked in the table: page p as -2 - p.
-// (What is decided here by counts that the second kernel changes.)
 __global__ void __launch_bounds__(kScanThreads)
     reserve_plan_kernel(PoolArgs a, Work w, int n, const int32_t* rows, const int32_t* start,
                         const int32_t* end) {
@@ -266,7 +272,7 @@ __global__ void __launch_bounds__(kScanThreads)
     const bool cut = s.ok && (start[i] & ((1 << a.page_shift) - 1)) != 0;  // the first page keeps tokens
     if (s.ok && s.lo < stop) {
       const int page = entries[s.lo];
-      if (shared_page(a, page, flags)) {
+      if (shared_page(a, entries + s.lo, page, flags)) {
         marked = 1;
         entries[s.lo] = -2 - page;
         if (cut) old = page;
@@ -280,7 +286,7 @@ __global__ void __launch_bounds__(kScanThreads)
       int count = 0;
       for (int e = lo + lane; e < hi; e += 32) {
         const int page = row[e];
-        if (!shared_page(a, page, flags)) continue;
+        if (!shared_page(a, row + e, page, flags)) continue;
         row[e] = -2 - page;
         ++count;
       }
@@ -376,7 +382,7 @@ __global__ void __launch_bounds__(kApplyThreads)
       for (int e0 = s.lo; e0 < min(s.hi, s.held); e0 += 32) {
         const int e = e0 + lane;
         const int v = e < min(s.hi, s.held) ? entries[e] : -1;
-        const bool marked = v <= -2;
+        const bool marked = is_mark(a, v);
         const unsigned mask = __ballot_sync(~0u, marked);
         if (marked && served) {
           const int page = free_page(f, rank + __popc(mask & ((1u << lane) - 1u)));

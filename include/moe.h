@@ -701,7 +701,8 @@ MOE_API int moe_kv_attention_shared(const moe_attn_config* cfg, int num_seqs, in
  * given in device arrays of int32 [n]; n may be up to 2^18. An item that does
  * not fit (see each call) changes nothing, sets MOE_DEV_BAD_ROW, and leaves the
  * others as they are. An entry outside [0, num_pages) among those held, or a
- * count that would fall below 0, sets MOE_DEV_BAD_PAGE and is passed over. */
+ * count that would fall below 0, sets MOE_DEV_BAD_PAGE and is passed over
+ * (moe_kv_reserve may leave -1 in the place of such an entry). */
 #define MOE_KV_MAX_CACHES 256
 
 typedef struct {
@@ -839,9 +840,10 @@ MOE_API int moe_get_status(const void* ws, void* stream, uint32_t* flags);
  * top-k ids against E. A failed check skips the
  * access or clamps the value into range (the outputs are then unusable) and
  * is counted in a device record, which also keeps the site, index and bound
- * of the first failure. The attention calls have no such checks: what they
- * read from a caller (positions, slots, page ids, offsets, lengths) is checked
- * in libmoe.so already. Same entry points and results otherwise; slower. */
+ * of the first failure. The attention calls and those on pages have no such
+ * checks: what they read from a caller (positions, slots, rows, page ids,
+ * offsets, lengths) is checked in libmoe.so already; norms read no indices.
+ * Same entry points and results otherwise; slower. */
 typedef struct {
   uint32_t count; /* failed check evaluations since the last take (one bad
                      value may be checked, and counted, several times)      */

@@ -82,6 +82,8 @@ class Pool:
                 page = self.table[r, e]
                 if not self._page_ok(page):
                     flags |= BAD_PAGE
+                    if -1 - len(refs) <= page <= -2:
+                        self.table[r, e] = -1
                 elif refs[page] > 1:
                     own.append(e)
             places = own + list(range(held[r], hi))

@@ -191,6 +191,24 @@ def test_bad_entries_and_counts_are_flagged_and_left():
     p.check()
 
 
+@pytest.mark.parametrize("start", [0, 20])
+def test_bad_entries_between_pages_that_are_replaced(start):
+    """Whatever stands in an entry, only pages of the pool are taken, counted or copied."""
+    p = Pool(rows=3, width=16, pages=40)
+    p.reserve([0], [0], [256])
+    p.fork([0], [1], [256])
+    for e, bad in ((0, -3), (2, -2), (4, -41), (6, -42), (8, -2 ** 31), (10, 2 ** 31 - 1), (12, -30), (13, 40)):
+        p.o.table[1, e] = bad
+    p.load()
+    p.reserve([1], [start], [256])
+    p.check()
+    p.o.table[0, 3], p.o.table[0, 5] = -4, -2 ** 31 + 1         # of an item that finds too few pages
+    p.o.refs[:] = np.maximum(p.o.refs, 1)
+    p.load()
+    p.reserve([0], [0], [256])
+    p.check()
+
+
 def test_page_calls_in_a_graph():
     """Captured once, replayed on other states: the same as eager calls."""
     p, q = (Pool(rows=8, width=12, pages=9000, seed=5) for _ in range(2))
