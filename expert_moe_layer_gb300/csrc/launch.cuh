@@ -15,6 +15,10 @@
 // everything that its call was handed (lengths, page ids, queries, the cache):
 // the kernel before it is the call's own, which only clears the status and the
 // counters, and what the caller enqueued ended before that one began.
+// With a shared prefix it is the same with both kernels behind the plan: the one
+// over prefixes sums up its own list from what the call was handed, and the one
+// over own keys reads the plan's list, written two kernels before it; the plan lets
+// its dependents go only after its own wait, and each of the two waits before it ends.
 #pragma once
 
 #include <cuda_runtime.h>
