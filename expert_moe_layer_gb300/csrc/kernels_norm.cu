@@ -301,9 +301,10 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : kMostThreads, 
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Rows that begin at chunks (16 bytes of the wider type) and have whole ones: straight from memory into registers, the next row's chunks under way while
-// a row is summed up. A thread has the same channels of every row and keeps their
-// weights and, where all rows share them, their gates. kChunks: chunks per thread.
+// Rows that begin at chunks (16 bytes of the wider type) and have whole ones: straight
+// from memory into registers, the next row's chunks under way while a row is summed up.
+// A thread has the same channels of every row and keeps their weights and, where all
+// rows share them, their gates. kChunks: chunks per thread.
 template <typename T, int V>
 struct Raw {
   uint32_t w[V * static_cast<int>(sizeof(T)) / 4];
