@@ -357,9 +357,17 @@ __host__ __device__ constexpr int chunk_of() {
   return 16 / static_cast<int>(sizeof(TA) > sizeof(TR) ? sizeof(TA) : sizeof(TR));
 }
 
-template <typename TA, typename TR, int kChunks, bool kWarpRow, bool kPost>
-__global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : kMostKeep,
-                                  kWarpRow ? (kPost ? 4 : 5) : 1)
+//
+// kTwo: two blocks an SM of up to kTwoThreads threads, where there are rows for more
+// than that, for bf16 activations normed once: one row under way is too few bytes then
+// (8192 rows of 5120 with a bf16 residual 51.4 us instead of 63.4, gated by element 62.8
+// instead of 74.5, of 2880 34.0 instead of 37.5, with an fp32 residual 81 instead of 85;
+// of 4096 45.8 and 45.0). fp32 rows of 5120 lose, 57.0 instead of 55.5, and rows normed on both
+// sides, whose weights then spill (of 2048 29.9 instead of 23.2, of 5120 70.4 and 68.9).
+constexpr int kTwoThreads = 320;
+template <typename TA, typename TR, int kChunks, bool kWarpRow, bool kPost, bool kTwo = false>
+__global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : kTwo ? kTwoThreads : kMostKeep,
+                                  kWarpRow ? (kPost ? 4 : 5) : kTwo ? 2 : 1)
     norm_whole_kernel(NormArgs a) {
   constexpr int V = chunk_of<TA, TR>();
   __shared__ float s_sum[2][32];
@@ -504,12 +512,12 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : kMostKeep,
   }
 }
 
-template <typename TA, typename TR, int kChunks, bool kWarpRow, bool kPost>
+template <typename TA, typename TR, int kChunks, bool kWarpRow, bool kPost, bool kTwo = false>
 cudaError_t launch_whole(const NormArgs& a, int sms, cudaStream_t st) {
   constexpr int kWarp = 32 * chunk_of<TA, TR>() * kChunks;
   const int threads = kWarpRow ? 32 * kRowsPerBlock : (a.H + kWarp - 1) / kWarp * 32;
   const int rows = kWarpRow ? kRowsPerBlock : 1;
-  auto* kern = &norm_whole_kernel<TA, TR, kChunks, kWarpRow, kPost>;
+  auto* kern = &norm_whole_kernel<TA, TR, kChunks, kWarpRow, kPost, kTwo>;
   // as many blocks as an SM holds, by size (0: not asked yet)
   static std::atomic<int> held[kMostKeep / 32 + 1] = {};
   int blocks = held[threads / 32].load(std::memory_order_relaxed);
@@ -577,6 +585,9 @@ cudaError_t launch_types(const NormArgs& a, int sms, cudaStream_t st) {
     if (a.H <= 32 * 16)
       return post ? launch_whole<TA, TR, kRow, true, true>(a, sms, st)
                   : launch_whole<TA, TR, kRow, true, false>(a, sms, st);
+    if constexpr (sizeof(TA) == 2)
+      if (a.H <= kTwoThreads * 16 && !post && a.T > 2 * sms)
+        return launch_whole<TA, TR, kRow, false, false, true>(a, sms, st);
     if (a.H <= kMostKeep * 16)
       return post ? launch_whole<TA, TR, kRow, false, true>(a, sms, st)
                   : launch_whole<TA, TR, kRow, false, false>(a, sms, st);

@@ -287,6 +287,8 @@ NORMS = [  # T, H, act, residual, kind, post, gate, strided
     (9000, 333, "bf16", "bf16", "rms", True, "full", 3), (1100, 4100, "bf16", "bf16", "rms", False, "none", False),
     (900, 12288, "bf16", "bf16", "rms", True, "channel", False), (400, 16383, "f32", "f32", "layer", True, "none", False),
     (2000, 1000, "f32", "bf16", "rms", False, "full", 3),
+    (700, 4096, "bf16", "f32", "layer", False, "full", True), (640, 5120, "bf16", "bf16", "rms", False, "channel", False),
+    (305, 1536, "bf16", "bf16", "layer", False, "full", False),
 ]
 
 
