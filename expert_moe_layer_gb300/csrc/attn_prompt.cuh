@@ -589,7 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       return cur.next(a, info, row_tiles, starts, t);
   };
 
-  auto by_keys = [&] { return kPart == kPrefix && t.keys; };
+  constexpr bool kByKeys = kPart == kPrefix && H::kHalves == 2;
+  auto by_keys = [&] { return kByKeys && t.keys; };
 
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
@@ -616,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (next()) {
         if (x >= t.halves && !by_keys()) {
           tile_no += t.tiles;
-          if constexpr (kPart == kPrefix) {
+          if constexpr (kByKeys) {
             if (!t.alone) {  // a single tile: nothing is left for this half
               const long row = (2l * blockIdx.x + (blockIdx.x == t.cta0)) * H::kTile + kHalf + row_l;
               stats[row] = make_float2(-INFINITY, 0.0f);
@@ -1323,13 +1324,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (next()) {
       const int halves = __shfl_sync(~0u, t.halves, 0), tiles = __shfl_sync(~0u, t.tiles, 0);
       if (tiles == 0) continue;
-      const bool keys = kPart == kPrefix && __shfl_sync(~0u, static_cast<int>(by_keys()), 0);
+      const bool keys = kByKeys && __shfl_sync(~0u, static_cast<int>(by_keys()), 0);
       const int both = keys ? 2 : halves;
       bool ok = true;
 #pragma unroll 1
       for (int x = 0; ok && x < both; ++x) ok = wait_warp(bars.q_ready[x], (q_phase >> x) & 1);
       q_phase ^= (1u << both) - 1u;
-      if constexpr (kPart == kPrefix) {
+      if constexpr (kByKeys) {
         if (keys) {
           // scores of the first two tiles, then P V of a tile and the scores of the
           // next but one, by the halves in turn: two chains that overlap
