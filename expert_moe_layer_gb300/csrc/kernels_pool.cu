@@ -574,7 +574,10 @@ __global__ void __launch_bounds__(kApplyThreads)
 }
 
 // A block per item takes the entries between what the row is to keep and what
-// it held; of items with the same row each takes the part that it finds.
+// it held; of items with the same row each takes the part that it finds. A count
+// is lowered by compare and swap, since one that lies outside the table has to
+// stay (a minimum would have changed it before anyone saw it: what such a row
+// names may be other rows' pages).
 __global__ void __launch_bounds__(kApplyThreads)
     release_kernel(PoolArgs a, int n, const int32_t* rows, const int32_t* keep) {
   __shared__ int s_held;
@@ -589,12 +592,22 @@ __global__ void __launch_bounds__(kApplyThreads)
     }
     const int left = min(entries_of(a, t), a.max_pages);
     __syncthreads();
-    if (threadIdx.x == 0) s_held = atomicMin(a.held + row, left);
+    if (threadIdx.x == 0) {
+      int held = __ldcg(a.held + row);
+      while (held > left && held <= a.max_pages) {
+        const int found = atomicCAS(a.held + row, held, left);
+        if (found == held) break;
+        held = found;
+      }
+      s_held = held;
+    }
     __syncthreads();
-    const int held = s_held;
-    if (held < 0 || held > a.max_pages) flags |= MOE_DEV_BAD_ROW;
+    const int stop = s_held;
+    if (stop < 0 || stop > a.max_pages) {
+      flags |= MOE_DEV_BAD_ROW;
+      continue;
+    }
     int32_t* entries = a.table + static_cast<long>(row) * a.max_pages;
-    const int stop = min(held, a.max_pages);
     for (int e0 = left + threadIdx.x; e0 < stop; e0 += kAhead * kApplyThreads) {
       int page[kAhead];
 #pragma unroll

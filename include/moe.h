@@ -700,7 +700,8 @@ MOE_API int moe_kv_attention_shared(const moe_attn_config* cfg, int num_seqs, in
  * comes out does not depend on the order in which the GPU runs it. n items are
  * given in device arrays of int32 [n]; n may be up to 2^18. An item that does
  * not fit (see each call) changes nothing, sets MOE_DEV_BAD_ROW, and leaves the
- * others as they are. An entry outside [0, num_pages) among those held, or a
+ * others as they are; a row whose count in `held` lies outside [0, max_pages] fits
+ * none. An entry outside [0, num_pages) among those held, or a
  * count that would fall below 0, sets MOE_DEV_BAD_PAGE and is passed over
  * (moe_kv_reserve may leave -1 in the place of such an entry). */
 #define MOE_KV_MAX_CACHES 256

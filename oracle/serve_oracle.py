@@ -28,6 +28,10 @@ class Pool:
     def _page_ok(self, p):
         return 0 <= p < len(self.refs)
 
+    def _count_ok(self, r):
+        """Whether a row holds as many entries as it may have."""
+        return 0 <= self.held[r] <= self.table.shape[1]
+
     def _drop(self, p):
         if self.refs[p] > 0:
             self.refs[p] -= 1
@@ -39,7 +43,7 @@ class Pool:
         for i, (p, c, t) in enumerate(zip(parents, children, tokens)):
             ok = self._row_ok(p) and self._row_ok(c) and 0 <= t <= self.table.shape[1] * self.ps
             ok = ok and c not in children[:i] and p not in children
-            ok = ok and held[c] == 0 and self._entries(t) <= held[p]
+            ok = ok and held[c] == 0 and self._entries(t) <= held[p] <= self.table.shape[1]
             if not ok:
                 flags |= BAD_ROW
                 continue
@@ -56,7 +60,7 @@ class Pool:
     def release(self, rows, keep):
         flags = 0
         for r, k in zip(rows, keep):
-            if not self._row_ok(r) or k < 0:
+            if not self._row_ok(r) or k < 0 or not self._count_ok(r):
                 flags |= BAD_ROW
                 continue
             left = min(self._entries(k), self.table.shape[1])
@@ -73,7 +77,8 @@ class Pool:
         at, full = 0, False
         copies, dropped = [], []
         for i, (r, a, b) in enumerate(zip(rows, start, end)):
-            if not self._row_ok(r) or r in rows[:i] or not 0 <= a <= b <= self.table.shape[1] * self.ps:
+            if (not self._row_ok(r) or r in rows[:i] or not 0 <= a <= b <= self.table.shape[1] * self.ps
+                    or not self._count_ok(r)):
                 flags |= BAD_ROW
                 continue
             lo, hi = (a // self.ps if a < b else self._entries(b)), self._entries(b)
@@ -123,7 +128,9 @@ class Pool:
         was = np.zeros(len(self.refs), bool)
         was[used] = True
         for r, h in enumerate(self.held):
-            for e in range(h):
+            if not self._count_ok(r):
+                flags |= BAD_ROW
+            for e in range(min(h, self.table.shape[1])):
                 p = self.table[r, e]
                 if not self._page_ok(p) or (p >= n and not was[p]):
                     flags |= BAD_PAGE
