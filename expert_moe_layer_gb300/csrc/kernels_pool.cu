@@ -437,14 +437,14 @@ __global__ void __launch_bounds__(kScanThreads)
 
 // The k-th page in use from `used` on goes to the k-th free page (all of which
 // lie below `used`): no page is both read and written. CTAs below `appliers`
-// follow the moves in the counts and the table, the others copy pages.
+// follow the moves in the counts and the table, the others copy pages. (The rows
+// are looked at where nothing moves too: their bad entries are reported.)
 __global__ void __launch_bounds__(kApplyThreads)
     compact_apply_kernel(PoolArgs a, Work w, const __grid_constant__ CacheList caches, int appliers) {
   pdl_enter();
   const Work f = {fresh(w.head), w.claims, w.items, w.copies, fresh(w.prefix),
                   fresh(w.list), fresh(w.ranks), w.chunk, w.chunks};
   const long used = f.head->used, moves = f.head->moves, stay = used - moves;
-  if (moves == 0) return;
   if (blockIdx.x >= appliers) {
     const long warps = static_cast<long>(gridDim.x - appliers) * (kApplyThreads / 32);
     const long warp = static_cast<long>(blockIdx.x - appliers) * (kApplyThreads / 32) + (threadIdx.x >> 5);

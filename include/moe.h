@@ -762,7 +762,10 @@ MOE_API int moe_kv_release(const moe_attn_config* cfg, const moe_kv_pool* pool, 
 /* moe_kv_compact: afterwards the pages in use are the first ones. With U pages in
  * use, the k-th of those from page U on moves to the k-th free page before it, in
  * every cache, in the counts and in every row that holds it. (U: pages with a
- * count other than 0.) The pages that were left keep their old bytes.
+ * count other than 0.) The pages that were left keep their old bytes. A row whose
+ * count in `held` lies outside [0, max_pages] sets MOE_DEV_BAD_ROW (its entries are
+ * followed as far as the table goes), an entry that names a free page from U on
+ * MOE_DEV_BAD_PAGE.
  *   used  [1] int32 out, nullable: U
  * ws: moe_kv_pool_workspace_size(cfg, pool, 0) bytes. */
 MOE_API int moe_kv_compact(const moe_attn_config* cfg, const moe_kv_pool* pool, int32_t* used,

@@ -36,3 +36,30 @@ def test_a_row_with_a_count_outside_the_table_is_not_forked_or_reserved(held):
     p.check()
     p.reserve([1, 2, 1], [16, 40, 0], [40, 50, 0])
     p.check()
+
+
+@pytest.mark.parametrize("held", COUNTS)
+def test_a_row_with_a_count_outside_the_table_is_flagged_by_compaction(held):
+    """Its entries within the table follow the moves all the same."""
+    p = _rows_in_use(held)
+    p.release([0])
+    p.check()
+    p.compact()
+    p.check()
+    p.compact()
+    p.check()
+
+
+@pytest.mark.parametrize("pages", [40, 9000])
+@pytest.mark.parametrize("bad", [99999, -1, 2 ** 31 - 1, -2 ** 31, 20])
+def test_compaction_looks_at_the_rows_where_nothing_moves(pages, bad):
+    p = Pool(rows=3, width=4, pages=pages, caches=1)
+    p.reserve(None, [0] * 3, [50, 0, 20])
+    p.o.table[2, 1] = bad                    # outside the pool, or (20) a free page
+    p.load()
+    p.compact()
+    p.check()
+    p.o.refs[:] = 1                          # no free page, nothing above the ones in use
+    p.load()
+    p.compact()
+    p.check()
