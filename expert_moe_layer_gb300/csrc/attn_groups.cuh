@@ -117,9 +117,10 @@ __device__ __forceinline__ long plan_groups(const AttnArgs& a, const Groups& gr,
       SeqInfo s = l.groups[g];
       s.q_len -= s.q0;
       int p = bad ? 0 : *const_cast<volatile int*>(l.limit + g) / kPrefixCut * kPrefixCut;
+      // whatever is left of its prefix (offsets that were refused set this flag anyway)
+      if (s.q_len > gr.max_len) flags |= MOE_DEV_BAD_SEGMENT;
       if (p > 0) {
         s.first_key = *const_cast<volatile int*>(l.first + g);
-        if (s.q_len > gr.max_len) flags |= MOE_DEV_BAD_SEGMENT;
         // (a group of one token, or of one request, has nothing to share)
         if (l.offsets[g + 1] - l.offsets[g] < 2 || s.q_len < 2 || s.q_len > gr.max_len) p = 0;
       }
