@@ -37,6 +37,11 @@ class PoolCache:
                               device="cuda")
         self.used = torch.zeros(1, dtype=torch.int32, device="cuda")
 
+    def room(self, tokens):
+        """Refuses requests that outgrow their row of the page table or the rotary table."""
+        if tokens > self.tokens:
+            raise ValueError(f"a request of {tokens} tokens; the cache holds {self.tokens}")
+
     def reserve(self, rows, start, end):
         B.moe_kv_reserve(self.cfg, self.pool, start.shape[0], rows, start, end, self.ws)
 
@@ -70,8 +75,7 @@ class Samples:
     """n rows that go on from one prompt of `tokens` tokens, a token per step."""
 
     def __init__(self, model, cache, first, n, tokens):
-        if tokens + 1 > cache.tokens:
-            raise ValueError(f"a request of {tokens + 1} tokens; the cache holds {cache.tokens}")
+        cache.room(tokens + 1)
         self.model, self.cache, self.n, self.host_len = model, cache, n, tokens
         hidden = model.layers[0]["o"].shape[0]
         self.rows = torch.arange(first, first + n, dtype=torch.int32, device="cuda")
@@ -104,8 +108,7 @@ class Samples:
 
     def step(self, x):
         """The samples' next tokens x [n, hidden] -> the same after the layers."""
-        if self.host_len + 1 > self.cache.tokens:
-            raise ValueError(f"a request of {self.host_len + 1} tokens; the cache holds {self.cache.tokens}")
+        self.cache.room(self.host_len + 1)
         self.host_len += 1
         if self.graph is None:
             side = torch.cuda.Stream()
@@ -126,6 +129,9 @@ class Samples:
 def sample(model, cache, prompt, n):
     """Runs a prompt [tokens, hidden] in row 0 and forks it into rows 0 .. n - 1."""
     t = prompt.shape[0]
+    cache.room(t + 1)
+    if not 1 <= n <= cache.rows:
+        raise ValueError(f"{n} samples; the cache holds 1 to {cache.rows}")
     cache.reserve(_ints([0]), _ints([0]), _ints([t]))
     at = torch.arange(t, device="cuda")
     ws = model.workspaces(1, t, t)
