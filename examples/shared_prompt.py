@@ -63,6 +63,8 @@ class PoolCache:
     def check(self):
         """Raises what the last pool call found wrong (synchronises)."""
         code, flags = B.moe_get_status(self.ws)
+        if flags & B.DEV_NO_PAGE:
+            raise RuntimeError("no free page")
         if code:
             raise RuntimeError(f"pool call: status {code}, flags {flags:#x}")
 
@@ -107,7 +109,8 @@ class Samples:
         return out
 
     def step(self, x):
-        """The samples' next tokens x [n, hidden] -> the same after the layers."""
+        """The samples' next tokens x [n, hidden] -> the same after the layers. Raises
+        where a sample finds no free page; the step can be taken again then."""
         self.cache.room(self.host_len + 1)
         self.host_len += 1
         if self.graph is None:
@@ -123,6 +126,12 @@ class Samples:
             torch.cuda.current_stream().wait_stream(side)
         self.x.copy_(x)
         self.graph.replay()
+        try:
+            self.cache.check()      # (a token without a page is stored nowhere)
+        except RuntimeError:
+            self.host_len -= 1
+            self.lens.sub_(1)
+            raise
         return self.out
 
 
@@ -133,6 +142,7 @@ def sample(model, cache, prompt, n):
     if not 1 <= n <= cache.rows:
         raise ValueError(f"{n} samples; the cache holds 1 to {cache.rows}")
     cache.reserve(_ints([0]), _ints([0]), _ints([t]))
+    cache.check()
     at = torch.arange(t, device="cuda")
     ws = model.workspaces(1, t, t)
     row = type("Row", (), dict(layers=cache.layers, page_table=cache.page_table[:1]))
@@ -153,7 +163,6 @@ def main():
     last = out[-1:] + 0.1 * torch.randn(n, 1024, device="cuda").bfloat16()
     for i in range(20):
         last = samples.step(_norm(last)).clone()
-    cache.check()
     held = int((cache.refs > 0).sum())
     print(f"{n} samples of {samples.host_len} tokens: {held} pages of {int(cache.held.sum())} held")
     cache.release(_ints(range(1, n, 2)))
