@@ -106,7 +106,9 @@ struct PrefixShape {
   int half_rows = 0, half_unit = 1;
 };
 // Up to so many groups every CTA of the prefix kernel sums up the list itself, in
-// shared memory, while the plan kernel still works on the own kernel's.
+// shared memory, while the plan kernel still works on the own kernel's. (It goes
+// through all requests for that; 64 groups, and 65 with the plan's list: 128 requests
+// 20 and 28 us, 1024 53 and 64, 4096 110 and 140, 65536 1367 and 1368.)
 constexpr int kSmallGroups = 64;
 
 struct PrefixHead {

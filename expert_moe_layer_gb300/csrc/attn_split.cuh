@@ -284,8 +284,9 @@ __host__ __device__ constexpr int ctas_per_sm() {
   if (D == 256) return 2;
   // as many as fit without spills: 16 rows of 128 channels take 68 us with two and
   // 74 with three, fp32 rows of 64 channels 49 with two and 45 with three. With 256
-  // channels 16 bf16 rows spill 172 bytes and 8 fp32 rows 136 at the 255 registers
-  // that a thread has at most, with any number of CTAs.
+  // channels 16 bf16 rows spill up to 176 bytes and 8 fp32 rows 116 at the 255 registers
+  // that a thread has at most, with any number of CTAs; over own keys, with the place of
+  // the prefix's sums, 336 and 164.
   return kRows == 16 || (kTerms == 2 && D == 128) ? 2 : kTerms == 2 ? 3 : kMaxCtasPerSm;
 }
 

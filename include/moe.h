@@ -661,13 +661,18 @@ MOE_API int moe_kv_attention(const moe_attn_config* cfg, int num_seqs, int T, in
  *     request that has queries (the others hold the same pages, or copies). What
  *     reaches past the tokens that every request with queries has before them is
  *     not taken as shared.
- *   max_group_len: at least the most query tokens of a group
+ *   max_group_len: at least the most query tokens of a group. It chooses the
+ *     kernel over the prefixes, one for the whole call: from 64 rows (max_group_len
+ *     times the heads of a group, bf16) one that is made for many rows. Groups of a
+ *     few rows are right there but slow, so that two requests can take longer than
+ *     unshared: a bound near the true sizes, or a call for the small groups, helps.
  * The other arguments and flags are those of moe_kv_attention. MOE_DEV_BAD_SEGMENT
  * is also set, and nothing shared, for group_offsets that decrease or leave
  * [0, num_seqs], a prefix below 0, or a group of more than max_group_len query
- * tokens (of that group): results are right all the same. With a window, from 128
- * rows per request (max_q_len times the heads of a group, bf16), and for requests
- * whose pages together (num_seqs rows of max_pages) are too few to gain by it, the
+ * tokens (of that group): results are right all the same. With a window (also one
+ * that is wider than any request: leave it 0 then), from 128 rows per request
+ * (max_q_len times the heads of a group, bf16), and for requests whose pages together
+ * (num_seqs rows of max_pages, whatever the lengths) are too few to gain by it, the
  * call is moe_kv_attention and does not look at the groups. num_groups may be up to
  * 2^18.
  * ws: moe_kv_attention_shared_workspace_size(...) bytes (0: invalid); it has room
@@ -698,8 +703,8 @@ MOE_API int moe_kv_attention_shared(const moe_attn_config* cfg, int num_seqs, in
  *
  * Every call is one atomic step: it decides by the pool as it finds it, and what
  * comes out does not depend on the order in which the GPU runs it. n items are
- * given in device arrays of int32 [n]; n may be up to 2^18. An item that does
- * not fit (see each call) changes nothing, sets MOE_DEV_BAD_ROW, and leaves the
+ * given in device arrays of int32 [n]; n may be up to 2^18 (0: a no-op). An item
+ * that does not fit (see each call) changes nothing, sets MOE_DEV_BAD_ROW, and leaves the
  * others as they are; a row whose count in `held` lies outside [0, max_pages] fits
  * none. An entry outside [0, num_pages) among those held, or a
  * count that would fall below 0, sets MOE_DEV_BAD_PAGE and is passed over
@@ -731,6 +736,8 @@ MOE_API size_t moe_kv_pool_workspace_size(const moe_attn_config* cfg, const moe_
  * the tokens end in is shared too: moe_kv_reserve gives each row its own before
  * it is written to. A child holds nothing (released, or fresh) and is named once;
  * a row is not parent and child in one call; the parent holds that many tokens.
+ * Each item looks through all children: up to some thousand items that is hidden
+ * behind the launch (4096 take 11 us), then the time grows with n^2 (65536 1.3 ms).
  * ws: NULL, or >= 4 bytes for the status word. */
 MOE_API int moe_kv_fork(const moe_attn_config* cfg, const moe_kv_pool* pool, int n,
                         const int32_t* parents, const int32_t* children, const int32_t* tokens,
@@ -811,7 +818,8 @@ typedef struct {
  *   y      [T, H], nullable: no block before; then post_w, post_b, gate and
  *          x_out are NULL and r = x
  *   x      [T, H] residual_dtype. y and x take a row stride in elements.
- *   post_w, post_b, pre_w, pre_b  [H] fp32, nullable (1 and 0)
+ *   post_w, post_b, pre_w, pre_b  [H] fp32, nullable (a factor of 1, whatever
+ *          weight_offset, and 0)
  *   gate   nullable; value of (t, c) at gate[t * gate_token_stride +
  *          c * gate_channel_stride], channel stride 0 or 1: one per channel
  *          (0, 1), per token (1, 0) or per element (H, 1)
