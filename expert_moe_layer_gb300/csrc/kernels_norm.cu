@@ -367,6 +367,9 @@ __host__ __device__ constexpr int chunk_of() {
 // instead of 74.5, of 2880 34.0 instead of 37.5, with an fp32 residual 81 instead of 85;
 // of 4096 45.8 and 45.0). fp32 rows of 5120 lose, 57.0 instead of 55.5, and rows normed on both
 // sides, whose weights then spill (of 2048 29.9 instead of 23.2, of 5120 70.4 and 68.9).
+// Wider rows need more threads, which have 72 registers with 448 (96 with 320, and 32 to
+// 56 bytes spilled): 208 to 372 bytes spill, rows of 6144 100 instead of 74, of 7168 110
+// instead of 80.
 constexpr int kTwoThreads = 320;
 template <typename TA, typename TR, int kChunks, bool kWarpRow, bool kPost, bool kTwo = false>
 __global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : kTwo ? kTwoThreads : kMostKeep,
